@@ -14,7 +14,8 @@ _BINDING_NAMES = (
     "attn_bwd_dq_convert", "attn_bwd_main_dkdv", "attn_bwd_dq", "attn_bwd_workspace_size", "alloc_workspace",
     "attn_last_device_error", "attn_device_error_word", "attn_watchdog_selftest",
     "status_string", "AttnError", "load_library", "ssd_fwd", "ssd_bwd", "ssd_workspace", "ATTN_DQ_AUTO", "ATTN_DQ_REDUCE",
-    "ATTN_DQ_SEPARATE",
+    "ATTN_DQ_SEPARATE", "rope_fwd", "rope_bwd", "alloc_kv_cache", "kv_cache_write", "kv_cache_read",
+    "alloc_decode_workspace", "attn_decode",
 )
 
 

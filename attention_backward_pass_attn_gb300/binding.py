@@ -78,6 +78,12 @@ def load_library(path: str | None = None):
             "ssd_workspace_size": (sz, [i, i, i, i, i, i]),
             "ssd_fwd": (i, [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, vp, sz, vp]),
             "ssd_bwd": (i, [vp] * 13 + [i, i, i, i, i, i, vp, sz, vp]),
+            "rope_fwd": (i, [vp] * 5 + [i, i] + [vp] * 3 + [i] * 6 + [vp]),
+            "rope_bwd": (i, [vp] * 5 + [i, i] + [vp] * 3 + [i] * 6 + [vp]),
+            "kv_cache_write": (i, [vp] * 10 + [i] * 7 + [vp]),
+            "kv_cache_read": (i, [vp] * 9 + [i] * 7 + [vp]),
+            "attn_decode_workspace_size": (sz, [i]),
+            "attn_decode": (i, [vp] * 9 + [i] * 8 + [f, vp, sz, vp]),
             "attn_last_device_error": (i, [vp]),
             "attn_device_error_word": (i, [vp, ctypes.POINTER(ctypes.c_int)]),
             "attn_watchdog_selftest": (i, [ctypes.c_uint64, vp]),
@@ -402,3 +408,271 @@ def ssd_bwd(x, dt, A, B, C, D, dy, workspace=None, out=None, stream=None):
                                 ws.numel() * ws.element_size(), _stream(stream))
     _check("ssd_bwd", st)
     return out
+
+
+# ------------------------------------------------------------------ the answering path
+# Rotary positions, the paged key/value cache, attention of one new token.
+# Tensors must live on the current CUDA device, whose current stream the calls
+# run on unless ``stream`` names another.
+_E4M3_DTYPES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _check_device(t: torch.Tensor, name: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError("%s must be on the current CUDA device" % name)
+
+
+def _check_like(t: torch.Tensor, name: str, shape, dtype, dev: int):
+    """A contiguous tensor of this shape and type on CUDA device ``dev``."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.get_device() != dev:
+        raise ValueError("%s must be on CUDA device %d, like the first tensor" % (name, dev))
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _check_rows(t: torch.Tensor, name: str, dev: int):
+    """A bf16 [B, H, N, d] tensor whose head dimension is contiguous, with any
+    16-byte strides; returns its three element strides."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.get_device() != dev:
+        raise ValueError("%s must be on CUDA device %d, like the first tensor" % (name, dev))
+    if t.dtype != torch.bfloat16:
+        raise ValueError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
+    sb, sh, sn, sd = t.stride()
+    if sd != 1 and t.shape[3] > 1:
+        raise ValueError("%s must be contiguous in its head dimension" % name)
+    for n, s in zip(t.shape, (sb, sh, sn)):
+        if n > 1 and s % 8:
+            raise ValueError("%s must have strides that are multiples of 8" % name)
+    return sb, sh, sn
+
+
+def _check_cache(k_cache, v_cache, k_descale, v_descale, page_table, dev):
+    """(pages, Hkv, page_size, d, B, max_pages) of a cache and its page table."""
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [pages, Hkv, page_size, d], got %s"
+                         % (tuple(k_cache.shape),))
+    if (k_descale is None) != (v_descale is None):
+        raise ValueError("k_descale and v_descale come together")
+    if k_descale is None:
+        if k_cache.dtype != torch.bfloat16:
+            raise ValueError("k_cache must be torch.bfloat16 without descale factors, got %s"
+                             % k_cache.dtype)
+    elif k_cache.dtype not in _E4M3_DTYPES:
+        raise ValueError("k_cache must hold e4m3 bytes (float8_e4m3fn or uint8) with descale "
+                         "factors, got %s" % k_cache.dtype)
+    shape = k_cache.shape
+    if not k_cache.is_contiguous():
+        raise ValueError("k_cache must be contiguous")
+    _check_like(v_cache, "v_cache", shape, k_cache.dtype, dev)
+    if k_descale is not None:
+        _check_like(k_descale, "k_descale", shape[:3], torch.float32, dev)
+        _check_like(v_descale, "v_descale", shape[:3], torch.float32, dev)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages], got %s" % (tuple(page_table.shape),))
+    _check_like(page_table, "page_table", page_table.shape, torch.int32, dev)
+    return (*shape, *page_table.shape)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rope(fn, q, k, pos, inv_freq, sections, interleaved, out, stream):
+    _check_device(q, "q")
+    B, H, N, d = _shape4(q, "q")
+    dev = q.get_device()
+    strides = list(_check_rows(q, "q", dev))
+    Hk = 0
+    if k is not None:
+        if _shape4(k, "k")[0] != B or k.shape[2] != N or k.shape[3] != d:
+            raise ValueError("k must be [B, Hk, N, d] with q's B, N and d, got %s"
+                             % (tuple(k.shape),))
+        Hk = k.shape[1]
+        strides += _check_rows(k, "k", dev)
+    else:
+        strides += (0, 0, 0)
+    if pos.dim() != 3 or pos.shape[1] not in (1, B) or pos.shape[2] != N:
+        raise ValueError("pos must be [axes, B or 1, N], got %s" % (tuple(pos.shape),))
+    axes = pos.shape[0]
+    _check_like(pos, "pos", pos.shape, torch.int32, dev)
+    _check_like(inv_freq, "inv_freq", (d // 2,), torch.float32, dev)
+    sections = (d // 2,) if sections is None else tuple(int(s) for s in sections)
+    if len(sections) != axes or sum(sections) != d // 2 or min(sections) < 0:
+        raise ValueError("sections must be %d counts that sum to d/2 = %d, got %s"
+                         % (axes, d // 2, sections))
+    oq, ok = (None, None) if out is None else out
+    if oq is None:
+        oq = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=q.device)
+    else:
+        _check_like(oq, "out[0]", (B, H, N, d), torch.bfloat16, dev)
+    if k is None:
+        ok = None
+    elif ok is None:
+        ok = torch.empty((B, Hk, N, d), dtype=torch.bfloat16, device=q.device)
+    else:
+        _check_like(ok, "out[1]", (B, Hk, N, d), torch.bfloat16, dev)
+    st = getattr(load_library(), fn)(q.data_ptr(), _ptr(k), pos.data_ptr(), inv_freq.data_ptr(),
+                                     (ctypes.c_int * axes)(*sections), axes,
+                                     int(bool(interleaved)), (ctypes.c_int64 * 6)(*strides),
+                                     oq.data_ptr(), _ptr(ok), B, H, Hk, N, d, pos.shape[1],
+                                     _stream(stream))
+    _check(fn, st)
+    return oq, ok
+
+
+def rope_fwd(q, k, pos, inv_freq, sections=None, interleaved=False, out=None, stream=None):
+    """q and k turned by their positions: (q', k'), bf16, contiguous.
+
+    q [B, H, N, d] and k [B, Hk, N, d] (or None): bf16 CUDA tensors, d = 64 or
+    128, contiguous in d; other strides are free as long as they are multiples
+    of 8 (so q may be ``qkv[:, :, :H].transpose(1, 2)`` of a fused projection).
+    pos: int32 [axes, B or 1, N].  inv_freq: fp32 [d/2], radians per position.
+    sections: how many pairs turn by each axis (sum d/2; default: one axis).
+    interleaved: pairs are (2i, 2i+1) instead of (i, i + d/2).
+    out: (q', k') to write into, contiguous; may be the inputs themselves when
+    those are contiguous.
+    """
+    return _rope("rope_fwd", q, k, pos, inv_freq, sections, interleaved, out, stream)
+
+
+def rope_bwd(dq, dk, pos, inv_freq, sections=None, interleaved=False, out=None, stream=None):
+    """The gradients of rope_fwd's q and k from those of its results (the turn
+    by the negative angles); arguments as for rope_fwd."""
+    return _rope("rope_bwd", dq, dk, pos, inv_freq, sections, interleaved, out, stream)
+
+
+def alloc_kv_cache(num_pages: int, Hkv: int, page_size: int, d: int, device,
+                   dtype=torch.bfloat16):
+    """(k_cache, v_cache, k_descale, v_descale), zeroed: a bf16 cache (factors
+    None), or an e4m3 one (dtype torch.float8_e4m3fn) with its fp32 factors."""
+    if dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise ValueError("dtype must be torch.bfloat16 or torch.float8_e4m3fn, got %s" % dtype)
+    shape = (num_pages, Hkv, page_size, d)
+    fp8 = dtype == torch.float8_e4m3fn
+    caches = [torch.zeros(shape, dtype=torch.uint8 if fp8 else dtype, device=device)
+              for _ in range(2)]
+    if not fp8:
+        return caches[0], caches[1], None, None
+    factors = [torch.ones(shape[:3], dtype=torch.float32, device=device) for _ in range(2)]
+    return caches[0].view(dtype), caches[1].view(dtype), factors[0], factors[1]
+
+
+def _check_span(start, count, B, dev):
+    _check_like(start, "start", (B,), torch.int32, dev)
+    if count is not None:
+        _check_like(count, "count", (B,), torch.int32, dev)
+
+
+def kv_cache_write(k, v, k_cache, v_cache, page_table, start, count=None, k_descale=None,
+                   v_descale=None, stream=None):
+    """Append k, v to a paged cache, in place.
+
+    k, v: bf16 [B, Hkv, T, d], strides as free as rope_fwd's.  Token t <
+    count[b] (default: all T) becomes position start[b] + t of sequence b.
+    k_cache, v_cache: [pages, Hkv, page_size, d], bf16, or e4m3 with fp32
+    factors k_descale, v_descale [pages, Hkv, page_size], which the call
+    chooses for every row it writes.  page_table: int32 [B, max_pages];
+    start, count: int32 [B].
+    """
+    _check_device(k_cache, "k_cache")
+    dev = k_cache.get_device()
+    P, Hkv, ps, d, B, mp = _check_cache(k_cache, v_cache, k_descale, v_descale, page_table, dev)
+    T = _shape4(k, "k")[2]
+    for t, n in ((k, "k"), (v, "v")):
+        if t.shape != (B, Hkv, T, d):
+            raise ValueError("%s must have shape %s, got %s" % (n, (B, Hkv, T, d),
+                                                                tuple(t.shape)))
+    strides = _check_rows(k, "k", dev) + _check_rows(v, "v", dev)
+    _check_span(start, count, B, dev)
+    st = load_library().kv_cache_write(k.data_ptr(), v.data_ptr(), (ctypes.c_int64 * 6)(*strides),
+                                       k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_descale),
+                                       _ptr(v_descale), page_table.data_ptr(), start.data_ptr(),
+                                       _ptr(count), B, Hkv, T, d, ps, P, mp, _stream(stream))
+    _check("kv_cache_write", st)
+
+
+def kv_cache_read(k_cache, v_cache, page_table, start, T: int, count=None, k_descale=None,
+                  v_descale=None, out=None, stream=None):
+    """(k, v), bf16 [B, Hkv, T, d]: positions start[b] .. start[b] + count[b] - 1
+    (default count: T) of each sequence, times their factors; zeros after them.
+    Arguments as for kv_cache_write; out: (k, v) to write into."""
+    _check_device(k_cache, "k_cache")
+    dev = k_cache.get_device()
+    P, Hkv, ps, d, B, mp = _check_cache(k_cache, v_cache, k_descale, v_descale, page_table, dev)
+    _check_span(start, count, B, dev)
+    shape = (B, Hkv, int(T), d)
+    if out is None:
+        k, v = (torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device) for _ in range(2))
+    else:
+        k, v = out
+        _check_like(k, "out[0]", shape, torch.bfloat16, dev)
+        _check_like(v, "out[1]", shape, torch.bfloat16, dev)
+    st = load_library().kv_cache_read(k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_descale),
+                                      _ptr(v_descale), page_table.data_ptr(), start.data_ptr(),
+                                      _ptr(count), k.data_ptr(), v.data_ptr(), B, Hkv, int(T), d,
+                                      ps, P, mp, _stream(stream))
+    _check("kv_cache_read", st)
+    return k, v
+
+
+def alloc_decode_workspace(d: int, device) -> torch.Tensor:
+    """The uint8 device buffer attn_decode needs for head dim d, whatever the
+    batch; calls that may overlap on the GPU need one each."""
+    n = int(load_library().attn_decode_workspace_size(d))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, k_descale=None,
+                v_descale=None, window=0, out=None, lse=None, workspace=None, stream=None):
+    """O and the log-sum-exp L of one new token per sequence over a paged cache.
+
+    q: bf16 [B, Hq, 1, d], contiguous, Hq a multiple of the cache's Hkv;
+    cache arguments as for kv_cache_write; seq_lens: int32 [B], the sequences'
+    lengths with the new token (whose k and v are in the cache already).
+    window > 0: only the last ``window`` positions are seen.
+    Returns (O bf16 [B, Hq, 1, d], L fp32 [B, Hq, 1]); a sequence of length 0
+    has O = 0 and L = -inf.
+    """
+    _check_device(q, "q")
+    dev = q.get_device()
+    P, Hkv, ps, d, B, mp = _check_cache(k_cache, v_cache, k_descale, v_descale, page_table, dev)
+    if k_cache.get_device() != dev:
+        raise ValueError("k_cache must be on CUDA device %d, like the first tensor" % dev)
+    Hq = _shape4(q, "q")[1]
+    _check_like(q, "q", (B, Hq, 1, d), torch.bfloat16, dev)
+    if Hkv < 1 or Hq % Hkv:
+        raise ValueError("q's %d heads must be a multiple of the cache's %d" % (Hq, Hkv))
+    _check_like(seq_lens, "seq_lens", (B,), torch.int32, dev)
+    if out is None:
+        out = torch.empty((B, Hq, 1, d), dtype=torch.bfloat16, device=q.device)
+    else:
+        _check_like(out, "out", (B, Hq, 1, d), torch.bfloat16, dev)
+    if lse is None:
+        lse = torch.empty((B, Hq, 1), dtype=torch.float32, device=q.device)
+    else:
+        _check_like(lse, "lse", (B, Hq, 1), torch.float32, dev)
+    if workspace is None:
+        workspace = alloc_decode_workspace(d, q.device)
+    elif workspace.get_device() != dev:
+        raise ValueError("workspace must be on CUDA device %d, like the first tensor" % dev)
+    st = load_library().attn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                    _ptr(k_descale), _ptr(v_descale), page_table.data_ptr(),
+                                    seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq,
+                                    Hkv, d, ps, P, mp, int(window), _default_scale(d, scale),
+                                    workspace.data_ptr(),
+                                    workspace.numel() * workspace.element_size(),
+                                    _stream(stream))
+    _check("attn_decode", st)
+    return out, lse

@@ -12,6 +12,7 @@
 #include "../../include/attn.h"
 #include "kernels.h"
 #include "ptx.cuh"
+#include "serving.h"
 
 namespace attn {
 
@@ -20,8 +21,8 @@ namespace attn {
 __device__ int g_device_error = 0;
 
 namespace {
-
 constexpr int kMaxDevices = 64;
+}  // namespace
 
 int* error_word_ptr() {
   static std::mutex mu;
@@ -36,6 +37,8 @@ int* error_word_ptr() {
   }
   return ptrs[dev];
 }
+
+namespace {
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static std::once_flag once;
@@ -267,7 +270,7 @@ const char* attn_status_string(int status) {
   switch (status) {
     case ATTN_OK: return "ok";
     case ATTN_ERR_INVALID_ARG: return "invalid argument";
-    case ATTN_ERR_UNSUPPORTED: return "unsupported shape (d must be 64 or 128)";
+    case ATTN_ERR_UNSUPPORTED: return "unsupported shape (d must be 64 or 128, a page size a multiple of 16)";
     case ATTN_ERR_CUDA: return "CUDA error";
     case ATTN_ERR_TIMEOUT: return "device wait timed out";
     case ATTN_ERR_WORKSPACE: return "workspace missing, misaligned or too small";

@@ -53,7 +53,8 @@ extern "C" {
 typedef enum {
   ATTN_OK = 0,
   ATTN_ERR_INVALID_ARG = 1, /* null pointer, negative size, bad scale, misaligned pointer */
-  ATTN_ERR_UNSUPPORTED = 2, /* d not in {64, 128}, or a size beyond the 32-bit index range */
+  ATTN_ERR_UNSUPPORTED = 2, /* d not in {64, 128}, a page size that is no multiple of 16, or a
+                               size beyond the 32-bit index range */
   ATTN_ERR_CUDA = 3,        /* a CUDA runtime/driver call or a launch failed */
   ATTN_ERR_TIMEOUT = 4,     /* a kernel's bounded wait ran out (reported by attn_last_device_error) */
   ATTN_ERR_WORKSPACE = 5,   /* workspace NULL, misaligned or smaller than attn_bwd_workspace_size */
@@ -311,6 +312,131 @@ int ssd_bwd(const void* x, const float* dt, const float* A, const void* B, const
             const float* D, const void* dy, float* dx, float* ddt, float* dA, float* dB,
             float* dC, float* dD, int Bt, int T, int H, int G, int N, int P, void* workspace,
             size_t workspace_bytes, void* stream);
+
+/*
+ * The answering path: what a model trained with the entry points above needs
+ * to produce one token after another.  Rotary positions turn q and k, the
+ * paged cache keeps k and v (in bf16, or in e4m3 with a factor per row), and
+ * attn_decode attends from each sequence's newest token over its pages.  The
+ * pages have no counterpart: they train, and never answer.
+ *
+ * The paged cache, of which the caller owns every buffer:
+ *
+ *   K_cache, V_cache      [num_pages][Hkv][page_size][d], bf16, or OCP FP8
+ *                         E4M3 bytes when the descale arrays are given;
+ *                         16-byte aligned
+ *   k_descale, v_descale  fp32 [num_pages][Hkv][page_size]: the factor of
+ *                         each stored row, stored value x factor = value;
+ *                         both NULL for a bf16 cache
+ *   page_table            int32 [B][max_pages]: position p of sequence b is
+ *                         row p % page_size of page page_table[b][p / page_size]
+ *
+ * page_size is a multiple of 16 (ATTN_ERR_UNSUPPORTED otherwise), num_pages,
+ * max_pages and Hkv are at least 1 (ATTN_ERR_INVALID_ARG otherwise), d is 64
+ * or 128, and max_pages x page_size fits 31 bits.  Sequences may share pages
+ * that are only read.  Tables, lengths and positions live in device memory,
+ * so a captured graph replays on the values of that moment.
+ *
+ * An entry that a call needs and that names no page (below 0, or num_pages
+ * and more), and a length or position outside what the table holds, is never
+ * followed: the call skips those positions, as said below, and records it in
+ * the device error word (attn_last_device_error then answers
+ * ATTN_ERR_DEVICE).  Entries that no position needs may hold anything.
+ */
+
+/*
+ * Rotary positions.  Pair i of each head row, i < d/2, is (x[i], x[i + d/2]),
+ * or (x[2i], x[2i+1]) with interleaved = 1, and turns by the angle
+ * theta = pos[axis(i)] x inv_freq[i]:
+ *
+ *   y_a = x_a cos theta - x_b sin theta,   y_b = x_b cos theta + x_a sin theta
+ *
+ * rope_bwd is its gradient, the turn by -theta.  Both round once, to bf16.
+ *
+ *   Q, K        bf16 [B][H][N][d] and [B][Hk][N][d]; K (and K_out) may be NULL
+ *               when Hk = 0, Q when H = 0
+ *   strides     host array of 6 element strides: Q's batch, head and token
+ *               stride, then K's; the head dimension is contiguous.  Every
+ *               stride of a dimension longer than 1 is >= 0 and a multiple of
+ *               8.  NULL = contiguous.  So heads of a fused projection
+ *               [B][N][heads][d] are taken as they lie.
+ *   Q_out, K_out  contiguous [B][H][N][d]; may be the inputs themselves when
+ *               those are contiguous, and must not overlap them otherwise
+ *   pos         int32 [axes][pos_batches][N], any sign; pos_batches is B, or
+ *               1 = the same for every batch element
+ *   inv_freq    fp32 [d/2], finite: radians per position
+ *   sections    host array of `axes` (1 to 4) counts that sum to d/2: the
+ *               first sections[0] pairs turn by axis 0, and so on (text: one
+ *               axis; images: height and width; video: time too)
+ *
+ * The angle is taken modulo one turn in 64-bit integers, so it is as good at
+ * position 2^30 as at 1.
+ */
+int rope_fwd(const void* Q, const void* K, const int* pos, const float* inv_freq,
+             const int* sections, int axes, int interleaved, const int64_t* strides, void* Q_out,
+             void* K_out, int B, int H, int Hk, int N, int d, int pos_batches, void* stream);
+int rope_bwd(const void* dQ, const void* dK, const int* pos, const float* inv_freq,
+             const int* sections, int axes, int interleaved, const int64_t* strides, void* dQ_out,
+             void* dK_out, int B, int H, int Hk, int N, int d, int pos_batches, void* stream);
+
+/*
+ * Append to the cache.  K, V: bf16 [B][Hkv][T][d] with `strides` as in
+ * rope_fwd (K's three, then V's; NULL = contiguous).  Token t < count[b] of
+ * sequence b becomes position start[b] + t; tokens at count[b] and beyond are
+ * a padded batch's filling and are not looked at.  start: int32 [B]; count:
+ * int32 [B], or NULL = T for all.  Positions outside the table and bad pages
+ * are skipped and recorded.  Nothing else in the cache changes.
+ *
+ * With descale arrays each row (the d values of one token and head) is
+ * rounded to e4m3: descale = the smallest power of two, at least 2^-126, with
+ * the largest finite |x| <= 448 descale (1 for a row of zeros), value =
+ * e4m3(x / descale), ties to even; infinities become +-448, NaN stays NaN.
+ *
+ * Two tokens of one call that fall on the same row of the cache (sequences
+ * that share the page they append to) leave that row unspecified.
+ */
+int kv_cache_write(const void* K, const void* V, const int64_t* strides, void* K_cache,
+                   void* V_cache, float* k_descale, float* v_descale, const int* page_table,
+                   const int* start, const int* count, int B, int Hkv, int T, int d, int page_size,
+                   int num_pages, int max_pages, void* stream);
+
+/*
+ * Read back: K, V (bf16, contiguous [B][Hkv][T][d]) receive positions
+ * start[b] .. start[b] + count[b] - 1 of each sequence, multiplied by their
+ * factors and rounded once to bf16.  Rows at count[b] and beyond, and rows of
+ * skipped positions, are zero.
+ */
+int kv_cache_read(const void* K_cache, const void* V_cache, const float* k_descale,
+                  const float* v_descale, const int* page_table, const int* start,
+                  const int* count, void* K, void* V, int B, int Hkv, int T, int d, int page_size,
+                  int num_pages, int max_pages, void* stream);
+
+/*
+ * Attention of one new token per sequence over the cache: with n =
+ * seq_lens[b] (int32 [B], the new token included, its k and v already
+ * written), query head h reads key/value head h / (Hq / Hkv) at positions
+ * max(0, n - window) <= j < n (window = 0: all), as attn_fwd_ex's last row
+ * does, and
+ *
+ *   S_j = scale <q, k_j>,  L = logsumexp(S),  O = sum_j exp(S_j - L) v_j.
+ *
+ * Q, O: bf16 [B][Hq][d]; L: fp32 [B][Hq], natural log.  A sequence with
+ * nothing to see (n = 0, or only skipped positions) gets O = 0 and L = -inf.
+ * Values of the cache at positions that are not visible have no effect, NaN
+ * and infinities included.  Hq is a multiple of Hkv.
+ *
+ * The work is split evenly over the GPU, whatever the lengths, and the parts
+ * of a sequence are joined in a fixed order: results repeat bit for bit.  The
+ * workspace (attn_decode_workspace_size(d) bytes, the same for every batch,
+ * 256-byte aligned, contents on entry of no matter) is the call's until the
+ * stream has passed it.
+ */
+size_t attn_decode_workspace_size(int d);
+int attn_decode(const void* Q, const void* K_cache, const void* V_cache, const float* k_descale,
+                const float* v_descale, const int* page_table, const int* seq_lens, void* O,
+                float* L, int B, int Hq, int Hkv, int d, int page_size, int num_pages,
+                int max_pages, int window, float scale, void* workspace, size_t workspace_bytes,
+                void* stream);
 
 /*
  * Interface utility of this library's boundary (failure detection); the paper
