@@ -47,6 +47,8 @@ class AttnError(RuntimeError):
 def load_library(path: str | None = None):
     """Load ``libattn_gb300.so`` (built in-tree by ``__graft_entry__.build()``)."""
     global _lib
+    if path is None and _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -414,20 +416,40 @@ def ssd_bwd(x, dt, A, B, C, D, dy, workspace=None, out=None, stream=None):
 # Rotary positions, the paged key/value cache, attention of one new token.
 # Tensors must live on the current CUDA device, whose current stream the calls
 # run on unless ``stream`` names another.
+# The checks come first as one cheap test; only what fails it is looked at for
+# the reason, so that a call of a few microseconds on the GPU is not drowned by
+# its checks.
 _E4M3_DTYPES = (torch.float8_e4m3fn, torch.uint8)
+_I64x6 = ctypes.c_int64 * 6
+_SECTIONS = {n: ctypes.c_int * n for n in range(1, 5)}
 
 
-def _check_device(t: torch.Tensor, name: str):
+def _device_index(t: torch.Tensor, name: str) -> int:
+    """The index of the current CUDA device, which t must be on."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    if t.get_device() != torch.cuda.current_device():
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
         raise ValueError("%s must be on the current CUDA device" % name)
+    return dev
+
+
+def _stream_on(stream, dev: int) -> int:
+    """The CUDA stream handle of ``stream``, or of device dev's current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
+        raise ValueError("stream must be on CUDA device %d, like the first tensor" % dev)
+    return _stream(stream)
 
 
 def _check_like(t: torch.Tensor, name: str, shape, dtype, dev: int):
     """A contiguous tensor of this shape and type on CUDA device ``dev``."""
+    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape \
+            and t.get_device() == dev and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.get_device() != dev:
@@ -440,49 +462,52 @@ def _check_like(t: torch.Tensor, name: str, shape, dtype, dev: int):
         raise ValueError("%s must be contiguous" % name)
 
 
-def _check_rows(t: torch.Tensor, name: str, dev: int):
+def _check_rows(t: torch.Tensor, name: str, shape, dev: int):
     """A bf16 [B, H, N, d] tensor whose head dimension is contiguous, with any
     16-byte strides; returns its three element strides."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.get_device() != dev:
         raise ValueError("%s must be on CUDA device %d, like the first tensor" % (name, dev))
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise ValueError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     sb, sh, sn, sd = t.stride()
-    if sd != 1 and t.shape[3] > 1:
+    if sd != 1 and shape[3] > 1:
         raise ValueError("%s must be contiguous in its head dimension" % name)
-    for n, s in zip(t.shape, (sb, sh, sn)):
-        if n > 1 and s % 8:
-            raise ValueError("%s must have strides that are multiples of 8" % name)
+    if (sb | sh | sn) & 7:
+        for n, s in zip(shape, (sb, sh, sn)):
+            if n > 1 and s % 8:
+                raise ValueError("%s must have strides that are multiples of 8" % name)
     return sb, sh, sn
 
 
 def _check_cache(k_cache, v_cache, k_descale, v_descale, page_table, dev):
     """(pages, Hkv, page_size, d, B, max_pages) of a cache and its page table."""
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache must be [pages, Hkv, page_size, d], got %s"
-                         % (tuple(k_cache.shape),))
-    if (k_descale is None) != (v_descale is None):
-        raise ValueError("k_descale and v_descale come together")
-    if k_descale is None:
-        if k_cache.dtype != torch.bfloat16:
-            raise ValueError("k_cache must be torch.bfloat16 without descale factors, got %s"
-                             % k_cache.dtype)
-    elif k_cache.dtype not in _E4M3_DTYPES:
-        raise ValueError("k_cache must hold e4m3 bytes (float8_e4m3fn or uint8) with descale "
-                         "factors, got %s" % k_cache.dtype)
     shape = k_cache.shape
-    if not k_cache.is_contiguous():
-        raise ValueError("k_cache must be contiguous")
-    _check_like(v_cache, "v_cache", shape, k_cache.dtype, dev)
-    if k_descale is not None:
+    if len(shape) != 4:
+        raise ValueError("k_cache must be [pages, Hkv, page_size, d], got %s" % (tuple(shape),))
+    dtype = k_cache.dtype
+    if k_descale is None or v_descale is None:
+        if k_descale is not v_descale:
+            raise ValueError("k_descale and v_descale come together")
+        if dtype is not torch.bfloat16:
+            raise ValueError("k_cache must be torch.bfloat16 without descale factors, got %s"
+                             % dtype)
+    else:
+        if dtype not in _E4M3_DTYPES:
+            raise ValueError("k_cache must hold e4m3 bytes (float8_e4m3fn or uint8) with descale "
+                             "factors, got %s" % dtype)
         _check_like(k_descale, "k_descale", shape[:3], torch.float32, dev)
         _check_like(v_descale, "v_descale", shape[:3], torch.float32, dev)
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [B, max_pages], got %s" % (tuple(page_table.shape),))
-    _check_like(page_table, "page_table", page_table.shape, torch.int32, dev)
-    return (*shape, *page_table.shape)
+    _check_like(k_cache, "k_cache", shape, dtype, dev)
+    _check_like(v_cache, "v_cache", shape, dtype, dev)
+    table = page_table.shape
+    if len(table) != 2:
+        raise ValueError("page_table must be [B, max_pages], got %s" % (tuple(table),))
+    _check_like(page_table, "page_table", table, torch.int32, dev)
+    return (*shape, *table)
 
 
 def _ptr(t):
@@ -490,33 +515,32 @@ def _ptr(t):
 
 
 def _rope(fn, q, k, pos, inv_freq, sections, interleaved, out, stream):
-    _check_device(q, "q")
-    B, H, N, d = _shape4(q, "q")
-    dev = q.get_device()
-    strides = list(_check_rows(q, "q", dev))
-    Hk = 0
-    if k is not None:
-        if _shape4(k, "k")[0] != B or k.shape[2] != N or k.shape[3] != d:
-            raise ValueError("k must be [B, Hk, N, d] with q's B, N and d, got %s"
-                             % (tuple(k.shape),))
-        Hk = k.shape[1]
-        strides += _check_rows(k, "k", dev)
+    dev = _device_index(q, "q")
+    shape = _shape4(q, "q")
+    B, H, N, d = shape
+    strides = _check_rows(q, "q", shape, dev)
+    if k is None:
+        Hk, strides = 0, strides + (0, 0, 0)
     else:
-        strides += (0, 0, 0)
-    if pos.dim() != 3 or pos.shape[1] not in (1, B) or pos.shape[2] != N:
-        raise ValueError("pos must be [axes, B or 1, N], got %s" % (tuple(pos.shape),))
-    axes = pos.shape[0]
-    _check_like(pos, "pos", pos.shape, torch.int32, dev)
+        Hk = _shape4(k, "k")[1]
+        strides += _check_rows(k, "k", (B, Hk, N, d), dev)
+    pshape = pos.shape
+    if len(pshape) != 3 or (pshape[1] != B and pshape[1] != 1) or pshape[2] != N:
+        raise ValueError("pos must be [axes, B or 1, N], got %s" % (tuple(pshape),))
+    axes = pshape[0]
+    _check_like(pos, "pos", pshape, torch.int32, dev)
     _check_like(inv_freq, "inv_freq", (d // 2,), torch.float32, dev)
-    sections = (d // 2,) if sections is None else tuple(int(s) for s in sections)
-    if len(sections) != axes or sum(sections) != d // 2 or min(sections) < 0:
-        raise ValueError("sections must be %d counts that sum to d/2 = %d, got %s"
-                         % (axes, d // 2, sections))
+    if sections is None:
+        sections = (d // 2,)
+    if axes not in _SECTIONS or len(sections) != axes or sum(sections) != d // 2 \
+            or min(sections) < 0:
+        raise ValueError("sections must be one count for each of pos's 1 to 4 axes that sum to "
+                         "d/2 = %d, got %s for %d" % (d // 2, tuple(sections), axes))
     oq, ok = (None, None) if out is None else out
     if oq is None:
-        oq = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=q.device)
+        oq = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
     else:
-        _check_like(oq, "out[0]", (B, H, N, d), torch.bfloat16, dev)
+        _check_like(oq, "out[0]", shape, torch.bfloat16, dev)
     if k is None:
         ok = None
     elif ok is None:
@@ -524,11 +548,11 @@ def _rope(fn, q, k, pos, inv_freq, sections, interleaved, out, stream):
     else:
         _check_like(ok, "out[1]", (B, Hk, N, d), torch.bfloat16, dev)
     st = getattr(load_library(), fn)(q.data_ptr(), _ptr(k), pos.data_ptr(), inv_freq.data_ptr(),
-                                     (ctypes.c_int * axes)(*sections), axes,
-                                     int(bool(interleaved)), (ctypes.c_int64 * 6)(*strides),
-                                     oq.data_ptr(), _ptr(ok), B, H, Hk, N, d, pos.shape[1],
-                                     _stream(stream))
-    _check(fn, st)
+                                     _SECTIONS[axes](*sections), axes, int(bool(interleaved)),
+                                     _I64x6(*strides), oq.data_ptr(), _ptr(ok), B, H, Hk, N, d,
+                                     pshape[1], _stream_on(stream, dev))
+    if st:
+        _check(fn, st)
     return oq, ok
 
 
@@ -586,21 +610,19 @@ def kv_cache_write(k, v, k_cache, v_cache, page_table, start, count=None, k_desc
     chooses for every row it writes.  page_table: int32 [B, max_pages];
     start, count: int32 [B].
     """
-    _check_device(k_cache, "k_cache")
-    dev = k_cache.get_device()
+    dev = _device_index(k_cache, "k_cache")
     P, Hkv, ps, d, B, mp = _check_cache(k_cache, v_cache, k_descale, v_descale, page_table, dev)
     T = _shape4(k, "k")[2]
-    for t, n in ((k, "k"), (v, "v")):
-        if t.shape != (B, Hkv, T, d):
-            raise ValueError("%s must have shape %s, got %s" % (n, (B, Hkv, T, d),
-                                                                tuple(t.shape)))
-    strides = _check_rows(k, "k", dev) + _check_rows(v, "v", dev)
+    shape = (B, Hkv, T, d)
+    strides = _check_rows(k, "k", shape, dev) + _check_rows(v, "v", shape, dev)
     _check_span(start, count, B, dev)
-    st = load_library().kv_cache_write(k.data_ptr(), v.data_ptr(), (ctypes.c_int64 * 6)(*strides),
+    st = load_library().kv_cache_write(k.data_ptr(), v.data_ptr(), _I64x6(*strides),
                                        k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_descale),
                                        _ptr(v_descale), page_table.data_ptr(), start.data_ptr(),
-                                       _ptr(count), B, Hkv, T, d, ps, P, mp, _stream(stream))
-    _check("kv_cache_write", st)
+                                       _ptr(count), B, Hkv, T, d, ps, P, mp,
+                                       _stream_on(stream, dev))
+    if st:
+        _check("kv_cache_write", st)
 
 
 def kv_cache_read(k_cache, v_cache, page_table, start, T: int, count=None, k_descale=None,
@@ -608,13 +630,13 @@ def kv_cache_read(k_cache, v_cache, page_table, start, T: int, count=None, k_des
     """(k, v), bf16 [B, Hkv, T, d]: positions start[b] .. start[b] + count[b] - 1
     (default count: T) of each sequence, times their factors; zeros after them.
     Arguments as for kv_cache_write; out: (k, v) to write into."""
-    _check_device(k_cache, "k_cache")
-    dev = k_cache.get_device()
+    dev = _device_index(k_cache, "k_cache")
     P, Hkv, ps, d, B, mp = _check_cache(k_cache, v_cache, k_descale, v_descale, page_table, dev)
     _check_span(start, count, B, dev)
     shape = (B, Hkv, int(T), d)
     if out is None:
-        k, v = (torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device) for _ in range(2))
+        k = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
+        v = torch.empty_like(k)
     else:
         k, v = out
         _check_like(k, "out[0]", shape, torch.bfloat16, dev)
@@ -622,16 +644,22 @@ def kv_cache_read(k_cache, v_cache, page_table, start, T: int, count=None, k_des
     st = load_library().kv_cache_read(k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_descale),
                                       _ptr(v_descale), page_table.data_ptr(), start.data_ptr(),
                                       _ptr(count), k.data_ptr(), v.data_ptr(), B, Hkv, int(T), d,
-                                      ps, P, mp, _stream(stream))
-    _check("kv_cache_read", st)
+                                      ps, P, mp, _stream_on(stream, dev))
+    if st:
+        _check("kv_cache_read", st)
     return k, v
+
+
+_decode_bytes = {}  # of the workspace, by head dim
 
 
 def alloc_decode_workspace(d: int, device) -> torch.Tensor:
     """The uint8 device buffer attn_decode needs for head dim d, whatever the
     batch; calls that may overlap on the GPU need one each."""
-    n = int(load_library().attn_decode_workspace_size(d))
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+    n = _decode_bytes.get(d)
+    if n is None:
+        n = _decode_bytes[d] = max(int(load_library().attn_decode_workspace_size(d)), 256)
+    return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, k_descale=None,
@@ -645,20 +673,18 @@ def attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, k_descale
     Returns (O bf16 [B, Hq, 1, d], L fp32 [B, Hq, 1]); a sequence of length 0
     has O = 0 and L = -inf.
     """
-    _check_device(q, "q")
-    dev = q.get_device()
+    dev = _device_index(q, "q")
     P, Hkv, ps, d, B, mp = _check_cache(k_cache, v_cache, k_descale, v_descale, page_table, dev)
-    if k_cache.get_device() != dev:
-        raise ValueError("k_cache must be on CUDA device %d, like the first tensor" % dev)
     Hq = _shape4(q, "q")[1]
-    _check_like(q, "q", (B, Hq, 1, d), torch.bfloat16, dev)
+    shape = (B, Hq, 1, d)
+    _check_like(q, "q", shape, torch.bfloat16, dev)
     if Hkv < 1 or Hq % Hkv:
         raise ValueError("q's %d heads must be a multiple of the cache's %d" % (Hq, Hkv))
     _check_like(seq_lens, "seq_lens", (B,), torch.int32, dev)
     if out is None:
-        out = torch.empty((B, Hq, 1, d), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty_like(q)
     else:
-        _check_like(out, "out", (B, Hq, 1, d), torch.bfloat16, dev)
+        _check_like(out, "out", shape, torch.bfloat16, dev)
     if lse is None:
         lse = torch.empty((B, Hq, 1), dtype=torch.float32, device=q.device)
     else:
@@ -673,6 +699,7 @@ def attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, k_descale
                                     Hkv, d, ps, P, mp, int(window), _default_scale(d, scale),
                                     workspace.data_ptr(),
                                     workspace.numel() * workspace.element_size(),
-                                    _stream(stream))
-    _check("attn_decode", st)
+                                    _stream_on(stream, dev))
+    if st:
+        _check("attn_decode", st)
     return out, lse

@@ -12,8 +12,8 @@
 //   whatever the lengths of the sequences: every block reads the same number
 //   of bytes and all end together.  A share that begins or ends inside a
 //   sequence leaves a partial result (running maximum, sum, unnormalised
-//   output) in the workspace; a second kernel joins those of each sequence in
-//   the order of their keys, so results repeat bit for bit.
+//   output) in the workspace, and the last of a sequence's blocks to arrive
+//   joins them, in the order of their keys: results repeat bit for bit.
 // - The keys of a unit are split over the block's four warps, each with its
 //   own running maximum, sum and output, joined in shared memory once per
 //   sequence and share.  In the loop warps do not wait for one another.
@@ -28,15 +28,17 @@
 //   absent heads and cost a trip through shared memory.
 // - K of the next keys is loaded while the current scores are weighted, V of
 //   the next keys while the next scores are formed: 4 to 8 KB in flight per
-//   warp, 16 warps per SM.
+//   warp, 12 warps per SM.
 //
-// Rounding.  Scores, maxima, sums and outputs are fp32.  The weights p go to
-// the tensor core as a sum of two bf16 numbers, 16 bits in all (2^-16; a
-// second instruction that costs nothing here), so the result's only rounding
-// that counts is the last one to bf16.  For an e4m3 cache, K is widened to
-// fp16 (exact) and meets a q scaled by a power of two into fp16's range
-// (exact down to 2^-29 of its largest element); V is widened to bf16 (exact)
-// and its factors multiply p in fp32.
+// Rounding.  Scores, maxima, sums and outputs are fp32.  The weights p meet a
+// bf16 V as a sum of two bf16 numbers, 16 bits in all (2^-16; a second
+// instruction that costs nothing here), so the result's only rounding that
+// counts is the last one to bf16.  For an e4m3 cache both products run in
+// fp16, which holds every e4m3 value: q is scaled by a power of two into
+// fp16's range (exact down to 2^-29 of its largest element), and the weights,
+// V's factors included, are scaled so that 2^15 is the most they can be and
+// rounded to fp16's 11 bits (2^-12 of the weight, down to 2^-29 of the
+// largest; a sixteenth of the last rounding's step).
 #include <cuda_fp16.h>
 
 #include "f32x2.cuh"
@@ -96,17 +98,17 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   return y;
 }
 
-// Two e4m3 values (low 16 bits) as fp16, and as bf16; both exact.
+// Two e4m3 values (low 16 bits) as fp16, exactly.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(two)));
   return h;
 }
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two) {
-  const uint32_t h = e4m3x2_to_f16x2(two);
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  return pack_bf16x2(f.x, f.y);
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
 
 // Reduction over the lanes that hold different keys of the same head.
 __device__ __forceinline__ float keys_max(float x) {
@@ -130,12 +132,32 @@ __host__ __device__ inline HeadSplit split_heads(int group) {
   return {nb, (group + nb - 1) / nb};
 }
 
-// What the joining kernel needs to know of the split, in the workspace's
-// meta section: entry i = the unit block i starts with, {b, head block, unit
-// within it, units in it}; a block that starts with unit 0 has nothing to
-// join to.  Entry 0 also carries the number of units in all, W.
-struct Start {
-  int b, h, u, n;
+// The blocks that share a head block count their arrivals in a word of the
+// workspace: the call's tag (48 bits) and the count.  open_count, which every
+// one of them runs before its work, makes the word the call's own: what an
+// earlier call or another owner left there has another tag, and the first to
+// replace it wins.  arrive is true for the last of `parts`, which leaves the
+// count at zero for a replay of the same launch.  One addition per block: a
+// compare-and-swap loop here cost 30 us where 57 blocks end together.
+__device__ __forceinline__ void fence_acq_rel_gpu() {
+  asm volatile("fence.acq_rel.gpu;" ::: "memory");
+}
+__device__ __forceinline__ void open_count(unsigned long long* word, unsigned long long tag) {
+  const unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(word);
+  if ((old >> 16) != tag) atomicCAS(word, old, tag << 16);
+}
+__device__ __forceinline__ bool arrive(unsigned long long* word, unsigned long long tag,
+                                       int parts) {
+  const unsigned long long old = atomicAdd(word, 1ull);
+  const bool last = int(old & 0xFFFFull) + 1 == parts;
+  if (last) atomicExch(word, tag << 16);
+  return last;
+}
+
+// A head block that this block has a part of: see join_parts.
+struct Piece {
+  int i0, parts, slot0, heads;
+  int64_t out;
 };
 
 // Units of sequence b, and its visible positions.
@@ -155,6 +177,7 @@ struct Warp {
   uint32_t kw[KT * 2 * C::kChunks][4];
   uint32_t vw[KT][4][C::kVWords];
   float kd[FP8 ? KT : 1][2], vd[FP8 ? KT : 1][2];
+  float v_top, v_up;  // e4m3: bound of V's factors so far (a power of two), 2^15 / v_top
   uint32_t qf[NG][D / 16][2];
   float factor[NG][2];
   float m[NG][2], l[NG][2];
@@ -163,30 +186,37 @@ struct Warp {
   __device__ __forceinline__ Warp(const DecodeArgs& args)
       : a(args), lane(threadIdx.x % 32), r(lane / 4), q(lane % 4) {}
 
-  // q's fragments for heads hq0 .. hq0 + heads - 1 of sequence b, and the
-  // running state's start.
-  __device__ __forceinline__ void begin(int b, int hq0, int heads) {
+  // q's fragments for heads hq0 .. hq0 + heads - 1 of sequence b, as they lie.
+  __device__ __forceinline__ void load_q(int b, int hq0, int heads) {
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       const int head = g * 8 + r;
       const uint4* src = reinterpret_cast<const uint4*>(
           static_cast<const uint16_t*>(a.q) + (int64_t(b) * a.Hq + hq0 + head) * D);
       const bool live = head < heads;
-      float amax = 0.f;
 #pragma unroll
-      for (int c = 0; c < C::kChunks; ++c) {
+      for (int c = 0; c < C::kChunks; ++c)
 #pragma unroll
         for (int x = 0; x < (FP8 ? 2 : 1); ++x) {
-          const uint4 w = live ? src[(4 * c + q) * (FP8 ? 2 : 1) + x] : make_uint4(0, 0, 0, 0);
+          const uint4 w = live ? __ldg(src + (4 * c + q) * (FP8 ? 2 : 1) + x) : make_uint4(0, 0, 0, 0);
           const int step = FP8 ? 4 * c + 2 * x : 2 * c;
           qf[g][step][0] = w.x;
           qf[g][step][1] = w.y;
           qf[g][step + 1][0] = w.z;
           qf[g][step + 1][1] = w.w;
         }
-      }
+    }
+  }
+
+  // The running state's start; q in the products' type, and what turns a
+  // product into a score.
+  __device__ __forceinline__ void begin() {
+    v_top = v_up = 0.f;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
       float f = a.scale_log2;
       if (FP8) {
+        float amax = 0.f;
 #pragma unroll
         for (int s = 0; s < D / 16; ++s)
 #pragma unroll
@@ -200,16 +230,14 @@ struct Warp {
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         // 2^e puts the largest element into [2^14, 2^15)
         const int e = min(14 - (int(__float_as_uint(amax) >> 23) - 127), 126);
-        const float up = __int_as_float((e + 127) << 23);
+        const float up = pow2f(e);
 #pragma unroll
         for (int s = 0; s < D / 16; ++s)
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const __half2 h = __floats2half2_rn(bf16lo_to_f32(qf[g][s][x]) * up,
-                                                bf16hi_to_f32(qf[g][s][x]) * up);
-            qf[g][s][x] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-        f *= __int_as_float((127 - e) << 23);
+          for (int x = 0; x < 2; ++x)
+            qf[g][s][x] = pack_f16x2(bf16lo_to_f32(qf[g][s][x]) * up,
+                                     bf16hi_to_f32(qf[g][s][x]) * up);
+        f *= pow2f(-e);
       }
       // the lane of head 2q (+1) holds that column's factor
       factor[g][0] = __shfl_sync(0xffffffffu, f, 8 * q);
@@ -227,10 +255,9 @@ struct Warp {
   }
 
   // The cache row of the first key of run `lane` (lanes below KT) of the step
-  // at key `tile`; -1 where there is none to read.
+  // at key `tile`, or of the last run below len; -1 on a bad page.
   __device__ __forceinline__ int64_t find(const int* table, int kvh, int tile, int len) {
-    const int pos = tile + 16 * lane;
-    if (lane >= KT || pos >= len) return -1;
+    const int pos = min(tile + 16 * (lane % KT), (len - 1) & ~(kPageQuantum - 1));
     const int pi = int(unsigned(pos) / unsigned(a.c.page_size));
     const int page = __ldg(table + pi);
     if (!page_in_range(page, a.c.num_pages)) {
@@ -240,62 +267,92 @@ struct Warp {
     return cache_row(page, a.c.Hkv, kvh, a.c.page_size, pos - pi * a.c.page_size);
   }
 
-  __device__ __forceinline__ bool sees(int64_t row, int key, int lo, int len) const {
+  // Whether every key of the step is visible and its pages are good.
+  __device__ __forceinline__ bool full(int64_t rows, int tile, int lo, int len) const {
+    return tile >= lo && tile + 16 * KT <= len &&
+           __all_sync(0xffffffffu, rows >= 0);
+  }
+  __device__ __forceinline__ static bool sees(int64_t row, int key, int lo, int len) {
     return row >= 0 && key >= lo && key < len;
   }
 
-  __device__ __forceinline__ void load_k(int64_t rows, int tile, int lo, int len) {
+  // The loads of a step have no conditions: a run that is only partly visible
+  // is read whole (it lies on one page), one past the length reads the last
+  // run again, one on a bad page row 0, and what must not count is masked
+  // where it is used.  A
+  // branch here made the registers that wait for the loads meet at its end,
+  // and the loop wait with them (62 us became 76 for the e4m3 batch below).
+  __device__ __forceinline__ void load_k(int64_t rows) {
     const uint8_t* cache = static_cast<const uint8_t*>(a.c.kc);
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
-      const int64_t row = __shfl_sync(0xffffffffu, rows, t);
+      const int64_t row = __shfl_sync(0xffffffffu, rows < 0 ? 0 : rows, t) + r;
+      const uint8_t* base = cache + row * C::kRow + q * 16;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const bool ok = sees(row, tile + 16 * t + 8 * x + r, lo, len);
-        const int64_t at = row + 8 * x + r;
 #pragma unroll
-        for (int c = 0; c < C::kChunks; ++c) {
-          uint32_t(&w)[4] = kw[(2 * t + x) * C::kChunks + c];
-          w[0] = w[1] = w[2] = w[3] = 0;
-          if (ok) ld_stream(w, cache + at * C::kRow + c * 64 + q * 16);
-        }
+        for (int c = 0; c < C::kChunks; ++c)
+          ld_stream(kw[(2 * t + x) * C::kChunks + c], base + x * 8 * C::kRow + c * 64);
         if (FP8) {
-          kd[t][x] = ok ? __ldg(a.c.kd + at) : 0.f;
-          vd[t][x] = ok ? __ldg(a.c.vd + at) : 0.f;
+          kd[t][x] = __ldg(a.c.kd + row + 8 * x);
+          vd[t][x] = __ldg(a.c.vd + row + 8 * x);
         }
       }
     }
   }
 
   // Row j of a thread's four: key 2q + (j & 1) + 8 (j >> 1) of the run.
-  __device__ __forceinline__ void load_v(int64_t rows, int tile, int lo, int len) {
+  __device__ __forceinline__ void load_v(int64_t rows) {
     const uint8_t* cache = static_cast<const uint8_t*>(a.c.vc);
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      const int64_t row = __shfl_sync(0xffffffffu, rows < 0 ? 0 : rows, t) + 2 * q;
+      const uint8_t* base = cache + row * C::kRow + r * (C::kVWords == 2 ? 8 : 16);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint8_t* p = base + ((j & 1) + 8 * (j >> 1)) * C::kRow;
+        uint32_t(&w)[C::kVWords] = vw[t][j];
+        if (C::kVWords == 2) {
+          asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v2.b32 {%0, %1}, [%2];"
+                       : "=r"(w[0]), "=r"(w[1])
+                       : "l"(p));
+        } else {
+#pragma unroll
+          for (int i = 0; i < C::kVWords; i += 4)
+            asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[(i + 2) % C::kVWords]),
+                           "=r"(w[(i + 3) % C::kVWords])
+                         : "l"(p + i * 32));
+        }
+      }
+    }
+  }
+
+  // Of a step that is not full: scores of what is not visible become -inf,
+  // V's rows and factors there zero (they may hold anything, NaN included).
+  __device__ __forceinline__ void mask(float (&s)[KT][NG][4], int64_t rows, int tile, int lo,
+                                       int len) {
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      const int64_t row = __shfl_sync(0xffffffffu, rows, t);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (sees(row, tile + 16 * t + 8 * x + r, lo, len)) continue;
+        if (FP8) vd[t][x] = 0.f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) s[t][g][2 * x] = s[t][g][2 * x + 1] = -INFINITY;
+      }
+    }
+  }
+  __device__ __forceinline__ void mask_v(int64_t rows, int tile, int lo, int len) {
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
       const int64_t row = __shfl_sync(0xffffffffu, rows, t);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int k = 2 * q + (j & 1) + 8 * (j >> 1);
-        const bool ok = sees(row, tile + 16 * t + k, lo, len);
-        const uint8_t* p = cache + (row + k) * C::kRow;
-        uint32_t(&w)[C::kVWords] = vw[t][j];
+        if (sees(row, tile + 16 * t + 2 * q + (j & 1) + 8 * (j >> 1), lo, len)) continue;
 #pragma unroll
-        for (int i = 0; i < C::kVWords; ++i) w[i] = 0;
-        if (ok) {
-          if (C::kVWords == 2) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(p + r * 8));
-            w[0] = v.x;
-            w[1] = v.y;
-          } else {
-#pragma unroll
-            for (int i = 0; i < C::kVWords / 4; ++i) {
-              uint32_t v[4];
-              ld_stream(v, p + i * 128 + r * 16);
-#pragma unroll
-              for (int x = 0; x < 4; ++x) w[4 * i + x] = v[x];
-            }
-          }
-        }
+        for (int i = 0; i < C::kVWords; ++i) vw[t][j][i] = 0;
       }
     }
   }
@@ -329,25 +386,18 @@ struct Warp {
   }
 
   // Weight the scores of the step's keys: running maximum and sum, rescaled
-  // accumulators, and P^T as two bf16 parts in the tensor core's layout.
-  __device__ __forceinline__ void weigh(float (&s)[KT][NG][4], int64_t rows, int tile, int lo,
-                                        int len, uint32_t (&p)[KT][NG][2][2]) {
+  // accumulators, and P^T in the tensor core's layout (bf16 V: two parts).
+  static constexpr int kParts = FP8 ? 1 : 2;
+  __device__ __forceinline__ void weigh(float (&s)[KT][NG][4], bool full, int64_t rows, int tile,
+                                        int lo, int len, uint32_t (&p)[KT][NG][kParts][2]) {
 #pragma unroll
-    for (int t = 0; t < KT; ++t) {
-      const int64_t row = __shfl_sync(0xffffffffu, rows, t);
+    for (int t = 0; t < KT; ++t)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const bool ok = sees(row, tile + 16 * t + 8 * x + r, lo, len);
+      for (int g = 0; g < NG; ++g)
 #pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            float& v = s[t][g][2 * x + y];
-            const float f = FP8 ? factor[g][y] * kd[t][x] : factor[g][y];
-            v = ok ? v * f : -INFINITY;
-          }
-      }
-    }
+        for (int x = 0; x < 4; ++x)
+          s[t][g][x] *= FP8 ? factor[g][x & 1] * kd[t][x / 2] : factor[g][x & 1];
+    if (!full) mask(s, rows, tile, lo, len);
     bool grown = false;
     float ref[NG][2], alpha[NG][2];
 #pragma unroll
@@ -363,11 +413,29 @@ struct Warp {
         grown |= mx != m[g][y];
         m[g][y] = mx;
       }
+    float v_down = 1.f;
+    if (FP8) {
+      float top = 0.f;
+#pragma unroll
+      for (int t = 0; t < KT; ++t) top = max3f(top, fabsf(vd[t][0]), fabsf(vd[t][1]));
+      if (__any_sync(0xffffffffu, top > v_top)) {
+        top = keys_max(top);
+        // the power of two above it, kept where 2^15 / v_top is a number too
+        const int e = max(int(__float_as_uint(top) >> 23) - 126, -111);
+        const float next = e > 127 ? 0x1p127f : pow2f(e);
+        v_down = v_top / next;
+        v_top = next;
+        v_up = e > 127 ? 0x1p-112f : pow2f(15 - e);
+        grown = true;
+      }
+    }
     if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         l[g][0] *= alpha[g][0];
         l[g][1] *= alpha[g][1];
+        alpha[g][0] *= v_down;
+        alpha[g][1] *= v_down;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -377,29 +445,49 @@ struct Warp {
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
+      for (int x = 0; x < 2; ++x) {
+        const float up = FP8 ? vd[t][x] * v_up : 1.f;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float w0 = ex2(s[t][g][2 * x] - ref[g][0]), w1 = ex2(s[t][g][2 * x + 1] - ref[g][1]);
+        for (int g = 0; g < NG; ++g) {
+          const float w0 = ex2(s[t][g][2 * x] - ref[g][0]);
+          const float w1 = ex2(s[t][g][2 * x + 1] - ref[g][1]);
           l[g][0] += w0;
           l[g][1] += w1;
           if (FP8) {
-            w0 *= vd[t][x];
-            w1 *= vd[t][x];
+            p[t][g][0][x] = transpose_8x8(pack_f16x2(w0 * up, w1 * up));
+          } else {
+            const uint32_t hi = pack_bf16x2(w0, w1);
+            p[t][g][0][x] = transpose_8x8(hi);
+            p[t][g][kParts - 1][x] =
+                transpose_8x8(pack_bf16x2(w0 - bf16lo_to_f32(hi), w1 - bf16hi_to_f32(hi)));
           }
-          const uint32_t hi = pack_bf16x2(w0, w1);
-          const uint32_t lo2 = pack_bf16x2(w0 - bf16lo_to_f32(hi), w1 - bf16hi_to_f32(hi));
-          p[t][g][0][x] = transpose_8x8(hi);
-          p[t][g][1][x] = transpose_8x8(lo2);
         }
+      }
   }
+  // One step's keys; MORE: with the loads of the next step's among it.
+  template <bool MORE>
+  __device__ __forceinline__ void step(int64_t rows, bool full, int tile, int lo, int len,
+                                       int64_t next_rows) {
+    float s[KT][NG][4];
+#pragma unroll
+    for (int t = 0; t < KT; ++t) scores(t, s[t]);
+    uint32_t p[KT][NG][kParts][2];
+    weigh(s, full, rows, tile, lo, len, p);
+    if (MORE) load_k(next_rows);
+    if (!full) mask_v(rows, tile, lo, len);
+    add(p);
+    if (MORE) load_v(next_rows);
+  }
+
+  // What turns an accumulator into sum_j p_j v_j.
+  __device__ __forceinline__ float unit() const { return FP8 ? v_top * 0x1p-15f : 1.f; }
 
   // O^T += V^T P^T over the step's keys.  Accumulator i of a thread covers
   // output columns column(i) and the next one.
   __device__ __forceinline__ int column(int i) const {
     return FP8 ? (D / 8) * r + 2 * i : (i / 4) * 64 + 8 * r + 2 * (i % 4);
   }
-  __device__ __forceinline__ void add(const uint32_t (&p)[KT][NG][2][2]) {
+  __device__ __forceinline__ void add(const uint32_t (&p)[KT][NG][kParts][2]) {
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -409,10 +497,10 @@ struct Warp {
           const uint32_t sel = i & 1 ? 0x7362u : 0x5140u;
           const uint32_t u = __byte_perm(vw[t][0][i / 2], vw[t][1][i / 2], sel);
           const uint32_t v = __byte_perm(vw[t][2][i / 2], vw[t][3][i / 2], sel);
-          a0 = e4m3x2_to_bf16x2(u);
-          a1 = e4m3x2_to_bf16x2(u >> 16);
-          a2 = e4m3x2_to_bf16x2(v);
-          a3 = e4m3x2_to_bf16x2(v >> 16);
+          a0 = e4m3x2_to_f16x2(u);
+          a1 = e4m3x2_to_f16x2(u >> 16);
+          a2 = e4m3x2_to_f16x2(v);
+          a3 = e4m3x2_to_f16x2(v >> 16);
         } else {
           a0 = __byte_perm(vw[t][0][i], vw[t][1][i], 0x5410);
           a1 = __byte_perm(vw[t][0][i], vw[t][1][i], 0x7632);
@@ -422,11 +510,122 @@ struct Warp {
 #pragma unroll
         for (int g = 0; g < NG; ++g)
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
-            mma_16x8x16<false>(acc[g][i], a0, a1, a2, a3, p[t][g][x][0], p[t][g][x][1]);
+          for (int x = 0; x < kParts; ++x)
+            mma_16x8x16<FP8>(acc[g][i], a0, a1, a2, a3, p[t][g][x][0], p[t][g][x][1]);
       }
   }
 };
+
+// The parts of one head block joined: part 0 in slot0, part k of share i0 + k
+// in that share's first slot; out = index of the head block's first output
+// row.  A warp takes HP heads at a time (two or four warps share a head when
+// there are fewer heads than warps), 16 rows of parts in flight, the first of
+// them ahead of the maximum that weights them; added in a fixed order.
+template <int D, int HP>
+__device__ __forceinline__ void join_parts(const DecodeArgs& a, const Piece& pc, float (*sh)[D]) {
+  constexpr int kCols = D / 32;      // output columns of a lane
+  constexpr int kFlight = 16 / HP;   // parts of a batch
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int share = HP > 1 || pc.heads >= 3 ? 1 : (pc.heads == 2 ? 2 : 4);  // warps per head
+  const int first = warp % share;
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
+  for (int h0 = 0; h0 < pc.heads; h0 += kWarps * HP / share) {
+    const int head = h0 + warp / share * HP;
+    auto at = [&](int k, int x) {
+      return int64_t(k == 0 ? pc.slot0 : 2 * (pc.i0 + k)) * kDecodeHeads + head + x;
+    };
+    float acc[HP][kCols], M[HP], sum[HP], ref[HP];
+    bool live[HP];
+#pragma unroll
+    for (int x = 0; x < HP; ++x) {
+      live[x] = head + x < pc.heads;
+      M[x] = -INFINITY;
+      sum[x] = ref[x] = 0.f;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) acc[x][c] = 0.f;
+    }
+    for (int k0 = first * kFlight; k0 < pc.parts || k0 == first * kFlight; k0 += kFlight * share) {
+      float o[HP][kFlight][kCols];
+      float2 mine[HP];  // lane j: maximum and sum of part k0 + j
+#pragma unroll
+      for (int x = 0; x < HP; ++x) {
+        mine[x] = make_float2(-INFINITY, 0.f);
+        if (live[x] && lane < kFlight && k0 + lane < pc.parts) mine[x] = __ldcg(ml + at(k0 + lane, x));
+#pragma unroll
+        for (int j = 0; j < kFlight; ++j) {
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) o[x][j][c] = 0.f;
+          if (!live[x] || k0 + j >= pc.parts) continue;
+          const float* src = a.part_o + at(k0 + j, x) * D + lane * kCols;
+          if (kCols == 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+            o[x][j][0] = v.x;
+            o[x][j][1] = v.y;
+            o[x][j][kCols - 2] = v.z;
+            o[x][j][kCols - 1] = v.w;
+          } else {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+            o[x][j][0] = v.x;
+            o[x][j][1] = v.y;
+          }
+        }
+      }
+      if (k0 == first * kFlight) {
+#pragma unroll
+        for (int x = 0; x < HP; ++x) {
+          if (live[x])
+            for (int k = lane; k < pc.parts; k += 32) M[x] = fmaxf(M[x], __ldcg(ml + at(k, x)).x);
+#pragma unroll
+          for (int s = 16; s > 0; s >>= 1)
+            M[x] = fmaxf(M[x], __shfl_xor_sync(0xffffffffu, M[x], s));
+          ref[x] = M[x] == -INFINITY ? 0.f : M[x];
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < HP; ++x) {
+        const float e = ex2(mine[x].x - ref[x]);
+        sum[x] += e * mine[x].y;
+#pragma unroll
+        for (int j = 0; j < kFlight; ++j) {
+          const float w = __shfl_sync(0xffffffffu, e, j);
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) acc[x][c] += w * o[x][j][c];
+        }
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < HP; ++x)
+#pragma unroll
+      for (int s = kFlight / 2; s > 0; s >>= 1)
+        sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], s);
+    if (HP == 1 && share > 1) {  // one round of the loop: every head has its warps
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) sh[warp][lane * kCols + c] = acc[0][c];
+      if (lane == 0) sh[kWarps][warp] = sum[0];
+      __syncthreads();
+      if (first) continue;
+      for (int w = 1; w < share; ++w) {
+        sum[0] += sh[kWarps][warp + w];
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) acc[0][c] += sh[warp + w][lane * kCols + c];
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < HP; ++x) {
+      if (!live[x]) continue;
+      const int64_t row = pc.out + head + x;
+      // lanes of kFlight or more hold no part: the sum is lane 0's
+      const float total = __shfl_sync(0xffffffffu, sum[x], 0);
+      const float inv = total == 0.f ? 0.f : 1.f / total;
+      uint32_t* dst =
+          reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + row * D + lane * kCols);
+#pragma unroll
+      for (int c = 0; c < kCols; c += 2)
+        dst[c / 2] = pack_bf16x2(acc[x][c] * inv, acc[x][c + 1] * inv);
+      if (lane == 0) a.lse[row] = total == 0.f ? -INFINITY : (M[x] + log2f(total)) * kLn2;
+    }
+  }
+}
 
 template <int D, bool FP8, int NG>
 __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const DecodeArgs a) {
@@ -438,6 +637,8 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
   __shared__ int64_t sh_scan[kWarps];
   __shared__ int64_t sh_prefix;
   __shared__ int sh_b;
+  __shared__ bool sh_last[2];
+  __shared__ Piece sh_piece[2];
 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const HeadSplit split = split_heads(a.Hq / a.c.Hkv);
@@ -482,13 +683,10 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
     for (int i = tid; i < a.Hq; i += kThreads) a.lse[int64_t(b) * a.Hq + i] = -INFINITY;
   }
 
-  Start* starts = reinterpret_cast<Start*>(a.meta);
-  if (int(blockIdx.x) >= G) {
-    if (tid == 0) starts[blockIdx.x] = {0, 0, 0, 0};
-    return;
-  }
+  if (int(blockIdx.x) >= G) return;
   const int64_t w0 = split_begin(blockIdx.x, W, G);
   int64_t left = split_begin(blockIdx.x + 1, W, G) - w0;
+  int64_t at_unit = w0;  // first unit of the current piece
 
   // The sequence that holds unit w0: its thread's part holds it.
   {
@@ -515,45 +713,52 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
     h = int(x / n);
     u = int(x - int64_t(h) * n);
   }
-  if (tid == 0) {
-    starts[blockIdx.x] = {b, h, u, n};
-    if (blockIdx.x == 0) *reinterpret_cast<int64_t*>(starts + kDecodeMaxBlocks) = W;
-  }
-
   Warp<D, FP8, NG> wp(a);
+  const int group = a.Hq / a.c.Hkv;
   bool first_segment = true;
-  while (true) {
-    const int units = int(left < n - u ? left : n - u);
+  int pieces = 0;
+  // The piece of head block (b, h) from unit u on: where it lies, and its
+  // first loads.
+  int units, heads, tile;
+  int64_t out, rows;
+  auto enter = [&] {
+    units = int(left < n - u ? left : n - u);
     const int kvh = h / split.blocks, hb = h % split.blocks;
-    const int group = a.Hq / a.c.Hkv;
     const int hq0 = kvh * group + hb * split.heads;
-    const int heads = min(split.heads, group - hb * split.heads);
-    const int* table = a.c.table + int64_t(b) * a.c.max_pages;
-    wp.begin(b, hq0, heads);
-
-    int tile = (lo & ~(kPageQuantum - 1)) + u * U + warp * C::KT * 16;
-    int64_t rows = wp.find(table, kvh, tile, len);
-    wp.load_k(rows, tile, lo, len);
-    wp.load_v(rows, tile, lo, len);
-    for (int i = 0; i < units; ++i) {
-      // past the last step nothing is read: its keys are not below len
-      const bool more = i + 1 < units;
-      const int next_tile = tile + U;
-      const int next_len = more ? len : 0;
-      const int64_t next_rows = wp.find(table, kvh, next_tile, next_len);
-      float s[C::KT][NG][4];
-#pragma unroll
-      for (int t = 0; t < C::KT; ++t) wp.scores(t, s[t]);
-      uint32_t p[C::KT][NG][2][2];
-      wp.weigh(s, rows, tile, lo, len, p);
-      wp.load_k(next_rows, next_tile, lo, next_len);
-      wp.add(p);
-      wp.load_v(next_rows, next_tile, lo, next_len);
-      tile = next_tile;
-      rows = next_rows;
+    heads = min(split.heads, group - hb * split.heads);
+    out = int64_t(b) * a.Hq + hq0;
+    tile = (lo & ~(kPageQuantum - 1)) + u * U + warp * C::KT * 16;
+    rows = wp.find(a.c.table + int64_t(b) * a.c.max_pages, kvh, tile, len);
+    wp.load_q(b, hq0, heads);
+    wp.load_k(rows);
+    wp.load_v(rows);
+  };
+  enter();
+  while (true) {
+    const bool whole = u == 0 && units == n;
+    const int64_t first_unit = at_unit - u;  // of the head block
+    const int i0 = whole ? int(blockIdx.x) : split_owner(first_unit, W, G);
+    if (!whole && tid == 0) open_count(a.arrivals + i0, a.tag);
+    wp.begin();
+    {
+      const int* table = a.c.table + int64_t(b) * a.c.max_pages;
+      const int kvh = h / split.blocks;
+      bool full = wp.full(rows, tile, lo, len);
+      // The last step stands apart: it has nothing to load.
+      for (int i = 1; i < units; ++i) {
+        const int64_t next_rows = wp.find(table, kvh, tile + U, len);
+        wp.template step<true>(rows, full, tile, lo, len, next_rows);
+        tile += U;
+        rows = next_rows;
+        full = wp.full(rows, tile, lo, len);
+      }
+      wp.template step<false>(rows, full, tile, lo, len, 0);
     }
 
-    // Join the four warps.
+    // The piece's results leave the registers; the next piece's first loads
+    // are under way while they are joined.
+    const int done_heads = heads, done_n = n;
+    const int64_t done_out = out;
 #pragma unroll
     for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -567,12 +772,22 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
           *reinterpret_cast<float2*>(&sh_o[warp][head][wp.column(i)]) =
-              make_float2(wp.acc[g][i][y], wp.acc[g][i][2 + y]);
+              make_float2(wp.acc[g][i][y] * wp.unit(), wp.acc[g][i][2 + y] * wp.unit());
       }
+    left -= units;
+    at_unit += units;
+    if (left) {
+      u = 0;
+      if (++h == Hn) {
+        h = 0;
+        do n = sequence_units<U>(a, ++b, &lo, &len);
+        while (n == 0);
+      }
+      enter();
+    }
     __syncthreads();
-    const bool whole = u == 0 && units == n;
     const int slot = 2 * blockIdx.x + (first_segment ? 0 : 1);
-    for (int i = tid; i < heads * (D / 2); i += kThreads) {
+    for (int i = tid; i < done_heads * (D / 2); i += kThreads) {
       const int head = i / (D / 2), c = 2 * (i % (D / 2));
       float M = -INFINITY;
 #pragma unroll
@@ -587,113 +802,52 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
         o1 += e * sh_o[w][head][c + 1];
       }
       if (whole) {
-        const int64_t out = int64_t(b) * a.Hq + hq0 + head;
+        const int64_t row = done_out + head;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + out * D + c) =
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + row * D + c) =
             pack_bf16x2(o0 * inv, o1 * inv);
-        if (c == 0) a.lse[out] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
+        if (c == 0) a.lse[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
       } else {
         const int64_t at = int64_t(slot) * kDecodeHeads + head;
         *reinterpret_cast<float2*>(a.part_o + at * D + c) = make_float2(o0, o1);
         if (c == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(M, sum);
       }
     }
-
-    left -= units;
-    if (left == 0) break;
-    __syncthreads();  // the shared tiles are free again
-    first_segment = false;
-    u = 0;
-    if (++h == Hn) {
-      h = 0;
-      do n = sequence_units<U>(a, ++b, &lo, &len);
-      while (n == 0);
+    if (!whole) {  // at most twice: a share's first and last head block
+      if (tid == 0)
+        sh_piece[pieces] = {i0, split_owner(first_unit + done_n - 1, W, G) - i0 + 1,
+                            // the first share may have come here after another head block
+                            2 * i0 + (split_begin(i0, W, G) < first_unit ? 1 : 0), done_heads,
+                            done_out};
+      ++pieces;
     }
+    __syncthreads();  // the shared tiles are free again, the parts are written
+    if (left == 0) break;
+    first_segment = false;
   }
-}
 
-// Joins the parts of every head block that more than one block worked on.
-// Grid block (j, head): if block j of the split began inside a head block,
-// and is the first to do so there, its predecessor holds that head block's
-// first part, and the parts up to the owner of its last unit are joined.
-template <int D>
-__global__ void __launch_bounds__(256) join_kernel(const DecodeArgs a) {
-  constexpr int kCols = D / 4;            // threads across the output
-  constexpr int kLanes = 256 / kCols;     // parts added at once
-  __shared__ float4 sh[kLanes][kCols];
-  grid_dep_wait();
-  grid_dep_launch();
-  const Start* starts = reinterpret_cast<const Start*>(a.meta);
-  const int j = blockIdx.x + 1;
-  const int4 st = __ldg(reinterpret_cast<const int4*>(starts + j));
-  const Start s = {st.x, st.y, st.z, st.w};
-  if (s.u == 0) return;
-  const int64_t W = *reinterpret_cast<const int64_t*>(starts + kDecodeMaxBlocks);
-  const int blocks = gridDim.x + 1;
-  const int G = int(W < blocks ? W : blocks);
-  const int64_t begin = split_begin(j, W, G) - s.u;
-  const int i0 = split_owner(begin, W, G);
-  if (i0 != j - 1) return;
-  const int i1 = split_owner(begin + s.n - 1, W, G);
-  const int group = a.Hq / a.c.Hkv;
-  const HeadSplit split = split_heads(group);
-  const int hb = s.h % split.blocks;
-  const int head = blockIdx.y;
-  if (head >= min(split.heads, group - hb * split.heads)) return;
-
-  // part k: block i0 + k; its first piece of work, except that the first
-  // block may have come to this head block after another one
-  const int parts = i1 - i0 + 1;
-  const int slot0 = 2 * i0 + (split_begin(i0, W, G) < begin ? 1 : 0);
-  const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
-  auto at = [&](int k) {
-    return int64_t(k == 0 ? slot0 : 2 * (i0 + k)) * kDecodeHeads + head;
-  };
-  const int lane = threadIdx.x % 32;
-  float M = -INFINITY;
-  for (int k = lane; k < parts; k += 32) M = fmaxf(M, ml[at(k)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float ref = M == -INFINITY ? 0.f : M;
-  float sum = 0.f;
-  for (int k = lane; k < parts; k += 32) {
-    const float2 x = ml[at(k)];
-    sum += ex2(x.x - ref) * x.y;
+  // Both pieces' arrivals at once, after one fence.
+  if (pieces == 0) return;
+  if (tid < pieces) {
+    fence_acq_rel_gpu();
+    sh_last[tid] = arrive(a.arrivals + sh_piece[tid].i0, a.tag, sh_piece[tid].parts);
+    fence_acq_rel_gpu();
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-
-  const int col = threadIdx.x % kCols, part = threadIdx.x / kCols;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = part; k < parts; k += kLanes) {
-    const float e = ex2(ml[at(k)].x - ref);
-    const float4 x = *reinterpret_cast<const float4*>(a.part_o + at(k) * D + col * 4);
-    acc.x += e * x.x;
-    acc.y += e * x.y;
-    acc.z += e * x.z;
-    acc.w += e * x.w;
-  }
-  sh[part][col] = acc;
   __syncthreads();
-  if (part) return;
-#pragma unroll
-  for (int k = 1; k < kLanes; ++k) {
-    const float4 x = sh[k][col];
-    acc.x += x.x;
-    acc.y += x.y;
-    acc.z += x.z;
-    acc.w += x.w;
-  }
-  const int64_t out = int64_t(s.b) * a.Hq + (s.h / split.blocks) * group + hb * split.heads + head;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + out * D + col * 4) =
-      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (col == 0) a.lse[out] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
+  for (int x = 0; x < pieces; ++x)
+    if (sh_last[x]) {
+      const Piece pc = sh_piece[x];
+      float(*sh)[D] = reinterpret_cast<float(*)[D]>(&sh_o[0][0][0]);
+      if (pc.heads > kWarps)
+        join_parts<D, 2>(a, pc, sh);
+      else
+        join_parts<D, 1>(a, pc, sh);
+      __syncthreads();
+    }
 }
 
 template <int D, bool FP8, int NG>
-cudaError_t launch(const DecodeArgs& a, int heads, cudaStream_t stream) {
+cudaError_t launch(const DecodeArgs& a, cudaStream_t stream) {
   using C = Cfg<D, FP8>;
   constexpr int kPerSm = NG == 1 ? 3 : 2;  // resident blocks: see __launch_bounds__
   // at most as many blocks as there can be units
@@ -703,17 +857,14 @@ cudaError_t launch(const DecodeArgs& a, int heads, cudaStream_t stream) {
   int64_t grid = int64_t(device_sm_count()) * kPerSm;
   if (grid > kDecodeMaxBlocks) grid = kDecodeMaxBlocks;
   if (grid > units) grid = units;
-  cudaError_t e = launch_kernel(decode_kernel<D, FP8, NG>, dim3(unsigned(grid)), dim3(kThreads), 0,
-                                stream, a);
-  if (e != cudaSuccess || grid == 1) return e;
-  return launch_kernel(join_kernel<D>, dim3(unsigned(grid - 1), unsigned(heads)), dim3(256), 0,
-                       stream, a);
+  return launch_kernel(decode_kernel<D, FP8, NG>, dim3(unsigned(grid)), dim3(kThreads), 0, stream,
+                       a);
 }
 
 template <int D, bool FP8>
 cudaError_t launch_heads(const DecodeArgs& a, cudaStream_t stream) {
   const int heads = split_heads(a.Hq / a.c.Hkv).heads;
-  return heads <= 8 ? launch<D, FP8, 1>(a, heads, stream) : launch<D, FP8, 2>(a, heads, stream);
+  return heads <= 8 ? launch<D, FP8, 1>(a, stream) : launch<D, FP8, 2>(a, stream);
 }
 
 }  // namespace

@@ -25,6 +25,7 @@ namespace attn {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kRows = 2;
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
 
@@ -58,60 +59,78 @@ __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) 
 struct Row {
   int b, h, t;
 };
-__device__ __forceinline__ Row row_of(int64_t i, int T, int Hkv) {
-  const int64_t bh = i / T;
-  return {int(bh / Hkv), int(bh % Hkv), int(i - bh * T)};
+__device__ __forceinline__ Row row_of(unsigned i, unsigned T, unsigned Hkv) {
+  const unsigned bh = i / T, b = bh / Hkv;
+  return {int(b), int(bh - b * Hkv), int(i - bh * T)};
 }
 
-template <int D, bool FP8>
+// Where row w of the call lies in the cache, or -1 (recorded by `lane` 0).
+__device__ __forceinline__ int64_t locate(const CacheArgs& c, const CacheRows& r, const Row& w,
+                                          int site, int lane, int* err) {
+  if (w.t >= (r.count ? __ldg(r.count + w.b) : r.T)) return -1;
+  const int64_t pos = int64_t(__ldg(r.start + w.b)) + w.t;
+  if (pos < 0 || pos >= c.capacity) {
+    if (lane == 0) report_error(err, kDevBadIndex, kSiteLength);
+    return -1;
+  }
+  const unsigned p = unsigned(pos), pi = p / unsigned(c.page_size);
+  const int page = __ldg(c.table + int64_t(w.b) * c.max_pages + pi);
+  if (!page_in_range(page, c.num_pages)) {
+    if (lane == 0) report_error(err, kDevBadIndex, site);
+    return -1;
+  }
+  return cache_row(page, c.Hkv, w.h, c.page_size, int(p - pi * c.page_size));
+}
+
+// Each group of D / 8 lanes takes R rows, their loads issued together.
+template <int D, bool FP8, int R>
 __global__ void __launch_bounds__(kThreads)
-    kv_write_kernel(const CacheArgs c, const CacheRows r, int64_t rows, int* err) {
-  constexpr int kLanes = D / 8;
+    kv_write_kernel(const CacheArgs c, const CacheRows r, unsigned rows, int* err) {
+  constexpr int kLanes = D / 8, kGroups = kThreads / kLanes;
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x % kLanes;
-  const int64_t i = int64_t(blockIdx.x) * (kThreads / kLanes) + threadIdx.x / kLanes;
-  const bool live = i < rows;
-  const Row w = live ? row_of(i, r.T, c.Hkv) : Row{0, 0, 0};
-  bool ok = live && w.t < (r.count ? __ldg(r.count + w.b) : r.T);
-  int64_t dst = 0;
-  if (ok) {
-    const int64_t pos = int64_t(__ldg(r.start + w.b)) + w.t;
-    ok = pos >= 0 && pos < c.capacity;
-    if (!ok && lane == 0) report_error(err, kDevBadIndex, kSiteLength);
-    if (ok) {
-      const int pi = int(pos) / c.page_size;
-      const int page = __ldg(c.table + int64_t(w.b) * c.max_pages + pi);
-      ok = page_in_range(page, c.num_pages);
-      if (!ok && lane == 0) report_error(err, kDevBadIndex, kSiteWritePage);
-      dst = cache_row(page, c.Hkv, w.h, c.page_size, int(pos) - pi * c.page_size);
-    }
+  const unsigned first = blockIdx.x * (kGroups * R) + threadIdx.x / kLanes;
+  int64_t dst[R];
+  uint4 x[R][2];
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    const unsigned i = first + j * kGroups;
+    dst[j] = -1;
+    x[j][0] = x[j][1] = make_uint4(0, 0, 0, 0);
+    if (i >= rows) continue;
+    const Row w = row_of(i, r.T, c.Hkv);
+    dst[j] = locate(c, r, w, kSiteWritePage, lane, err);
+    if (dst[j] < 0) continue;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      x[j][s] = __ldg(reinterpret_cast<const uint4*>(
+          static_cast<const uint16_t*>(r.x[s]) + w.b * r.sb[s] + w.h * r.sh[s] + w.t * r.st[s] +
+          lane * 8));
   }
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (ok)
-      x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(r.x[s]) + w.b * r.sb[s] +
-                                          w.h * r.sh[s] + w.t * r.st[s] + lane * 8);
-    uint8_t* cache = static_cast<uint8_t*>(s ? c.vc : c.kc);
-    if (!FP8) {
-      if (ok) *reinterpret_cast<uint4*>(cache + (dst * D + lane * 8) * 2) = x;
-    } else {
-      const int e = descale_exponent(row_amax_bits<kLanes>(x));  // all lanes: shuffles
-      if (!ok) continue;
+  for (int j = 0; j < R; ++j)
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      uint8_t* cache = static_cast<uint8_t*>(s ? c.vc : c.kc);
+      if (!FP8) {
+        if (dst[j] >= 0) *reinterpret_cast<uint4*>(cache + (dst[j] * D + lane * 8) * 2) = x[j][s];
+        continue;
+      }
+      const int e = descale_exponent(row_amax_bits<kLanes>(x[j][s]));  // all lanes: shuffles
+      if (dst[j] < 0) continue;
       const float inv = pow2f(-e);
-      const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
+      const uint32_t w4[4] = {x[j][s].x, x[j][s].y, x[j][s].z, x[j][s].w};
       float f[8];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         f[2 * k] = bf16lo_to_f32(w4[k]) * inv;
         f[2 * k + 1] = bf16hi_to_f32(w4[k]) * inv;
       }
-      *reinterpret_cast<uint2*>(cache + dst * D + lane * 8) =
+      *reinterpret_cast<uint2*>(cache + dst[j] * D + lane * 8) =
           make_uint2(pack_e4m3x4(f[0], f[1], f[2], f[3]), pack_e4m3x4(f[4], f[5], f[6], f[7]));
-      if (lane == 0) (s ? c.vd : c.kd)[dst] = pow2f(e);
+      if (lane == 0) (s ? c.vd : c.kd)[dst[j]] = pow2f(e);
     }
-  }
 }
 
 // Two e4m3 values (low 16 bits) as floats, exactly.
@@ -121,61 +140,70 @@ __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t two) {
   return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, int R>
 __global__ void __launch_bounds__(kThreads)
-    kv_read_kernel(const CacheArgs c, const CacheRows r, int64_t rows, int* err) {
-  constexpr int kLanes = D / 8;
+    kv_read_kernel(const CacheArgs c, const CacheRows r, unsigned rows, int* err) {
+  constexpr int kLanes = D / 8, kGroups = kThreads / kLanes;
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x % kLanes;
-  const int64_t i = int64_t(blockIdx.x) * (kThreads / kLanes) + threadIdx.x / kLanes;
-  if (i >= rows) return;
-  const Row w = row_of(i, r.T, c.Hkv);
-  bool ok = w.t < (r.count ? __ldg(r.count + w.b) : r.T);
-  int64_t src = 0;
-  if (ok) {
-    const int64_t pos = int64_t(__ldg(r.start + w.b)) + w.t;
-    ok = pos >= 0 && pos < c.capacity;
-    if (!ok && lane == 0) report_error(err, kDevBadIndex, kSiteLength);
-    if (ok) {
-      const int pi = int(pos) / c.page_size;
-      const int page = __ldg(c.table + int64_t(w.b) * c.max_pages + pi);
-      ok = page_in_range(page, c.num_pages);
-      if (!ok && lane == 0) report_error(err, kDevBadIndex, kSiteReadPage);
-      src = cache_row(page, c.Hkv, w.h, c.page_size, int(pos) - pi * c.page_size);
+  const unsigned first = blockIdx.x * (kGroups * R) + threadIdx.x / kLanes;
+  uint4 x[R][2];  // e4m3: the first two words
+  float f[R][2];
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    const unsigned i = first + j * kGroups;
+    x[j][0] = x[j][1] = make_uint4(0, 0, 0, 0);
+    f[j][0] = f[j][1] = 0.f;
+    if (i >= rows) continue;
+    const int64_t src = locate(c, r, row_of(i, r.T, c.Hkv), kSiteReadPage, lane, err);
+    if (src < 0) continue;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const uint8_t* cache = static_cast<const uint8_t*>(s ? c.vc : c.kc);
+      if (FP8) {
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(cache + src * D + lane * 8));
+        x[j][s].x = u.x;
+        x[j][s].y = u.y;
+        f[j][s] = __ldg((s ? c.vd : c.kd) + src);
+      } else {
+        x[j][s] = __ldg(reinterpret_cast<const uint4*>(cache + (src * D + lane * 8) * 2));
+      }
     }
   }
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    uint4 y = make_uint4(0, 0, 0, 0);
-    const uint8_t* cache = static_cast<const uint8_t*>(s ? c.vc : c.kc);
-    if (ok) {
-      if (!FP8) {
-        y = *reinterpret_cast<const uint4*>(cache + (src * D + lane * 8) * 2);
-      } else {
-        const uint2 u = *reinterpret_cast<const uint2*>(cache + src * D + lane * 8);
-        const float f = (s ? c.vd : c.kd)[src];
+  for (int j = 0; j < R; ++j) {
+    const unsigned i = first + j * kGroups;
+    if (i >= rows) continue;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      uint4 y = x[j][s];
+      if (FP8) {
         uint32_t o[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float2 g = e4m3x2_to_f32((k < 2 ? u.x : u.y) >> (k & 1 ? 16 : 0));
-          o[k] = pack_bf16x2(g.x * f, g.y * f);
+          const float2 g = e4m3x2_to_f32((k < 2 ? y.x : y.y) >> (k & 1 ? 16 : 0));
+          o[k] = pack_bf16x2(g.x * f[j][s], g.y * f[j][s]);
         }
         y = make_uint4(o[0], o[1], o[2], o[3]);
       }
+      // the output is contiguous: row i of [B][Hkv][T]
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(r.x[s]) + int64_t(i) * D + lane * 8) = y;
     }
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(r.x[s]) + w.b * r.sb[s] + w.h * r.sh[s] +
-                              w.t * r.st[s] + lane * 8) = y;
   }
 }
 
+// Rows per group of lanes: one while that leaves the GPU short of blocks.
 template <typename K>
-cudaError_t launch(K kernel, const CacheArgs& c, const CacheRows& r, int* err,
+cudaError_t launch(K one, K several, const CacheArgs& c, const CacheRows& r, int* err,
                    cudaStream_t stream) {
-  const int64_t rows = int64_t(c.B) * c.Hkv * r.T;
-  const int per_block = kThreads / (c.d / 8);
-  return launch_kernel(kernel, dim3(unsigned((rows + per_block - 1) / per_block)), dim3(kThreads),
-                       0, stream, c, r, rows, err);
+  const unsigned rows = unsigned(int64_t(c.B) * c.Hkv * r.T);
+  const unsigned groups = kThreads / (c.d / 8);
+  const unsigned blocks = (rows + groups - 1) / groups;
+  if (blocks <= unsigned(device_sm_count()) * 8)
+    return launch_kernel(one, dim3(blocks), dim3(kThreads), 0, stream, c, r, rows, err);
+  return launch_kernel(several, dim3((blocks + kRows - 1) / kRows), dim3(kThreads), 0, stream, c, r,
+                       rows, err);
 }
 
 }  // namespace
@@ -183,19 +211,19 @@ cudaError_t launch(K kernel, const CacheArgs& c, const CacheRows& r, int* err,
 cudaError_t launch_kv_write(const CacheArgs& c, const CacheRows& r, int* err,
                             cudaStream_t stream) {
   if (c.d == 64)
-    return c.kd ? launch(kv_write_kernel<64, true>, c, r, err, stream)
-                : launch(kv_write_kernel<64, false>, c, r, err, stream);
-  return c.kd ? launch(kv_write_kernel<128, true>, c, r, err, stream)
-              : launch(kv_write_kernel<128, false>, c, r, err, stream);
+    return c.kd ? launch(kv_write_kernel<64, true, 1>, kv_write_kernel<64, true, kRows>, c, r, err, stream)
+                : launch(kv_write_kernel<64, false, 1>, kv_write_kernel<64, false, kRows>, c, r, err, stream);
+  return c.kd ? launch(kv_write_kernel<128, true, 1>, kv_write_kernel<128, true, kRows>, c, r, err, stream)
+              : launch(kv_write_kernel<128, false, 1>, kv_write_kernel<128, false, kRows>, c, r, err, stream);
 }
 
 cudaError_t launch_kv_read(const CacheArgs& c, const CacheRows& r, int* err,
                            cudaStream_t stream) {
   if (c.d == 64)
-    return c.kd ? launch(kv_read_kernel<64, true>, c, r, err, stream)
-                : launch(kv_read_kernel<64, false>, c, r, err, stream);
-  return c.kd ? launch(kv_read_kernel<128, true>, c, r, err, stream)
-              : launch(kv_read_kernel<128, false>, c, r, err, stream);
+    return c.kd ? launch(kv_read_kernel<64, true, 1>, kv_read_kernel<64, true, kRows>, c, r, err, stream)
+                : launch(kv_read_kernel<64, false, 1>, kv_read_kernel<64, false, kRows>, c, r, err, stream);
+  return c.kd ? launch(kv_read_kernel<128, true, 1>, kv_read_kernel<128, true, kRows>, c, r, err, stream)
+              : launch(kv_read_kernel<128, false, 1>, kv_read_kernel<128, false, kRows>, c, r, err, stream);
 }
 
 }  // namespace attn

@@ -20,6 +20,8 @@
 //
 // A thread owns 8 pairs (two 16-byte pieces) of a token, forms their eight
 // sines and cosines once, and runs over heads of q and k with them.
+#include <algorithm>
+
 #include "kernels.h"
 #include "ptx.cuh"
 #include "serving.h"
@@ -27,8 +29,9 @@
 namespace attn {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kPairs = 8;  // per thread
+constexpr int kBlocksPerSm = 8;
 
 // floor(2^64 / (2 pi)): the turn of one radian.
 constexpr uint64_t kTurnPerRadian = 0x28BE60DB9391054Aull;
@@ -116,8 +119,14 @@ cudaError_t launch(const RopeArgs& a, cudaStream_t stream) {
   constexpr int kTokens = kThreads / (D / 2 / kPairs);
   const int64_t blocks = (int64_t(a.B) * a.N + kTokens - 1) / kTokens;
   const int heads = a.heads[0] + a.heads[1];
-  return launch_kernel(rope_kernel<D, INTERLEAVED>, dim3(unsigned(blocks), 1), dim3(kThreads), 0,
-                       stream, a, heads);
+  // Few tokens: the heads are split over blocks too, each with sines of its
+  // own, until there are about kBlocksPerSm for every SM.
+  const int64_t want = int64_t(device_sm_count()) * kBlocksPerSm;
+  const int64_t slices = std::min<int64_t>({heads, (want + blocks - 1) / blocks, 65535});
+  const int slice = int((heads + slices - 1) / slices);
+  return launch_kernel(rope_kernel<D, INTERLEAVED>,
+                       dim3(unsigned(blocks), unsigned((heads + slice - 1) / slice)),
+                       dim3(kThreads), 0, stream, a, slice);
 }
 
 }  // namespace

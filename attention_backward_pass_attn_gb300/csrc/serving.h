@@ -55,8 +55,8 @@ struct CacheArgs {
   int capacity;      // max_pages * page_size
 };
 
-// kv_cache.cu.  Rows of k and v: [B][Hkv][T][d] with element strides (batch,
-// head, token).
+// kv_cache.cu.  Rows of k and v: [B][Hkv][T][d], read with element strides
+// (batch, head, token), written contiguous.
 struct CacheRows {
   void* x[2];  // k, v
   int64_t sb[2], sh[2], st[2];
@@ -77,7 +77,8 @@ struct DecodeArgs {
   int Hq;
   int window;
   float scale_log2;      // scale * log2(e)
-  int* meta;             // workspace: int4 per thread block, its first unit; then int64 W
+  unsigned long long* arrivals;  // workspace: a word per thread block, see arrive()
+  unsigned long long tag;        // 48 bits, another one for every call
   float* part_ml;        // workspace: [2 * blocks][16][2] running maximum and sum
   float* part_o;         // workspace: [2 * blocks][16][d] unnormalised output
   int* err;
@@ -85,7 +86,9 @@ struct DecodeArgs {
 // Thread blocks the split's workspace provides for.
 constexpr int kDecodeMaxBlocks = 608;
 constexpr int kDecodeHeads = 16;  // heads of one key/value head a block works on at most
-inline size_t decode_meta_bytes() { return (sizeof(int) * 4 * size_t(kDecodeMaxBlocks) + sizeof(int64_t) + 255) / 256 * 256; }
+inline size_t decode_arrival_bytes() {
+  return (sizeof(unsigned long long) * kDecodeMaxBlocks + 255) / 256 * 256;
+}
 inline size_t decode_ml_bytes() {
   return sizeof(float) * 2 * kDecodeHeads * 2 * size_t(kDecodeMaxBlocks);
 }

@@ -2,6 +2,8 @@
 // include/attn.h): rotary positions, the paged key/value cache and attention
 // of one new token.  Argument validation, workspace carve-up, and the calls
 // into the kernel launchers.
+#include <atomic>
+#include <chrono>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -108,6 +110,15 @@ int set_cache(CacheArgs* c, const void* kc, const void* vc, const float* kd, con
   return ATTN_OK;
 }
 
+// A 48-bit number that no earlier call of this process had, and another
+// process's calls hardly: what the decode's arrival words are told apart by.
+unsigned long long next_tag() {
+  static std::atomic<unsigned long long> tag{
+      (unsigned long long)std::chrono::steady_clock::now().time_since_epoch().count() *
+      0x9E3779B97F4A7C15ull};
+  return tag.fetch_add(1, std::memory_order_relaxed) & 0xFFFFFFFFFFFFull;
+}
+
 }  // namespace
 }  // namespace attn
 
@@ -178,7 +189,6 @@ int kv_cache_read(const void* K_cache, const void* V_cache, const float* k_desca
   CacheRows r = {};
   r.x[0] = K;
   r.x[1] = V;
-  for (int s = 0; s < 2; ++s) set_strides(nullptr, B, Hkv, T, d, &r.sb[s], &r.sh[s], &r.st[s]);
   r.start = start;
   r.count = count;
   r.T = T;
@@ -189,7 +199,7 @@ int kv_cache_read(const void* K_cache, const void* V_cache, const float* k_desca
 
 size_t attn_decode_workspace_size(int d) {
   if (d != 64 && d != 128) return 0;
-  return decode_meta_bytes() + decode_ml_bytes() + decode_o_bytes(d);
+  return decode_arrival_bytes() + decode_ml_bytes() + decode_o_bytes(d);
 }
 
 int attn_decode(const void* Q, const void* K_cache, const void* V_cache, const float* k_descale,
@@ -220,9 +230,10 @@ int attn_decode(const void* Q, const void* K_cache, const void* V_cache, const f
   a.scale_log2 = scale * 1.4426950408889634f;
   if (!std::isfinite(a.scale_log2)) return ATTN_ERR_INVALID_ARG;
   char* ws = static_cast<char*>(workspace);
-  a.meta = reinterpret_cast<int*>(ws);
-  a.part_ml = reinterpret_cast<float*>(ws + decode_meta_bytes());
-  a.part_o = reinterpret_cast<float*>(ws + decode_meta_bytes() + decode_ml_bytes());
+  a.arrivals = reinterpret_cast<unsigned long long*>(ws);
+  a.tag = next_tag();
+  a.part_ml = reinterpret_cast<float*>(ws + decode_arrival_bytes());
+  a.part_o = reinterpret_cast<float*>(ws + decode_arrival_bytes() + decode_ml_bytes());
   a.err = error_word_ptr();
   if (!a.err) return ATTN_ERR_CUDA;
   return launch_status(launch_decode(a, (cudaStream_t)stream));
