@@ -122,16 +122,6 @@ __device__ __forceinline__ float keys_sum(float x) {
   return x + __shfl_xor_sync(0xffffffffu, x, 16);
 }
 
-// Query heads of a key head, cut into blocks of at most kDecodeHeads.
-struct HeadSplit {
-  int blocks;  // per key head
-  int heads;   // per block (the last may have fewer)
-};
-__host__ __device__ inline HeadSplit split_heads(int group) {
-  const int nb = (group + kDecodeHeads - 1) / kDecodeHeads;
-  return {nb, (group + nb - 1) / nb};
-}
-
 // The blocks that share a head block count their arrivals in a word of the
 // workspace: the call's tag (48 bits) and the count.  open_count, which every
 // one of them runs before its work, makes the word the call's own: what an
@@ -154,10 +144,48 @@ __device__ __forceinline__ bool arrive(unsigned long long* word, unsigned long l
   return last;
 }
 
-// A head block that this block has a part of: see join_parts.
+// Partial results to be joined: part 0 lies in slot0, part k >= 1 in the first
+// slot of share share1 + (k - 1) stride.
+struct Parts {
+  int slot0, share1, stride, parts;
+  __device__ __forceinline__ int slot(int k) const {
+    return k == 0 ? slot0 : 2 * (share1 + (k - 1) * stride);
+  }
+};
+
+// More than kDirect parts of a head block are joined in two steps: first those
+// of each kGroup consecutive shares (share / kGroup), into the slot of the
+// first of them, then those results.  One block alone would read hundreds of
+// parts for longer than it computed.
+constexpr int kDirect = 32, kGroup = 16;
+
+// A head block that this block has a part of, with shares i0 .. i1.
 struct Piece {
-  int i0, parts, slot0, heads;
-  int64_t out;
+  int i0, i1, slot0, heads;
+  int64_t out;  // its first output row
+  __device__ __forceinline__ bool direct() const { return i1 - i0 < kDirect; }
+  // The parts joined together with share i's.
+  __device__ __forceinline__ Parts group(int i) const {
+    const int g = i / kGroup * kGroup;
+    const int from = direct() || g < i0 ? i0 : g;
+    const int to = direct() || g + kGroup - 1 > i1 ? i1 : g + kGroup - 1;
+    return {from == i0 ? slot0 : 2 * from, from + 1, 1, to - from + 1};
+  }
+  // The groups' results.
+  __device__ __forceinline__ Parts groups() const {
+    const int g = i0 / kGroup;
+    return {slot0, (g + 1) * kGroup, kGroup, i1 / kGroup - g + 1};
+  }
+};
+
+// A run of units of one head block, and where it stands.  Kept in shared
+// memory while the keys are walked, whose loop needs the registers.
+struct Work {
+  int64_t left;        // units of the block's share from this run's first on
+  int64_t first_unit;  // the head block's first unit among all units
+  int b, h, u, n;      // sequence, head block, first unit of the run, units of the head block
+  int lo, len;         // visible positions of the sequence
+  __device__ __forceinline__ int units() const { return int(left < n - u ? left : n - u); }
 };
 
 // Units of sequence b, and its visible positions.
@@ -516,115 +544,101 @@ struct Warp {
   }
 };
 
-// The parts of one head block joined: part 0 in slot0, part k of share i0 + k
-// in that share's first slot; out = index of the head block's first output
-// row.  A warp takes HP heads at a time (two or four warps share a head when
-// there are fewer heads than warps), 16 rows of parts in flight, the first of
-// them ahead of the maximum that weights them; added in a fixed order.
-template <int D, int HP>
-__device__ __forceinline__ void join_parts(const DecodeArgs& a, const Piece& pc, float (*sh)[D]) {
-  constexpr int kCols = D / 32;      // output columns of a lane
-  constexpr int kFlight = 16 / HP;   // parts of a batch
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int share = HP > 1 || pc.heads >= 3 ? 1 : (pc.heads == 2 ? 2 : 4);  // warps per head
-  const int first = warp % share;
-  const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
-  for (int h0 = 0; h0 < pc.heads; h0 += kWarps * HP / share) {
-    const int head = h0 + warp / share * HP;
-    auto at = [&](int k, int x) {
-      return int64_t(k == 0 ? pc.slot0 : 2 * (pc.i0 + k)) * kDecodeHeads + head + x;
-    };
-    float acc[HP][kCols], M[HP], sum[HP], ref[HP];
-    bool live[HP];
+// Joining the parts of a head block, all threads of the block together.  With
+// four warps on the SM and nothing to hide them, what counts is how many reads
+// follow one another: all heads' maxima and sums are one, then IT x KP rows of
+// every thread.  w: the weights, kDecodeHeads x kPartsStride of shared memory.
+// `out` < 0: the result is a part of the second step, in slot ps.slot0, its
+// maximum and sum in an array of their own.
+constexpr int kPartsStride = 40;  // at least the parts of one join, a multiple of 8
+
+__device__ __forceinline__ void join_weights(const DecodeArgs& a, const Parts& ps, int heads,
+                                             int64_t out, float* w) {
+  constexpr int kLanes = kThreads / kDecodeHeads, kEach = kPartsStride / kLanes;
+  const float2* ml = reinterpret_cast<const float2*>(ps.stride == 1 ? a.part_ml : a.part_ml2);
+  const int head = min(int(threadIdx.x) / kLanes, heads - 1), lane = threadIdx.x % kLanes;
+  const int last = ps.parts - 1;
+  float2 x[kEach];
+  float M = -INFINITY, sum = 0.f;
 #pragma unroll
-    for (int x = 0; x < HP; ++x) {
-      live[x] = head + x < pc.heads;
-      M[x] = -INFINITY;
-      sum[x] = ref[x] = 0.f;
+  for (int i = 0; i < kEach; ++i)
+    x[i] = __ldcg(ml + ps.slot(min(lane + kLanes * i, last)) * kDecodeHeads + head);
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) acc[x][c] = 0.f;
-    }
-    for (int k0 = first * kFlight; k0 < pc.parts || k0 == first * kFlight; k0 += kFlight * share) {
-      float o[HP][kFlight][kCols];
-      float2 mine[HP];  // lane j: maximum and sum of part k0 + j
+  for (int i = 0; i < kEach; ++i) M = fmaxf(M, x[i].x);
 #pragma unroll
-      for (int x = 0; x < HP; ++x) {
-        mine[x] = make_float2(-INFINITY, 0.f);
-        if (live[x] && lane < kFlight && k0 + lane < pc.parts) mine[x] = __ldcg(ml + at(k0 + lane, x));
+  for (int s = kLanes / 2; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+  const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
-        for (int j = 0; j < kFlight; ++j) {
+  for (int i = 0; i < kEach; ++i) {
+    x[i].x = lane + kLanes * i <= last ? ex2(x[i].x - ref) : 0.f;
+    sum += x[i].x == 0.f ? 0.f : x[i].x * x[i].y;
+  }
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) o[x][j][c] = 0.f;
-          if (!live[x] || k0 + j >= pc.parts) continue;
-          const float* src = a.part_o + at(k0 + j, x) * D + lane * kCols;
-          if (kCols == 4) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-            o[x][j][0] = v.x;
-            o[x][j][1] = v.y;
-            o[x][j][kCols - 2] = v.z;
-            o[x][j][kCols - 1] = v.w;
-          } else {
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-            o[x][j][0] = v.x;
-            o[x][j][1] = v.y;
-          }
-        }
-      }
-      if (k0 == first * kFlight) {
+  for (int s = kLanes / 2; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+  const float unit = out < 0 ? 1.f : (sum == 0.f ? 0.f : 1.f / sum);
 #pragma unroll
-        for (int x = 0; x < HP; ++x) {
-          if (live[x])
-            for (int k = lane; k < pc.parts; k += 32) M[x] = fmaxf(M[x], __ldcg(ml + at(k, x)).x);
+  for (int i = 0; i < kEach; ++i) w[head * kPartsStride + lane + kLanes * i] = x[i].x * unit;
+  if (lane == 0) {
+    if (out >= 0)
+      a.lse[out + head] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
+    else
+      reinterpret_cast<float2*>(a.part_ml2)[ps.slot0 * kDecodeHeads + head] = make_float2(M, sum);
+  }
+}
+
+template <int D, int IT, int KP>
+__device__ __forceinline__ void join_rows(const DecodeArgs& a, const Parts& ps, int heads,
+                                          int64_t out, const float* w) {
+  const int items = heads * (D / 4), last = ps.parts - 1;
+#pragma unroll 1
+  for (int i0 = threadIdx.x; i0 < items; i0 += IT * kThreads) {
+    float4 acc[IT];
 #pragma unroll
-          for (int s = 16; s > 0; s >>= 1)
-            M[x] = fmaxf(M[x], __shfl_xor_sync(0xffffffffu, M[x], s));
-          ref[x] = M[x] == -INFINITY ? 0.f : M[x];
-        }
+    for (int n = 0; n < IT; ++n) acc[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int k0 = 0; k0 <= last; k0 += KP) {
+      float4 v[KP][IT];
+#pragma unroll
+      for (int j = 0; j < KP; ++j) {
+        const float* src = a.part_o + ps.slot(min(k0 + j, last)) * (kDecodeHeads * D);
+#pragma unroll
+        for (int n = 0; n < IT; ++n)
+          v[j][n] = __ldcg(reinterpret_cast<const float4*>(src) + min(i0 + n * kThreads, items - 1));
       }
 #pragma unroll
-      for (int x = 0; x < HP; ++x) {
-        const float e = ex2(mine[x].x - ref[x]);
-        sum[x] += e * mine[x].y;
+      for (int j = 0; j < KP; ++j)  // parts past the last have weight 0
 #pragma unroll
-        for (int j = 0; j < kFlight; ++j) {
-          const float w = __shfl_sync(0xffffffffu, e, j);
-#pragma unroll
-          for (int c = 0; c < kCols; ++c) acc[x][c] += w * o[x][j][c];
+        for (int n = 0; n < IT; ++n) {
+          const float e = w[min(i0 + n * kThreads, items - 1) / (D / 4) * kPartsStride + k0 + j];
+          acc[n].x += e * v[j][n].x;
+          acc[n].y += e * v[j][n].y;
+          acc[n].z += e * v[j][n].z;
+          acc[n].w += e * v[j][n].w;
         }
-      }
     }
 #pragma unroll
-    for (int x = 0; x < HP; ++x)
-#pragma unroll
-      for (int s = kFlight / 2; s > 0; s >>= 1)
-        sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], s);
-    if (HP == 1 && share > 1) {  // one round of the loop: every head has its warps
-#pragma unroll
-      for (int c = 0; c < kCols; ++c) sh[warp][lane * kCols + c] = acc[0][c];
-      if (lane == 0) sh[kWarps][warp] = sum[0];
-      __syncthreads();
-      if (first) continue;
-      for (int w = 1; w < share; ++w) {
-        sum[0] += sh[kWarps][warp + w];
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) acc[0][c] += sh[warp + w][lane * kCols + c];
-      }
-    }
-#pragma unroll
-    for (int x = 0; x < HP; ++x) {
-      if (!live[x]) continue;
-      const int64_t row = pc.out + head + x;
-      // lanes of kFlight or more hold no part: the sum is lane 0's
-      const float total = __shfl_sync(0xffffffffu, sum[x], 0);
-      const float inv = total == 0.f ? 0.f : 1.f / total;
-      uint32_t* dst =
-          reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + row * D + lane * kCols);
-#pragma unroll
-      for (int c = 0; c < kCols; c += 2)
-        dst[c / 2] = pack_bf16x2(acc[x][c] * inv, acc[x][c + 1] * inv);
-      if (lane == 0) a.lse[row] = total == 0.f ? -INFINITY : (M[x] + log2f(total)) * kLn2;
+    for (int n = 0; n < IT; ++n) {
+      const int i = i0 + n * kThreads;
+      if (i >= items) continue;
+      if (out >= 0)
+        reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + out * D)[i] =
+            make_uint2(pack_bf16x2(acc[n].x, acc[n].y), pack_bf16x2(acc[n].z, acc[n].w));
+      else
+        reinterpret_cast<float4*>(a.part_o + ps.slot0 * (kDecodeHeads * D))[i] = acc[n];
     }
   }
+}
+
+template <int D>
+__device__ __forceinline__ void join_parts(const DecodeArgs& a, const Parts& ps, int heads,
+                                           int64_t out, float* w) {
+  join_weights(a, ps, heads, out, w);
+  __syncthreads();
+  if (heads * (D / 4) <= kThreads)
+    join_rows<D, 1, 20>(a, ps, heads, out, w);
+  else
+    join_rows<D, 4, 8>(a, ps, heads, out, w);
+  __syncthreads();
 }
 
 template <int D, bool FP8, int NG>
@@ -635,14 +649,12 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
   __shared__ float sh_o[kWarps][NG * 8][kHeadStride];
   __shared__ float sh_ml[kWarps][NG * 8][2];
   __shared__ int64_t sh_scan[kWarps];
-  __shared__ int64_t sh_prefix;
-  __shared__ int sh_b;
+  __shared__ int64_t sh_W;
+  __shared__ Work sh_work[2];
   __shared__ bool sh_last[2];
   __shared__ Piece sh_piece[2];
 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const HeadSplit split = split_heads(a.Hq / a.c.Hkv);
-  const int Hn = a.c.Hkv * split.blocks;  // head blocks of a sequence
   grid_dep_wait();
   grid_dep_launch();
 
@@ -671,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
     if (w < warp) scan += sh_scan[w];
     total += sh_scan[w];
   }
-  const int64_t W = total * Hn;
+  const int64_t W = total * a.head_blocks;
   const int G = int(W < int64_t(gridDim.x) ? W : int64_t(gridDim.x));
 
   // Sequences with nothing to see.
@@ -684,81 +696,85 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
   }
 
   if (int(blockIdx.x) >= G) return;
-  const int64_t w0 = split_begin(blockIdx.x, W, G);
-  int64_t left = split_begin(blockIdx.x + 1, W, G) - w0;
-  int64_t at_unit = w0;  // first unit of the current piece
 
-  // The sequence that holds unit w0: its thread's part holds it.
+  // The sequence that holds the share's first unit: its thread's part of the
+  // batch holds it.
   {
-    const int64_t first = (scan - mine) * Hn;
-    if (w0 >= first && w0 < scan * Hn) {
+    const int64_t w0 = split_begin(blockIdx.x, W, G);
+    if (w0 >= (scan - mine) * a.head_blocks && w0 < scan * a.head_blocks) {
+      Work w;
       int64_t prefix = scan - mine;
-      int b = b_begin;
-      for (;; ++b) {
-        int lo, len;
-        const int n = sequence_units<U>(a, b, &lo, &len);
-        if (w0 < (prefix + n) * Hn) break;
-        prefix += n;
+      for (w.b = b_begin;; ++w.b) {
+        w.n = sequence_units<U>(a, w.b, &w.lo, &w.len);
+        if (w0 < (prefix + w.n) * a.head_blocks) break;
+        prefix += w.n;
       }
-      sh_b = b;
-      sh_prefix = prefix;
+      const int64_t x = w0 - prefix * a.head_blocks;
+      w.h = int(x / w.n);
+      w.u = int(x - int64_t(w.h) * w.n);
+      w.first_unit = w0 - w.u;
+      w.left = split_begin(blockIdx.x + 1, W, G) - w0;
+      sh_work[0] = w;
+      sh_W = W;
     }
   }
   __syncthreads();
-  int b = sh_b, lo, len;
-  int n = sequence_units<U>(a, b, &lo, &len);
-  int h, u;
-  {
-    const int64_t x = w0 - sh_prefix * Hn;
-    h = int(x / n);
-    u = int(x - int64_t(h) * n);
-  }
+
   Warp<D, FP8, NG> wp(a);
-  const int group = a.Hq / a.c.Hkv;
-  bool first_segment = true;
-  int pieces = 0;
-  // The piece of head block (b, h) from unit u on: where it lies, and its
-  // first loads.
-  int units, heads, tile;
-  int64_t out, rows;
-  auto enter = [&] {
-    units = int(left < n - u ? left : n - u);
-    const int kvh = h / split.blocks, hb = h % split.blocks;
-    const int hq0 = kvh * group + hb * split.heads;
-    heads = min(split.heads, group - hb * split.heads);
-    out = int64_t(b) * a.Hq + hq0;
-    tile = (lo & ~(kPageQuantum - 1)) + u * U + warp * C::KT * 16;
-    rows = wp.find(a.c.table + int64_t(b) * a.c.max_pages, kvh, tile, len);
-    wp.load_q(b, hq0, heads);
+  int64_t rows;
+  // A run's first loads.
+  auto heads_of = [&](int h) {
+    return min(a.block_heads, a.group - h % a.group_blocks * a.block_heads);
+  };
+  auto first_head = [&](int h) {
+    return h / a.group_blocks * a.group + h % a.group_blocks * a.block_heads;
+  };
+  auto first_tile = [&](const Work& w) {
+    return (w.lo & ~(kPageQuantum - 1)) + w.u * U + warp * C::KT * 16;
+  };
+  auto enter = [&](const Work& w) {
+    rows = wp.find(a.c.table + int64_t(w.b) * a.c.max_pages, w.h / a.group_blocks, first_tile(w),
+                   w.len);
+    wp.load_q(w.b, first_head(w.h), heads_of(w.h));
     wp.load_k(rows);
     wp.load_v(rows);
   };
-  enter();
-  while (true) {
-    const bool whole = u == 0 && units == n;
-    const int64_t first_unit = at_unit - u;  // of the head block
-    const int i0 = whole ? int(blockIdx.x) : split_owner(first_unit, W, G);
-    if (!whole && tid == 0) open_count(a.arrivals + i0, a.tag);
-    wp.begin();
+  enter(sh_work[0]);
+  int pieces = 0;
+  for (int turn = 0;; ++turn) {
     {
-      const int* table = a.c.table + int64_t(b) * a.c.max_pages;
-      const int kvh = h / split.blocks;
-      bool full = wp.full(rows, tile, lo, len);
+    const Work w = sh_work[turn & 1];
+    const int units = w.units();
+      if (tid == 0 && units != w.n) {
+        const int64_t W = sh_W;
+        const int G = int(W < int64_t(gridDim.x) ? W : int64_t(gridDim.x));
+        const int i0 = split_owner(w.first_unit, W, G);
+        const Piece pc = {i0, split_owner(w.first_unit + w.n - 1, W, G),
+                          // the first share may have come here after another head block
+                          2 * i0 + (split_begin(i0, W, G) < w.first_unit ? 1 : 0), heads_of(w.h),
+                          int64_t(w.b) * a.Hq + first_head(w.h)};
+        sh_piece[pieces] = pc;
+        open_count(a.arrivals + pc.group(blockIdx.x).slot0, a.tag);
+        if (!pc.direct()) open_count(a.arrivals2 + pc.slot0, a.tag);
+      }
+      wp.begin();
+      const int* table = a.c.table + int64_t(w.b) * a.c.max_pages;
+      const int kvh = w.h / a.group_blocks;
+      int tile = first_tile(w);
+      bool full = wp.full(rows, tile, w.lo, w.len);
       // The last step stands apart: it has nothing to load.
       for (int i = 1; i < units; ++i) {
-        const int64_t next_rows = wp.find(table, kvh, tile + U, len);
-        wp.template step<true>(rows, full, tile, lo, len, next_rows);
+        const int64_t next_rows = wp.find(table, kvh, tile + U, w.len);
+        wp.template step<true>(rows, full, tile, w.lo, w.len, next_rows);
         tile += U;
         rows = next_rows;
-        full = wp.full(rows, tile, lo, len);
+        full = wp.full(rows, tile, w.lo, w.len);
       }
-      wp.template step<false>(rows, full, tile, lo, len, 0);
+      wp.template step<false>(rows, full, tile, w.lo, w.len, 0);
     }
 
-    // The piece's results leave the registers; the next piece's first loads
-    // are under way while they are joined.
-    const int done_heads = heads, done_n = n;
-    const int64_t done_out = out;
+    // The run's results leave the registers; the next run's first loads are
+    // under way while they are joined.
 #pragma unroll
     for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -774,20 +790,32 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
           *reinterpret_cast<float2*>(&sh_o[warp][head][wp.column(i)]) =
               make_float2(wp.acc[g][i][y] * wp.unit(), wp.acc[g][i][2 + y] * wp.unit());
       }
-    left -= units;
-    at_unit += units;
-    if (left) {
-      u = 0;
-      if (++h == Hn) {
-        h = 0;
-        do n = sequence_units<U>(a, ++b, &lo, &len);
-        while (n == 0);
-      }
-      enter();
-    }
     __syncthreads();
-    const int slot = 2 * blockIdx.x + (first_segment ? 0 : 1);
-    for (int i = tid; i < done_heads * (D / 2); i += kThreads) {
+    const volatile Work& seen = sh_work[turn & 1];
+    const int units = int(seen.left < seen.n - seen.u ? seen.left : seen.n - seen.u);
+    const bool whole = units == seen.n, more = seen.left > units;
+    if (more) {
+      Work w;
+      w.left = seen.left - units;
+      w.first_unit = seen.first_unit + seen.n;
+      w.u = 0;
+      w.b = seen.b;
+      w.h = seen.h + 1;
+      w.n = seen.n;
+      w.lo = seen.lo;
+      w.len = seen.len;
+      if (w.h == a.head_blocks) {
+        w.h = 0;
+        do w.n = sequence_units<U>(a, ++w.b, &w.lo, &w.len);
+        while (w.n == 0);
+      }
+      if (tid == 0) sh_work[(turn & 1) ^ 1] = w;
+      enter(w);
+    }
+    const int heads = heads_of(seen.h);
+    const int64_t out = int64_t(seen.b) * a.Hq + first_head(seen.h);
+    const int slot = 2 * blockIdx.x + (turn ? 1 : 0);
+    for (int i = tid; i < heads * (D / 2); i += kThreads) {
       const int head = i / (D / 2), c = 2 * (i % (D / 2));
       float M = -INFINITY;
 #pragma unroll
@@ -802,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
         o1 += e * sh_o[w][head][c + 1];
       }
       if (whole) {
-        const int64_t row = done_out + head;
+        const int64_t row = out + head;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + row * D + c) =
             pack_bf16x2(o0 * inv, o1 * inv);
@@ -813,37 +841,42 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
         if (c == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(M, sum);
       }
     }
-    if (!whole) {  // at most twice: a share's first and last head block
-      if (tid == 0)
-        sh_piece[pieces] = {i0, split_owner(first_unit + done_n - 1, W, G) - i0 + 1,
-                            // the first share may have come here after another head block
-                            2 * i0 + (split_begin(i0, W, G) < first_unit ? 1 : 0), done_heads,
-                            done_out};
-      ++pieces;
-    }
-    __syncthreads();  // the shared tiles are free again, the parts are written
-    if (left == 0) break;
-    first_segment = false;
+    if (!whole) ++pieces;  // at most twice: a share's first and last head block
+    __syncthreads();       // the shared tiles are free again, the parts are written
+    if (!more) break;
   }
 
-  // Both pieces' arrivals at once, after one fence.
-  if (pieces == 0) return;
-  if (tid < pieces) {
-    fence_acq_rel_gpu();
-    sh_last[tid] = arrive(a.arrivals + sh_piece[tid].i0, a.tag, sh_piece[tid].parts);
-    fence_acq_rel_gpu();
-  }
-  __syncthreads();
-  for (int x = 0; x < pieces; ++x)
-    if (sh_last[x]) {
-      const Piece pc = sh_piece[x];
-      float(*sh)[D] = reinterpret_cast<float(*)[D]>(&sh_o[0][0][0]);
-      if (pc.heads > kWarps)
-        join_parts<D, 2>(a, pc, sh);
-      else
-        join_parts<D, 1>(a, pc, sh);
-      __syncthreads();
+  // Both pieces' arrivals at once, after one fence; then the second step of
+  // those that take two.
+  bool waits = tid < pieces;  // this thread has an arrival to make
+#pragma unroll 1
+  for (int step = 0; pieces; ++step) {
+    if (tid < 2) {
+      bool last = false;
+      if (waits) {
+        const Piece pc = sh_piece[tid];
+        fence_acq_rel_gpu();
+        last = step ? arrive(a.arrivals2 + pc.slot0, a.tag, pc.groups().parts)
+                    : arrive(a.arrivals + pc.group(blockIdx.x).slot0, a.tag,
+                             pc.group(blockIdx.x).parts);
+        fence_acq_rel_gpu();
+        waits = last && step == 0 && !pc.direct();
+      }
+      sh_last[tid] = last;
     }
+    __syncthreads();
+    bool again = false;
+#pragma unroll 1
+    for (int x = 0; x < pieces; ++x) {
+      if (!sh_last[x]) continue;
+      const Piece pc = sh_piece[x];
+      const bool whole = step || pc.direct();
+      again |= !whole;
+      join_parts<D>(a, step ? pc.groups() : pc.group(blockIdx.x), pc.heads, whole ? pc.out : -1,
+                    &sh_o[0][0][0]);
+    }
+    if (!again) break;
+  }
 }
 
 template <int D, bool FP8, int NG>
@@ -851,9 +884,8 @@ cudaError_t launch(const DecodeArgs& a, cudaStream_t stream) {
   using C = Cfg<D, FP8>;
   constexpr int kPerSm = NG == 1 ? 3 : 2;  // resident blocks: see __launch_bounds__
   // at most as many blocks as there can be units
-  const HeadSplit split = split_heads(a.Hq / a.c.Hkv);
   const int seen = a.window > 0 && a.window < a.c.capacity ? a.window : a.c.capacity;
-  const int64_t units = int64_t(a.c.B) * a.c.Hkv * split.blocks * (seen / C::kUnit + 2);
+  const int64_t units = int64_t(a.c.B) * a.head_blocks * (seen / C::kUnit + 2);
   int64_t grid = int64_t(device_sm_count()) * kPerSm;
   if (grid > kDecodeMaxBlocks) grid = kDecodeMaxBlocks;
   if (grid > units) grid = units;
@@ -863,13 +895,17 @@ cudaError_t launch(const DecodeArgs& a, cudaStream_t stream) {
 
 template <int D, bool FP8>
 cudaError_t launch_heads(const DecodeArgs& a, cudaStream_t stream) {
-  const int heads = split_heads(a.Hq / a.c.Hkv).heads;
-  return heads <= 8 ? launch<D, FP8, 1>(a, stream) : launch<D, FP8, 2>(a, stream);
+  return a.block_heads <= 8 ? launch<D, FP8, 1>(a, stream) : launch<D, FP8, 2>(a, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
+cudaError_t launch_decode(const DecodeArgs& args, cudaStream_t stream) {
+  DecodeArgs a = args;
+  a.group = a.Hq / a.c.Hkv;
+  a.group_blocks = (a.group + kDecodeHeads - 1) / kDecodeHeads;
+  a.block_heads = (a.group + a.group_blocks - 1) / a.group_blocks;
+  a.head_blocks = a.c.Hkv * a.group_blocks;
   if (a.c.d == 64)
     return a.c.kd ? launch_heads<64, true>(a, stream) : launch_heads<64, false>(a, stream);
   return a.c.kd ? launch_heads<128, true>(a, stream) : launch_heads<128, false>(a, stream);

@@ -77,9 +77,13 @@ struct DecodeArgs {
   int Hq;
   int window;
   float scale_log2;      // scale * log2(e)
-  unsigned long long* arrivals;  // workspace: a word per thread block, see arrive()
+  // set by launch_decode: the query heads of a key head, cut into blocks of at
+  // most kDecodeHeads (the last may have fewer)
+  int group, group_blocks, block_heads;
+  int head_blocks;       // of a sequence
+  unsigned long long *arrivals, *arrivals2;  // workspace: a word per slot each, see arrive()
   unsigned long long tag;        // 48 bits, another one for every call
-  float* part_ml;        // workspace: [2 * blocks][16][2] running maximum and sum
+  float *part_ml, *part_ml2;  // workspace: [2 * blocks][16][2] running maximum and sum
   float* part_o;         // workspace: [2 * blocks][16][d] unnormalised output
   int* err;
 };
@@ -87,7 +91,7 @@ struct DecodeArgs {
 constexpr int kDecodeMaxBlocks = 608;
 constexpr int kDecodeHeads = 16;  // heads of one key/value head a block works on at most
 inline size_t decode_arrival_bytes() {
-  return (sizeof(unsigned long long) * kDecodeMaxBlocks + 255) / 256 * 256;
+  return sizeof(unsigned long long) * 2 * size_t(kDecodeMaxBlocks);  // one of the two arrays
 }
 inline size_t decode_ml_bytes() {
   return sizeof(float) * 2 * kDecodeHeads * 2 * size_t(kDecodeMaxBlocks);

@@ -199,7 +199,7 @@ int kv_cache_read(const void* K_cache, const void* V_cache, const float* k_desca
 
 size_t attn_decode_workspace_size(int d) {
   if (d != 64 && d != 128) return 0;
-  return decode_arrival_bytes() + decode_ml_bytes() + decode_o_bytes(d);
+  return 2 * decode_arrival_bytes() + 2 * decode_ml_bytes() + decode_o_bytes(d);
 }
 
 int attn_decode(const void* Q, const void* K_cache, const void* V_cache, const float* k_descale,
@@ -231,9 +231,11 @@ int attn_decode(const void* Q, const void* K_cache, const void* V_cache, const f
   if (!std::isfinite(a.scale_log2)) return ATTN_ERR_INVALID_ARG;
   char* ws = static_cast<char*>(workspace);
   a.arrivals = reinterpret_cast<unsigned long long*>(ws);
+  a.arrivals2 = reinterpret_cast<unsigned long long*>(ws + decode_arrival_bytes());
   a.tag = next_tag();
-  a.part_ml = reinterpret_cast<float*>(ws + decode_arrival_bytes());
-  a.part_o = reinterpret_cast<float*>(ws + decode_arrival_bytes() + decode_ml_bytes());
+  a.part_ml = reinterpret_cast<float*>(ws + 2 * decode_arrival_bytes());
+  a.part_ml2 = reinterpret_cast<float*>(ws + 2 * decode_arrival_bytes() + decode_ml_bytes());
+  a.part_o = reinterpret_cast<float*>(ws + 2 * decode_arrival_bytes() + 2 * decode_ml_bytes());
   a.err = error_word_ptr();
   if (!a.err) return ATTN_ERR_CUDA;
   return launch_status(launch_decode(a, (cudaStream_t)stream));

@@ -129,6 +129,22 @@ def test_decode_split_over_a_long_sequence(fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("Hkv,group,d,lens", [
+    (1, 1, 64, [9000]), (1, 1, 128, [6000, 0, 2500]), (1, 2, 128, [5000]), (2, 2, 64, [9001, 70]),
+    (1, 3, 64, [7777]), (1, 6, 128, [5003]), (1, 13, 128, [3001, 5]), (3, 4, 128, [3500])])
+def test_decode_many_parts(Hkv, group, d, lens, fp8):
+    """Few heads and long sequences: dozens of blocks share a head, and their
+    parts are joined in two steps."""
+    c = filled_cache(lens, 32, Hkv, d, 60 + group, fp8)
+    q = make_tensor((len(lens), Hkv * group, 1, d), 61 + group, std=2.0)
+    o, lse = run(q, c, lens)
+    check(o, lse, serving.decode(q, c["k64"], c["v64"], c["table"], lens, 1 / math.sqrt(d)), d)
+    for _ in range(3):
+        o2, lse2 = run(q, c, lens)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_decode_large_scores(fp8):
     """Scores of several hundred, one key far above the rest, and factors of
     very different sizes: nothing overflows."""
