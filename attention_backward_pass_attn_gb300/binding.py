@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 import os
 import threading
 
@@ -415,13 +416,14 @@ def ssd_bwd(x, dt, A, B, C, D, dy, workspace=None, out=None, stream=None):
 # ------------------------------------------------------------------ the answering path
 # Rotary positions, the paged key/value cache, attention of one new token.
 # Tensors must live on the current CUDA device, whose current stream the calls
-# run on unless ``stream`` names another.
+# run on unless ``stream`` names another; what a call allocates belongs to the
+# stream it runs on.
 # The checks come first as one cheap test; only what fails it is looked at for
 # the reason, so that a call of a few microseconds on the GPU is not drowned by
 # its checks.
 _E4M3_DTYPES = (torch.float8_e4m3fn, torch.uint8)
-_I64x6 = ctypes.c_int64 * 6
-_SECTIONS = {n: ctypes.c_int * n for n in range(1, 5)}
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _device_index(t: torch.Tensor, name: str) -> int:
@@ -431,7 +433,7 @@ def _device_index(t: torch.Tensor, name: str) -> int:
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
     dev = t.get_device()
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         raise ValueError("%s must be on the current CUDA device" % name)
     return dev
 
@@ -439,10 +441,36 @@ def _device_index(t: torch.Tensor, name: str) -> int:
 def _stream_on(stream, dev: int) -> int:
     """The CUDA stream handle of ``stream``, or of device dev's current one."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return _current_stream(dev)
     if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
         raise ValueError("stream must be on CUDA device %d, like the first tensor" % dev)
     return _stream(stream)
+
+
+def _empty(shape, dtype, dev: int, stream) -> torch.Tensor:
+    """Uninitialised memory of the stream the call runs on: on another than
+    the current one, the allocator must not hand it to the current one when it
+    is freed."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+# ctypes arrays of strides and section counts by their values: making one
+# costs more than the rest of a call's checks.
+_arrays = {}
+
+
+def _array(ctype, values: tuple):
+    got = _arrays.get((ctype, values))
+    if got is None:
+        if len(_arrays) >= 4096:
+            _arrays.clear()
+        got = _arrays[(ctype, values)] = (ctype * len(values))(*values)
+    return got
 
 
 def _check_like(t: torch.Tensor, name: str, shape, dtype, dev: int):
@@ -467,12 +495,12 @@ def _check_rows(t: torch.Tensor, name: str, shape, dev: int):
     16-byte strides; returns its three element strides."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if t.get_device() != dev:
-        raise ValueError("%s must be on CUDA device %d, like the first tensor" % (name, dev))
-    if t.dtype is not torch.bfloat16:
-        raise ValueError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.dtype is not torch.bfloat16:
+        raise ValueError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
+    if t.get_device() != dev:
+        raise ValueError("%s must be on CUDA device %d, like the first tensor" % (name, dev))
     sb, sh, sn, sd = t.stride()
     if sd != 1 and shape[3] > 1:
         raise ValueError("%s must be contiguous in its head dimension" % name)
@@ -516,13 +544,13 @@ def _ptr(t):
 
 def _rope(fn, q, k, pos, inv_freq, sections, interleaved, out, stream):
     dev = _device_index(q, "q")
-    shape = _shape4(q, "q")
+    shape = q.shape if q.dim() == 4 else _shape4(q, "q")
     B, H, N, d = shape
     strides = _check_rows(q, "q", shape, dev)
     if k is None:
         Hk, strides = 0, strides + (0, 0, 0)
     else:
-        Hk = _shape4(k, "k")[1]
+        Hk = (k.shape if k.dim() == 4 else _shape4(k, "k"))[1]
         strides += _check_rows(k, "k", (B, Hk, N, d), dev)
     pshape = pos.shape
     if len(pshape) != 3 or (pshape[1] != B and pshape[1] != 1) or pshape[2] != N:
@@ -530,30 +558,35 @@ def _rope(fn, q, k, pos, inv_freq, sections, interleaved, out, stream):
     axes = pshape[0]
     _check_like(pos, "pos", pshape, torch.int32, dev)
     _check_like(inv_freq, "inv_freq", (d // 2,), torch.float32, dev)
-    if sections is None:
-        sections = (d // 2,)
-    if axes not in _SECTIONS or len(sections) != axes or sum(sections) != d // 2 \
+    sections = (d // 2,) if sections is None else tuple(sections)
+    if not 1 <= axes <= 4 or len(sections) != axes or sum(sections) != d // 2 \
             or min(sections) < 0:
         raise ValueError("sections must be one count for each of pos's 1 to 4 axes that sum to "
-                         "d/2 = %d, got %s for %d" % (d // 2, tuple(sections), axes))
+                         "d/2 = %d, got %s for %d" % (d // 2, sections, axes))
     oq, ok = (None, None) if out is None else out
     if oq is None:
-        oq = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        oq = _empty(shape, torch.bfloat16, dev, stream)
     else:
         _check_like(oq, "out[0]", shape, torch.bfloat16, dev)
     if k is None:
-        ok = None
-    elif ok is None:
-        ok = torch.empty((B, Hk, N, d), dtype=torch.bfloat16, device=q.device)
+        ok, kp, okp = None, None, None
     else:
-        _check_like(ok, "out[1]", (B, Hk, N, d), torch.bfloat16, dev)
-    st = getattr(load_library(), fn)(q.data_ptr(), _ptr(k), pos.data_ptr(), inv_freq.data_ptr(),
-                                     _SECTIONS[axes](*sections), axes, int(bool(interleaved)),
-                                     _I64x6(*strides), oq.data_ptr(), _ptr(ok), B, H, Hk, N, d,
-                                     pshape[1], _stream_on(stream, dev))
+        if ok is None:
+            ok = _empty((B, Hk, N, d), torch.bfloat16, dev, stream)
+        else:
+            _check_like(ok, "out[1]", (B, Hk, N, d), torch.bfloat16, dev)
+        kp, okp = k.data_ptr(), ok.data_ptr()
+    st = fn(load_library())(q.data_ptr(), kp, pos.data_ptr(), inv_freq.data_ptr(),
+                            _array(ctypes.c_int, sections), axes, 1 if interleaved else 0,
+                            _array(ctypes.c_int64, strides), oq.data_ptr(), okp, B, H, Hk, N, d,
+                            pshape[1], _stream_on(stream, dev))
     if st:
-        _check(fn, st)
+        _check("rope", st)
     return oq, ok
+
+
+_ROPE_FWD = operator.attrgetter("rope_fwd")
+_ROPE_BWD = operator.attrgetter("rope_bwd")
 
 
 def rope_fwd(q, k, pos, inv_freq, sections=None, interleaved=False, out=None, stream=None):
@@ -568,13 +601,13 @@ def rope_fwd(q, k, pos, inv_freq, sections=None, interleaved=False, out=None, st
     out: (q', k') to write into, contiguous; may be the inputs themselves when
     those are contiguous.
     """
-    return _rope("rope_fwd", q, k, pos, inv_freq, sections, interleaved, out, stream)
+    return _rope(_ROPE_FWD, q, k, pos, inv_freq, sections, interleaved, out, stream)
 
 
 def rope_bwd(dq, dk, pos, inv_freq, sections=None, interleaved=False, out=None, stream=None):
     """The gradients of rope_fwd's q and k from those of its results (the turn
     by the negative angles); arguments as for rope_fwd."""
-    return _rope("rope_bwd", dq, dk, pos, inv_freq, sections, interleaved, out, stream)
+    return _rope(_ROPE_BWD, dq, dk, pos, inv_freq, sections, interleaved, out, stream)
 
 
 def alloc_kv_cache(num_pages: int, Hkv: int, page_size: int, d: int, device,
@@ -612,11 +645,12 @@ def kv_cache_write(k, v, k_cache, v_cache, page_table, start, count=None, k_desc
     """
     dev = _device_index(k_cache, "k_cache")
     P, Hkv, ps, d, B, mp = _check_cache(k_cache, v_cache, k_descale, v_descale, page_table, dev)
-    T = _shape4(k, "k")[2]
+    T = (k.shape if k.dim() == 4 else _shape4(k, "k"))[2]
     shape = (B, Hkv, T, d)
     strides = _check_rows(k, "k", shape, dev) + _check_rows(v, "v", shape, dev)
     _check_span(start, count, B, dev)
-    st = load_library().kv_cache_write(k.data_ptr(), v.data_ptr(), _I64x6(*strides),
+    st = load_library().kv_cache_write(k.data_ptr(), v.data_ptr(),
+                                       _array(ctypes.c_int64, strides),
                                        k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_descale),
                                        _ptr(v_descale), page_table.data_ptr(), start.data_ptr(),
                                        _ptr(count), B, Hkv, T, d, ps, P, mp,
@@ -635,8 +669,8 @@ def kv_cache_read(k_cache, v_cache, page_table, start, T: int, count=None, k_des
     _check_span(start, count, B, dev)
     shape = (B, Hkv, int(T), d)
     if out is None:
-        k = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
-        v = torch.empty_like(k)
+        k = _empty(shape, torch.bfloat16, dev, stream)
+        v = _empty(shape, torch.bfloat16, dev, stream)
     else:
         k, v = out
         _check_like(k, "out[0]", shape, torch.bfloat16, dev)
@@ -650,16 +684,28 @@ def kv_cache_read(k_cache, v_cache, page_table, start, T: int, count=None, k_des
     return k, v
 
 
-_decode_bytes = {}  # of the workspace, by head dim
-
-
 def alloc_decode_workspace(d: int, device) -> torch.Tensor:
     """The uint8 device buffer attn_decode needs for head dim d, whatever the
     batch; calls that may overlap on the GPU need one each."""
-    n = _decode_bytes.get(d)
-    if n is None:
-        n = _decode_bytes[d] = max(int(load_library().attn_decode_workspace_size(d)), 256)
+    n = max(int(load_library().attn_decode_workspace_size(d)), 256)
     return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+# attn_decode's own workspaces, one for every stream it was called on without
+# one: calls on a stream follow one another.  A call that is being captured
+# gets memory of its graph instead, which may replay on any stream.
+_decode_workspaces = {}
+
+
+def _decode_workspace(dev: int, stream):
+    handle = _stream_on(stream, dev)
+    if stream is not None or torch._C._cuda_isCurrentStreamCapturing():
+        n = int(load_library().attn_decode_workspace_size(128))
+        return _empty((n,), torch.uint8, dev, stream), handle
+    ws = _decode_workspaces.get((dev, handle))
+    if ws is None:
+        ws = _decode_workspaces[(dev, handle)] = alloc_decode_workspace(128, dev)
+    return ws, handle
 
 
 def attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, k_descale=None,
@@ -671,35 +717,40 @@ def attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, k_descale
     lengths with the new token (whose k and v are in the cache already).
     window > 0: only the last ``window`` positions are seen.
     Returns (O bf16 [B, Hq, 1, d], L fp32 [B, Hq, 1]); a sequence of length 0
-    has O = 0 and L = -inf.
+    has O = 0 and L = -inf.  workspace: from alloc_decode_workspace; without
+    one, the call uses one that is kept for its stream.
     """
     dev = _device_index(q, "q")
     P, Hkv, ps, d, B, mp = _check_cache(k_cache, v_cache, k_descale, v_descale, page_table, dev)
-    Hq = _shape4(q, "q")[1]
+    Hq = (q.shape if q.dim() == 4 else _shape4(q, "q"))[1]
     shape = (B, Hq, 1, d)
     _check_like(q, "q", shape, torch.bfloat16, dev)
     if Hkv < 1 or Hq % Hkv:
         raise ValueError("q's %d heads must be a multiple of the cache's %d" % (Hq, Hkv))
     _check_like(seq_lens, "seq_lens", (B,), torch.int32, dev)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(shape, torch.bfloat16, dev, stream)
     else:
         _check_like(out, "out", shape, torch.bfloat16, dev)
     if lse is None:
-        lse = torch.empty((B, Hq, 1), dtype=torch.float32, device=q.device)
+        lse = _empty((B, Hq, 1), torch.float32, dev, stream)
     else:
         _check_like(lse, "lse", (B, Hq, 1), torch.float32, dev)
     if workspace is None:
-        workspace = alloc_decode_workspace(d, q.device)
+        workspace, handle = _decode_workspace(dev, stream)
     elif workspace.get_device() != dev:
         raise ValueError("workspace must be on CUDA device %d, like the first tensor" % dev)
-    st = load_library().attn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                    _ptr(k_descale), _ptr(v_descale), page_table.data_ptr(),
-                                    seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq,
-                                    Hkv, d, ps, P, mp, int(window), _default_scale(d, scale),
-                                    workspace.data_ptr(),
-                                    workspace.numel() * workspace.element_size(),
-                                    _stream_on(stream, dev))
+    else:
+        handle = _stream_on(stream, dev)
+    if k_descale is None:
+        kd = vd = None
+    else:
+        kd, vd = k_descale.data_ptr(), v_descale.data_ptr()
+    st = load_library().attn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kd, vd,
+                                    page_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
+                                    lse.data_ptr(), B, Hq, Hkv, d, ps, P, mp, int(window),
+                                    _default_scale(d, scale), workspace.data_ptr(),
+                                    workspace.nbytes, handle)
     if st:
         _check("attn_decode", st)
     return out, lse
