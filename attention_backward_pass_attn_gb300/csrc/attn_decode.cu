@@ -286,7 +286,7 @@ struct Warp {
   // at key `tile`, or of the last run below len; -1 on a bad page.
   __device__ __forceinline__ int64_t find(const int* table, int kvh, int tile, int len) {
     const int pos = min(tile + 16 * (lane % KT), (len - 1) & ~(kPageQuantum - 1));
-    const int pi = int(unsigned(pos) / unsigned(a.c.page_size));
+    const int pi = int(fast_div(pos, a.c.page_div));
     const int page = __ldg(table + pi);
     if (!page_in_range(page, a.c.num_pages)) {
       report_error(a.err, kDevBadIndex, kSiteDecodePage);

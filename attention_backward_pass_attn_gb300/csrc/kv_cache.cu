@@ -27,23 +27,27 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRows = 2;
 
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 
-// Largest finite magnitude of a row as bf16 bits, over the row's lanes.
-template <int LANES>
-__device__ __forceinline__ uint32_t row_amax_bits(const uint4& x) {
-  uint32_t m = 0;
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    uint32_t mag = w[k] & 0x7FFF7FFFu;
-    if ((mag & 0xFFFFu) >= 0x7F80u) mag &= 0xFFFF0000u;
-    if ((mag >> 16) >= 0x7F80u) mag &= 0x0000FFFFu;
-    m = max_u16x2(m, mag);
-  }
+// Largest magnitude among a lane's 8 values, as bf16 bits; of the finite ones
+// when there are others.
+__device__ __forceinline__ uint32_t amax_bits(const uint4& x) {
+  const uint32_t w[4] = {x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu, x.z & 0x7FFF7FFFu,
+                         x.w & 0x7FFF7FFFu};
+  uint32_t m = max_u16x2(max_u16x2(w[0], w[1]), max_u16x2(w[2], w[3]));
   m = max(m & 0xFFFFu, m >> 16);
+  if (m >= 0x7F80u) {  // an infinity or a NaN
+    m = 0;
 #pragma unroll
-  for (int o = LANES / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o, LANES));
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t lo = w[k] & 0xFFFFu, hi = w[k] >> 16;
+      m = max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+    }
+  }
   return m;
 }
 
@@ -59,9 +63,9 @@ __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) 
 struct Row {
   int b, h, t;
 };
-__device__ __forceinline__ Row row_of(unsigned i, unsigned T, unsigned Hkv) {
-  const unsigned bh = i / T, b = bh / Hkv;
-  return {int(b), int(bh - b * Hkv), int(i - bh * T)};
+__device__ __forceinline__ Row row_of(unsigned i, const CacheArgs& c, const CacheRows& r) {
+  const unsigned bh = fast_div(i, r.T_div), b = fast_div(bh, r.head_div);
+  return {int(b), int(bh - b * c.Hkv), int(i - bh * r.T)};
 }
 
 // Where row w of the call lies in the cache, or -1 (recorded by `lane` 0).
@@ -73,7 +77,7 @@ __device__ __forceinline__ int64_t locate(const CacheArgs& c, const CacheRows& r
     if (lane == 0) report_error(err, kDevBadIndex, kSiteLength);
     return -1;
   }
-  const unsigned p = unsigned(pos), pi = p / unsigned(c.page_size);
+  const unsigned p = unsigned(pos), pi = fast_div(p, c.page_div);
   const int page = __ldg(c.table + int64_t(w.b) * c.max_pages + pi);
   if (!page_in_range(page, c.num_pages)) {
     if (lane == 0) report_error(err, kDevBadIndex, site);
@@ -99,7 +103,7 @@ __global__ void __launch_bounds__(kThreads)
     dst[j] = -1;
     x[j][0] = x[j][1] = make_uint4(0, 0, 0, 0);
     if (i >= rows) continue;
-    const Row w = row_of(i, r.T, c.Hkv);
+    const Row w = row_of(i, c, r);
     dst[j] = locate(c, r, w, kSiteWritePage, lane, err);
     if (dst[j] < 0) continue;
 #pragma unroll
@@ -109,28 +113,37 @@ __global__ void __launch_bounds__(kThreads)
           lane * 8));
   }
 #pragma unroll
-  for (int j = 0; j < R; ++j)
+  for (int j = 0; j < R; ++j) {
+    uint32_t amax = 0;  // K's in the low half, V's in the high one
+    if (FP8) {
+      amax = amax_bits(x[j][0]) | amax_bits(x[j][1]) << 16;
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1)  // all lanes: shuffles
+        amax = max_u16x2(amax, __shfl_xor_sync(0xffffffffu, amax, o, kLanes));
+    }
+    if (dst[j] < 0) continue;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       uint8_t* cache = static_cast<uint8_t*>(s ? c.vc : c.kc);
       if (!FP8) {
-        if (dst[j] >= 0) *reinterpret_cast<uint4*>(cache + (dst[j] * D + lane * 8) * 2) = x[j][s];
+        *reinterpret_cast<uint4*>(cache + (dst[j] * D + lane * 8) * 2) = x[j][s];
         continue;
       }
-      const int e = descale_exponent(row_amax_bits<kLanes>(x[j][s]));  // all lanes: shuffles
-      if (dst[j] < 0) continue;
-      const float inv = pow2f(-e);
-      const uint32_t w4[4] = {x[j][s].x, x[j][s].y, x[j][s].z, x[j][s].w};
-      float f[8];
+      const int e = descale_exponent(s ? amax >> 16 : amax & 0xFFFFu);
+      // 1 / descale as two bf16: x / descale is exact, or below every e4m3
+      // value's half and rounded to zero either way
+      const uint32_t inv = uint32_t(127 - e) << 7 | uint32_t(127 - e) << 23;
+      const uint32_t w[4] = {mul_bf16x2(x[j][s].x, inv), mul_bf16x2(x[j][s].y, inv),
+                             mul_bf16x2(x[j][s].z, inv), mul_bf16x2(x[j][s].w, inv)};
+      uint32_t o[2];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        f[2 * k] = bf16lo_to_f32(w4[k]) * inv;
-        f[2 * k + 1] = bf16hi_to_f32(w4[k]) * inv;
-      }
-      *reinterpret_cast<uint2*>(cache + dst[j] * D + lane * 8) =
-          make_uint2(pack_e4m3x4(f[0], f[1], f[2], f[3]), pack_e4m3x4(f[4], f[5], f[6], f[7]));
+      for (int k = 0; k < 2; ++k)
+        o[k] = pack_e4m3x4(bf16lo_to_f32(w[2 * k]), bf16hi_to_f32(w[2 * k]),
+                           bf16lo_to_f32(w[2 * k + 1]), bf16hi_to_f32(w[2 * k + 1]));
+      *reinterpret_cast<uint2*>(cache + dst[j] * D + lane * 8) = make_uint2(o[0], o[1]);
       if (lane == 0) (s ? c.vd : c.kd)[dst[j]] = pow2f(e);
     }
+  }
 }
 
 // Two e4m3 values (low 16 bits) as floats, exactly.
@@ -156,7 +169,7 @@ __global__ void __launch_bounds__(kThreads)
     x[j][0] = x[j][1] = make_uint4(0, 0, 0, 0);
     f[j][0] = f[j][1] = 0.f;
     if (i >= rows) continue;
-    const int64_t src = locate(c, r, row_of(i, r.T, c.Hkv), kSiteReadPage, lane, err);
+    const int64_t src = locate(c, r, row_of(i, c, r), kSiteReadPage, lane, err);
     if (src < 0) continue;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {

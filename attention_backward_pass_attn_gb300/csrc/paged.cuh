@@ -58,4 +58,22 @@ ATTN_HD int64_t split_begin(int i, int64_t W, int G) { return int64_t(i) * W / G
 // i W / G < x + 1  <=>  i < (x + 1) G / W.
 ATTN_HD int split_owner(int64_t x, int64_t W, int G) { return int(((x + 1) * G - 1) / W); }
 
+// Division of 0 <= n < 2^31 by a fixed d >= 1, as a multiplication: with
+// s = ceil(log2 d) and mul = floor(2^(31 + s) / d) + 1 < 2^32, the product
+// exceeds n 2^(31 + s) / d by less than n <= 2^31, too little to reach the next
+// quotient.  A division by a number that the compiler does not know takes
+// some twenty instructions, this two.
+struct FastDiv {
+  uint32_t mul;    // 0: d = 1
+  uint32_t shift;
+};
+inline FastDiv make_fast_div(uint32_t d) {
+  uint32_t s = 0;
+  while ((uint64_t(1) << s) < d) ++s;
+  return s == 0 ? FastDiv{0, 0} : FastDiv{uint32_t((uint64_t(1) << (31 + s)) / d + 1), s - 1};
+}
+ATTN_HD uint32_t fast_div(uint32_t n, const FastDiv& f) {
+  return f.mul ? uint32_t((uint64_t(n) * f.mul) >> 32) >> f.shift : n;
+}
+
 }  // namespace attn

@@ -8,6 +8,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "paged.cuh"
+
 namespace attn {
 
 // The current device's error word (attn_api.cu); null if it has none.
@@ -39,6 +41,7 @@ struct RopeArgs {
   int axis_end[kMaxAxes];  // first pair index past each axis's pairs
   int axes;
   int B, N, d;
+  FastDiv N_div;  // by N
   int interleaved;
   int backward;
 };
@@ -53,6 +56,7 @@ struct CacheArgs {
   const int* table;  // [B][max_pages]
   int num_pages, Hkv, page_size, d, max_pages, B;
   int capacity;      // max_pages * page_size
+  FastDiv page_div;  // by page_size
 };
 
 // kv_cache.cu.  Rows of k and v: [B][Hkv][T][d], read with element strides
@@ -63,6 +67,7 @@ struct CacheRows {
   const int* start;  // [B]
   const int* count;  // [B] or null = T
   int T;
+  FastDiv T_div, head_div;  // by T and by the cache's Hkv
 };
 cudaError_t launch_kv_write(const CacheArgs& c, const CacheRows& r, int* err, cudaStream_t stream);
 cudaError_t launch_kv_read(const CacheArgs& c, const CacheRows& r, int* err, cudaStream_t stream);

@@ -74,6 +74,7 @@ int rope(const void* Q, const void* K, const int* pos, const float* inv_freq, co
   a.axes = axes;
   a.B = B;
   a.N = N;
+  a.N_div = make_fast_div(N);
   a.d = d;
   a.interleaved = interleaved;
   a.backward = backward;
@@ -107,6 +108,7 @@ int set_cache(CacheArgs* c, const void* kc, const void* vc, const float* kd, con
   c->max_pages = max_pages;
   c->B = B;
   c->capacity = max_pages * page_size;
+  c->page_div = make_fast_div(page_size);
   return ATTN_OK;
 }
 
@@ -166,6 +168,8 @@ int kv_cache_write(const void* K, const void* V, const int64_t* strides, void* K
   r.start = start;
   r.count = count;
   r.T = T;
+  r.T_div = make_fast_div(T);
+  r.head_div = make_fast_div(Hkv);
   int* err = error_word_ptr();
   if (!err) return ATTN_ERR_CUDA;
   return launch_status(launch_kv_write(c, r, err, (cudaStream_t)stream));
@@ -192,6 +196,8 @@ int kv_cache_read(const void* K_cache, const void* V_cache, const float* k_desca
   r.start = start;
   r.count = count;
   r.T = T;
+  r.T_div = make_fast_div(T);
+  r.head_div = make_fast_div(Hkv);
   int* err = error_word_ptr();
   if (!err) return ATTN_ERR_CUDA;
   return launch_status(launch_kv_read(c, r, err, (cudaStream_t)stream));

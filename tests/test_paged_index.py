@@ -69,6 +69,25 @@ int main() {
     for (int i = 0; i < G; ++i) CHECK(split_owner(split_begin(i, W, G), W, G) == i);
     CHECK(split_owner(W - 1, W, G) == G - 1);
   }
+  // division by multiplication: every small case, and the edges of every quotient
+  // near the ends of the range
+  for (uint32_t d = 1; d <= 300; ++d) {
+    const FastDiv f = make_fast_div(d);
+    for (uint32_t n = 0; n < 5000; ++n) CHECK(fast_div(n, f) == n / d);
+  }
+  uint32_t rnd = 12345;
+  for (int i = 0; i < 200000; ++i) {
+    rnd = rnd * 1664525u + 1013904223u;
+    const uint32_t d = (rnd >> (i % 31)) % 0x7FFFFFFFu + 1;
+    const FastDiv f = make_fast_div(d);
+    const uint32_t q = 0x7FFFFFFFu / d;
+    for (uint32_t n : {0u, d - 1, q * d - 1, q * d, 0x7FFFFFFFu, q / 2 * d, (q / 2 + 1) * d - 1})
+      if (n <= 0x7FFFFFFFu) CHECK(fast_div(n, f) == n / d);
+  }
+  for (uint32_t d : {0x7FFFFFFFu, 0x7FFFFFFEu, 0x40000000u, 0x40000001u}) {
+    const FastDiv f = make_fast_div(d);
+    for (uint32_t n : {0u, 1u, d - 1, d, 0x7FFFFFFFu}) CHECK(fast_div(n, f) == n / d);
+  }
   return 0;
 }
 """
