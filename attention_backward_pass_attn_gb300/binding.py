@@ -430,11 +430,10 @@ def _device_index(t: torch.Tensor, name: str) -> int:
     """The index of the current CUDA device, which t must be on."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
     dev = t.get_device()
     if dev != _current_device():
-        raise ValueError("%s must be on the current CUDA device" % name)
+        raise ValueError("%s must be on the current CUDA device" % name if t.is_cuda else
+                         "%s must be a CUDA tensor" % name)
     return dev
 
 

@@ -588,8 +588,21 @@ __device__ __forceinline__ void join_weights(const DecodeArgs& a, const Parts& p
 
 template <int D, int IT, int KP>
 __device__ __forceinline__ void join_rows(const DecodeArgs& a, const Parts& ps, int heads,
-                                          int64_t out, const float* w) {
+                                          int64_t out, float* w) {
   const int items = heads * (D / 4), last = ps.parts - 1;
+  float4 v[KP][IT];
+  auto load = [&](int i0, int k0) {
+#pragma unroll
+    for (int j = 0; j < KP; ++j) {
+      const float* src = a.part_o + ps.slot(min(k0 + j, last)) * (kDecodeHeads * D);
+#pragma unroll
+      for (int n = 0; n < IT; ++n)
+        v[j][n] = __ldcg(reinterpret_cast<const float4*>(src) + min(i0 + n * kThreads, items - 1));
+    }
+  };
+  load(threadIdx.x, 0);  // ahead of the weights, which need a read of their own
+  join_weights(a, ps, heads, out, w);
+  __syncthreads();
 #pragma unroll 1
   for (int i0 = threadIdx.x; i0 < items; i0 += IT * kThreads) {
     float4 acc[IT];
@@ -597,14 +610,7 @@ __device__ __forceinline__ void join_rows(const DecodeArgs& a, const Parts& ps, 
     for (int n = 0; n < IT; ++n) acc[n] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
     for (int k0 = 0; k0 <= last; k0 += KP) {
-      float4 v[KP][IT];
-#pragma unroll
-      for (int j = 0; j < KP; ++j) {
-        const float* src = a.part_o + ps.slot(min(k0 + j, last)) * (kDecodeHeads * D);
-#pragma unroll
-        for (int n = 0; n < IT; ++n)
-          v[j][n] = __ldcg(reinterpret_cast<const float4*>(src) + min(i0 + n * kThreads, items - 1));
-      }
+      if (k0 || i0 >= kThreads) load(i0, k0);
 #pragma unroll
       for (int j = 0; j < KP; ++j)  // parts past the last have weight 0
 #pragma unroll
@@ -632,8 +638,6 @@ __device__ __forceinline__ void join_rows(const DecodeArgs& a, const Parts& ps, 
 template <int D>
 __device__ __forceinline__ void join_parts(const DecodeArgs& a, const Parts& ps, int heads,
                                            int64_t out, float* w) {
-  join_weights(a, ps, heads, out, w);
-  __syncthreads();
   if (heads * (D / 4) <= kThreads)
     join_rows<D, 1, 20>(a, ps, heads, out, w);
   else
