@@ -431,9 +431,10 @@ def _device_index(t: torch.Tensor, name: str) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     dev = t.get_device()
+    if dev < 0:
+        raise ValueError("%s must be a CUDA tensor" % name)
     if dev != _current_device():
-        raise ValueError("%s must be on the current CUDA device" % name if t.is_cuda else
-                         "%s must be a CUDA tensor" % name)
+        raise ValueError("%s must be on the current CUDA device" % name)
     return dev
 
 

@@ -87,7 +87,8 @@ int check_cache(int B, int Hkv, int d, int page_size, int num_pages, int max_pag
     return ATTN_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
   if (page_size % kPageQuantum) return ATTN_ERR_UNSUPPORTED;
-  if ((long long)max_pages * page_size > INT_MAX) return ATTN_ERR_UNSUPPORTED;
+  // a key index one unit of work past the last position stays in 31 bits
+  if ((long long)max_pages * page_size > INT_MAX - 4096) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
 

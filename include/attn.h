@@ -333,8 +333,9 @@ int ssd_bwd(const void* x, const float* dt, const float* A, const void* B, const
  *
  * page_size is a multiple of 16 (ATTN_ERR_UNSUPPORTED otherwise), num_pages,
  * max_pages and Hkv are at least 1 (ATTN_ERR_INVALID_ARG otherwise), d is 64
- * or 128, and max_pages x page_size fits 31 bits.  Sequences may share pages
- * that are only read.  Tables, lengths and positions live in device memory,
+ * or 128, and max_pages x page_size is at most 2^31 - 4097
+ * (ATTN_ERR_UNSUPPORTED otherwise).  Sequences may share pages that are only
+ * read.  Tables, lengths and positions live in device memory,
  * so a captured graph replays on the values of that moment.
  *
  * An entry that a call needs and that names no page (below 0, or num_pages

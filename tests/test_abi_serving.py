@@ -91,6 +91,7 @@ def test_cache_validation(lib, kind):
     assert call(d=96) == UNSUPPORTED
     assert call(ps=8) == UNSUPPORTED and call(ps=24) == UNSUPPORTED
     assert call(ps=1 << 16, mp=1 << 15) == UNSUPPORTED       # positions beyond 31 bits
+    assert call(ps=4096, mp=(1 << 19) - 1) == UNSUPPORTED    # or too near their end
     for bad in (dict(ps=0), dict(ps=-16), dict(P=0), dict(mp=0), dict(Hkv=0), dict(B=-1),
                 dict(kc=None), dict(vc=FAKE + 8), dict(table=None), dict(table=FAKE + 2),
                 dict(kd=FAKE), dict(vd=FAKE), dict(kd=FAKE, vd=FAKE + 2), dict(x=None),

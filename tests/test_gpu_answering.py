@@ -246,6 +246,37 @@ def test_chained_calls_see_finished_results():
         assert torch.equal(a, b)
 
 
+def test_what_a_call_allocates_belongs_to_its_stream():
+    """Results and workspaces of calls on another stream than the current one
+    are not handed out again on the current one while that stream still works:
+    a long queue of calls there, and allocations here meanwhile."""
+    s = step_state(98)
+    step(s)
+    torch.cuda.synchronize()
+    ref = s["o"].clone()
+    other = torch.cuda.Stream()
+    busy = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(30):
+        with torch.cuda.stream(other):
+            torch.mm(busy, busy)  # the calls below wait behind it
+        o, lse = ab.attn_decode(s["q"], s["kc"], s["vc"], s["table"], s["after"],
+                                k_descale=s["kd"], v_descale=s["vd"], stream=other)
+        ab.attn_decode(s["q"], s["kc"], s["vc"], s["table"], s["after"], k_descale=s["kd"],
+                       v_descale=s["vd"], stream=other)  # dropped at once
+        junk = [torch.full((1 << 20,), float("nan"), device="cuda") for _ in range(12)]
+    other.synchronize()
+    assert torch.equal(o, ref)
+    del junk, lse
+    for handle in (other.cuda_stream, other):
+        with torch.cuda.stream(other):
+            pass
+        o, _ = ab.attn_decode(s["q"], s["kc"], s["vc"], s["table"], s["after"],
+                              k_descale=s["kd"], v_descale=s["vd"], stream=handle)
+        other.synchronize()
+        assert torch.equal(o, ref)
+
+
 def test_a_stream_argument_is_used():
     s = step_state(97)
     step(s)

@@ -212,6 +212,69 @@ def test_decode_bad_pages_and_lengths(fp8):
     check(o, lse, ref, d)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_decode_many_sequences(fp8):
+    """More sequences than a block has threads, most of them empty or a few
+    positions long, and more head blocks than thread blocks."""
+    rng = np.random.default_rng(8)
+    lens = [int(n) for n in rng.choice([0, 0, 1, 5, 16, 17, 40, 100, 300], 700)]
+    lens[-1] = 0
+    c = filled_cache(lens, 16, 2, 64, 81, fp8)
+    q = make_tensor((len(lens), 4, 1, 64), 82)
+    o, lse = run(q, c, lens)
+    check(o, lse, serving.decode(q, c["k64"], c["v64"], c["table"], lens, 1 / 8), 64)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_cache_beyond_32_bits(fp8):
+    """A cache of more than 2^31 values (2^32 in 8 bits), its last pages used:
+    written, attended and read back."""
+    Hkv, d, page, n = 2, 128, 64, 200
+    P = ((1 << 32 if fp8 else 1 << 31) // (Hkv * d * page)) + 40
+    kc, vc = (torch.empty((P, Hkv, page, d), device="cuda",
+                          dtype=torch.float8_e4m3fn if fp8 else torch.bfloat16) for _ in range(2))
+    kd, vd = ((torch.empty((P, Hkv, page), device="cuda") for _ in range(2)) if fp8
+              else (None, None))
+    table = torch.tensor([[P - 1, P - 7, P - 3, P - 20], [P - 2, 0, P // 2, P - 21]],
+                         dtype=torch.int32).cuda()
+    x = make_tensor((2, n, 2 * Hkv, d), 90).cuda()
+    k, v = x[:, :, :Hkv].transpose(1, 2), x[:, :, Hkv:].transpose(1, 2)
+    zero, lens = i32([0, 0]).cuda(), i32([n, n - 9]).cuda()
+    ab.kv_cache_write(k, v, kc, vc, table, zero, lens, kd, vd)
+    q = make_tensor((2, 8, 1, d), 91)
+    o, lse = ab.attn_decode(q.cuda(), kc, vc, table, lens, k_descale=kd, v_descale=vd)
+    kr, vr = ab.kv_cache_read(kc, vc, table, zero, n, lens, kd, vd)
+    # the oracle on the rounded rows, laid out as a small cache of their own
+    small = torch.arange(8, dtype=torch.int32).view(2, 4)
+    val = []
+    for t in (k, v):
+        t = t.contiguous().cpu()
+        if fp8:
+            code, fac = serving.quantise_rows(t)
+            t = torch.from_numpy(serving.e4m3_to_f64(code) * fac[..., None])
+        t = torch.nn.functional.pad(t.double(), (0, 0, 0, 4 * page - n))
+        val.append(t.view(2, Hkv, 4, page, d).permute(0, 2, 1, 3, 4).reshape(8, Hkv, page, d).numpy())
+    check(o, lse, serving.decode(q, val[0], val[1], small, [n, n - 9], 1 / math.sqrt(d)), d)
+    for got, w in ((kr, val[0]), (vr, val[1])):
+        w = w.reshape(2, 4, Hkv, page, d).transpose(0, 2, 1, 3, 4).reshape(2, Hkv, 4 * page, d)[:, :, :n]
+        w[1, :, n - 9:] = 0
+        assert np.array_equal(f64(got), w)
+
+
+def test_decode_takes_bytes_and_given_outputs():
+    """uint8 views of an e4m3 cache, and outputs of the caller's."""
+    lens = [70, 33]
+    c = filled_cache(lens, 16, 2, 64, 45, True)
+    q = make_tensor((2, 4, 1, 64), 46)
+    ref = run(q, c, lens)
+    out = torch.empty(2, 4, 1, 64, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(2, 4, 1, device="cuda")
+    c["kc"], c["vc"] = c["kc"].view(torch.uint8), c["vc"].view(torch.uint8)
+    got = run(q, c, lens, out=out, lse=lse)
+    assert got[0] is out and got[1] is lse
+    assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+
+
 def test_decode_workspace_contents_do_not_matter():
     """A workspace of NaN bytes, then the same workspace after another batch."""
     d, page, Hkv, group = 128, 16, 2, 4
