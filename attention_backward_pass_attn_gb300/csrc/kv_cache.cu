@@ -12,8 +12,7 @@
 // where 1 / descale is still finite.
 //
 // Bound by HBM: a written row is read once (2 d bytes) and written once (2 d,
-// or d + 4 in e4m3); reading back is the reverse.  D / 8 lanes hold a row,
-// 16 bytes of bf16 each.
+// or d + 4 in e4m3); reading back is the reverse.
 #include <cuda_fp16.h>
 
 #include "kernels.h"
@@ -25,7 +24,6 @@ namespace attn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 2;
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   uint32_t d;
@@ -33,17 +31,20 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// Largest magnitude among a lane's 8 values, as bf16 bits; of the finite ones
+// Largest magnitude among a lane's 16 values, as bf16 bits; of the finite ones
 // when there are others.
-__device__ __forceinline__ uint32_t amax_bits(const uint4& x) {
-  const uint32_t w[4] = {x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu, x.z & 0x7FFF7FFFu,
-                         x.w & 0x7FFF7FFFu};
-  uint32_t m = max_u16x2(max_u16x2(w[0], w[1]), max_u16x2(w[2], w[3]));
+__device__ __forceinline__ uint32_t amax_bits(const uint4 (&x)[2]) {
+  const uint32_t w[8] = {x[0].x & 0x7FFF7FFFu, x[0].y & 0x7FFF7FFFu, x[0].z & 0x7FFF7FFFu,
+                         x[0].w & 0x7FFF7FFFu, x[1].x & 0x7FFF7FFFu, x[1].y & 0x7FFF7FFFu,
+                         x[1].z & 0x7FFF7FFFu, x[1].w & 0x7FFF7FFFu};
+  uint32_t m = w[0];
+#pragma unroll
+  for (int k = 1; k < 8; ++k) m = max_u16x2(m, w[k]);
   m = max(m & 0xFFFFu, m >> 16);
   if (m >= 0x7F80u) {  // an infinity or a NaN
     m = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 8; ++k) {
       const uint32_t lo = w[k] & 0xFFFFu, hi = w[k] >> 16;
       m = max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
     }
@@ -86,63 +87,67 @@ __device__ __forceinline__ int64_t locate(const CacheArgs& c, const CacheRows& r
   return cache_row(page, c.Hkv, w.h, c.page_size, int(p - pi * c.page_size));
 }
 
-// Each group of D / 8 lanes takes R rows, their loads issued together.
-template <int D, bool FP8, int R>
+// D / 16 lanes take a row of K and of V, 8 values of either half each: finding
+// the row is shared by 64 bytes a lane.  With 32 bytes a lane and 64-bit
+// divisions this kernel was bound by its instructions (the ALU 71 % busy) at
+// 76 us for the 20k tokens that now take 36.
+template <int D, bool FP8>
 __global__ void __launch_bounds__(kThreads)
     kv_write_kernel(const CacheArgs c, const CacheRows r, unsigned rows, int* err) {
-  constexpr int kLanes = D / 8, kGroups = kThreads / kLanes;
+  constexpr int kLanes = D / 16, kGroups = kThreads / kLanes;
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x % kLanes;
-  const unsigned first = blockIdx.x * (kGroups * R) + threadIdx.x / kLanes;
-  int64_t dst[R];
-  uint4 x[R][2];
-#pragma unroll
-  for (int j = 0; j < R; ++j) {
-    const unsigned i = first + j * kGroups;
-    dst[j] = -1;
-    x[j][0] = x[j][1] = make_uint4(0, 0, 0, 0);
-    if (i >= rows) continue;
+  const unsigned i = blockIdx.x * kGroups + threadIdx.x / kLanes;
+  uint4 x[2][2] = {};
+  int64_t dst = -1;
+  if (i < rows) {
     const Row w = row_of(i, c, r);
-    dst[j] = locate(c, r, w, kSiteWritePage, lane, err);
-    if (dst[j] < 0) continue;
+    dst = locate(c, r, w, kSiteWritePage, lane, err);
+    if (dst >= 0) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
-      x[j][s] = __ldg(reinterpret_cast<const uint4*>(
-          static_cast<const uint16_t*>(r.x[s]) + w.b * r.sb[s] + w.h * r.sh[s] + w.t * r.st[s] +
-          lane * 8));
-  }
-#pragma unroll
-  for (int j = 0; j < R; ++j) {
-    uint32_t amax = 0;  // K's in the low half, V's in the high one
-    if (FP8) {
-      amax = amax_bits(x[j][0]) | amax_bits(x[j][1]) << 16;
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1)  // all lanes: shuffles
-        amax = max_u16x2(amax, __shfl_xor_sync(0xffffffffu, amax, o, kLanes));
-    }
-    if (dst[j] < 0) continue;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      uint8_t* cache = static_cast<uint8_t*>(s ? c.vc : c.kc);
-      if (!FP8) {
-        *reinterpret_cast<uint4*>(cache + (dst[j] * D + lane * 8) * 2) = x[j][s];
-        continue;
+      for (int s = 0; s < 2; ++s) {
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(r.x[s]) +
+                                                          w.b * r.sb[s] + w.h * r.sh[s] +
+                                                          w.t * r.st[s]);
+        x[s][0] = __ldg(src + lane);
+        x[s][1] = __ldg(src + kLanes + lane);
       }
-      const int e = descale_exponent(s ? amax >> 16 : amax & 0xFFFFu);
-      // 1 / descale as two bf16: x / descale is exact, or below every e4m3
-      // value's half and rounded to zero either way
-      const uint32_t inv = uint32_t(127 - e) << 7 | uint32_t(127 - e) << 23;
-      const uint32_t w[4] = {mul_bf16x2(x[j][s].x, inv), mul_bf16x2(x[j][s].y, inv),
-                             mul_bf16x2(x[j][s].z, inv), mul_bf16x2(x[j][s].w, inv)};
-      uint32_t o[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        o[k] = pack_e4m3x4(bf16lo_to_f32(w[2 * k]), bf16hi_to_f32(w[2 * k]),
-                           bf16lo_to_f32(w[2 * k + 1]), bf16hi_to_f32(w[2 * k + 1]));
-      *reinterpret_cast<uint2*>(cache + dst[j] * D + lane * 8) = make_uint2(o[0], o[1]);
-      if (lane == 0) (s ? c.vd : c.kd)[dst[j]] = pow2f(e);
     }
+  }
+  if (!__any_sync(0xffffffffu, dst >= 0)) return;  // a padded batch's filling
+  uint32_t amax = 0;  // K's in the low half, V's in the high one
+  if (FP8) {
+    amax = amax_bits(x[0]) | amax_bits(x[1]) << 16;
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1)
+      amax = max_u16x2(amax, __shfl_xor_sync(0xffffffffu, amax, o, kLanes));
+  }
+  if (dst < 0) return;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    uint8_t* cache = static_cast<uint8_t*>(s ? c.vc : c.kc) + dst * (D * (FP8 ? 1 : 2));
+    if (!FP8) {
+      reinterpret_cast<uint4*>(cache)[lane] = x[s][0];
+      reinterpret_cast<uint4*>(cache)[kLanes + lane] = x[s][1];
+      continue;
+    }
+    const int e = descale_exponent(s ? amax >> 16 : amax & 0xFFFFu);
+    // 1 / descale as two bf16: x / descale is exact, or below every e4m3
+    // value's half and rounded to zero either way
+    const uint32_t inv = uint32_t(127 - e) * 0x00800080u;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const uint4 v = x[s][half];
+      const uint32_t w[4] = {mul_bf16x2(v.x, inv), mul_bf16x2(v.y, inv), mul_bf16x2(v.z, inv),
+                             mul_bf16x2(v.w, inv)};
+      reinterpret_cast<uint2*>(cache)[half * kLanes + lane] =
+          make_uint2(pack_e4m3x4(bf16lo_to_f32(w[0]), bf16hi_to_f32(w[0]), bf16lo_to_f32(w[1]),
+                                 bf16hi_to_f32(w[1])),
+                     pack_e4m3x4(bf16lo_to_f32(w[2]), bf16hi_to_f32(w[2]), bf16lo_to_f32(w[3]),
+                                 bf16hi_to_f32(w[3])));
+    }
+    if (lane == 0) (s ? c.vd : c.kd)[dst] = pow2f(e);
   }
 }
 
@@ -153,70 +158,64 @@ __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t two) {
   return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
-template <int D, bool FP8, int R>
+template <int D, bool FP8>
 __global__ void __launch_bounds__(kThreads)
     kv_read_kernel(const CacheArgs c, const CacheRows r, unsigned rows, int* err) {
-  constexpr int kLanes = D / 8, kGroups = kThreads / kLanes;
+  constexpr int kLanes = D / 16, kGroups = kThreads / kLanes;
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x % kLanes;
-  const unsigned first = blockIdx.x * (kGroups * R) + threadIdx.x / kLanes;
-  uint4 x[R][2];  // e4m3: the first two words
-  float f[R][2];
-#pragma unroll
-  for (int j = 0; j < R; ++j) {
-    const unsigned i = first + j * kGroups;
-    x[j][0] = x[j][1] = make_uint4(0, 0, 0, 0);
-    f[j][0] = f[j][1] = 0.f;
-    if (i >= rows) continue;
-    const int64_t src = locate(c, r, row_of(i, c, r), kSiteReadPage, lane, err);
-    if (src < 0) continue;
+  const unsigned i = blockIdx.x * kGroups + threadIdx.x / kLanes;
+  if (i >= rows) return;
+  uint4 y[2][2] = {};
+  const int64_t src = locate(c, r, row_of(i, c, r), kSiteReadPage, lane, err);
+  if (src >= 0) {
+    uint2 u[2][2];
+    float f[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const uint8_t* cache = static_cast<const uint8_t*>(s ? c.vc : c.kc);
-      if (FP8) {
-        const uint2 u = __ldg(reinterpret_cast<const uint2*>(cache + src * D + lane * 8));
-        x[j][s].x = u.x;
-        x[j][s].y = u.y;
-        f[j][s] = __ldg((s ? c.vd : c.kd) + src);
-      } else {
-        x[j][s] = __ldg(reinterpret_cast<const uint4*>(cache + (src * D + lane * 8) * 2));
+      const uint8_t* cache =
+          static_cast<const uint8_t*>(s ? c.vc : c.kc) + src * (D * (FP8 ? 1 : 2));
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (FP8)
+          u[s][half] = __ldg(reinterpret_cast<const uint2*>(cache) + half * kLanes + lane);
+        else
+          y[s][half] = __ldg(reinterpret_cast<const uint4*>(cache) + half * kLanes + lane);
       }
+      if (FP8) f[s] = __ldg((s ? c.vd : c.kd) + src);
+    }
+    if (FP8) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t o[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 g =
+                e4m3x2_to_f32((k < 2 ? u[s][half].x : u[s][half].y) >> (k & 1 ? 16 : 0));
+            o[k] = pack_bf16x2(g.x * f[s], g.y * f[s]);
+          }
+          y[s][half] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
     }
   }
 #pragma unroll
-  for (int j = 0; j < R; ++j) {
-    const unsigned i = first + j * kGroups;
-    if (i >= rows) continue;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      uint4 y = x[j][s];
-      if (FP8) {
-        uint32_t o[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 g = e4m3x2_to_f32((k < 2 ? y.x : y.y) >> (k & 1 ? 16 : 0));
-          o[k] = pack_bf16x2(g.x * f[j][s], g.y * f[j][s]);
-        }
-        y = make_uint4(o[0], o[1], o[2], o[3]);
-      }
-      // the output is contiguous: row i of [B][Hkv][T]
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(r.x[s]) + int64_t(i) * D + lane * 8) = y;
-    }
+  for (int s = 0; s < 2; ++s) {  // the output is contiguous: row i of [B][Hkv][T]
+    uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(r.x[s]) + int64_t(i) * D);
+    out[lane] = y[s][0];
+    out[kLanes + lane] = y[s][1];
   }
 }
 
-// Rows per group of lanes: one while that leaves the GPU short of blocks.
 template <typename K>
-cudaError_t launch(K one, K several, const CacheArgs& c, const CacheRows& r, int* err,
+cudaError_t launch(K kernel, const CacheArgs& c, const CacheRows& r, int* err,
                    cudaStream_t stream) {
   const unsigned rows = unsigned(int64_t(c.B) * c.Hkv * r.T);
-  const unsigned groups = kThreads / (c.d / 8);
-  const unsigned blocks = (rows + groups - 1) / groups;
-  if (blocks <= unsigned(device_sm_count()) * 8)
-    return launch_kernel(one, dim3(blocks), dim3(kThreads), 0, stream, c, r, rows, err);
-  return launch_kernel(several, dim3((blocks + kRows - 1) / kRows), dim3(kThreads), 0, stream, c, r,
-                       rows, err);
+  const unsigned per_block = kThreads / (c.d / 16);
+  return launch_kernel(kernel, dim3((rows + per_block - 1) / per_block), dim3(kThreads), 0, stream,
+                       c, r, rows, err);
 }
 
 }  // namespace
@@ -224,19 +223,19 @@ cudaError_t launch(K one, K several, const CacheArgs& c, const CacheRows& r, int
 cudaError_t launch_kv_write(const CacheArgs& c, const CacheRows& r, int* err,
                             cudaStream_t stream) {
   if (c.d == 64)
-    return c.kd ? launch(kv_write_kernel<64, true, 1>, kv_write_kernel<64, true, kRows>, c, r, err, stream)
-                : launch(kv_write_kernel<64, false, 1>, kv_write_kernel<64, false, kRows>, c, r, err, stream);
-  return c.kd ? launch(kv_write_kernel<128, true, 1>, kv_write_kernel<128, true, kRows>, c, r, err, stream)
-              : launch(kv_write_kernel<128, false, 1>, kv_write_kernel<128, false, kRows>, c, r, err, stream);
+    return c.kd ? launch(kv_write_kernel<64, true>, c, r, err, stream)
+                : launch(kv_write_kernel<64, false>, c, r, err, stream);
+  return c.kd ? launch(kv_write_kernel<128, true>, c, r, err, stream)
+              : launch(kv_write_kernel<128, false>, c, r, err, stream);
 }
 
 cudaError_t launch_kv_read(const CacheArgs& c, const CacheRows& r, int* err,
                            cudaStream_t stream) {
   if (c.d == 64)
-    return c.kd ? launch(kv_read_kernel<64, true, 1>, kv_read_kernel<64, true, kRows>, c, r, err, stream)
-                : launch(kv_read_kernel<64, false, 1>, kv_read_kernel<64, false, kRows>, c, r, err, stream);
-  return c.kd ? launch(kv_read_kernel<128, true, 1>, kv_read_kernel<128, true, kRows>, c, r, err, stream)
-              : launch(kv_read_kernel<128, false, 1>, kv_read_kernel<128, false, kRows>, c, r, err, stream);
+    return c.kd ? launch(kv_read_kernel<64, true>, c, r, err, stream)
+                : launch(kv_read_kernel<64, false>, c, r, err, stream);
+  return c.kd ? launch(kv_read_kernel<128, true>, c, r, err, stream)
+              : launch(kv_read_kernel<128, false>, c, r, err, stream);
 }
 
 }  // namespace attn
