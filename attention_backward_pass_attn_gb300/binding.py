@@ -422,6 +422,7 @@ def ssd_bwd(x, dt, A, B, C, D, dy, workspace=None, out=None, stream=None):
 # the reason, so that a call of a few microseconds on the GPU is not drowned by
 # its checks.
 _E4M3_DTYPES = (torch.float8_e4m3fn, torch.uint8)
+_DEVICES = [torch.device("cuda", i) for i in range(64)]  # cheaper to pass than an index
 _current_device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream
 
@@ -451,8 +452,8 @@ def _empty(shape, dtype, dev: int, stream) -> torch.Tensor:
     """Uninitialised memory of the stream the call runs on: on another than
     the current one, the allocator must not hand it to the current one when it
     is freed."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+    if stream is None or _stream_on(stream, dev) == _current_stream(dev):
+        return torch.empty(shape, dtype=dtype, device=_DEVICES[dev])
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=dev)
     with torch.cuda.stream(stream):
@@ -729,7 +730,7 @@ def attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, k_descale
         raise ValueError("q's %d heads must be a multiple of the cache's %d" % (Hq, Hkv))
     _check_like(seq_lens, "seq_lens", (B,), torch.int32, dev)
     if out is None:
-        out = _empty(shape, torch.bfloat16, dev, stream)
+        out = torch.empty_like(q) if stream is None else _empty(shape, torch.bfloat16, dev, stream)
     else:
         _check_like(out, "out", shape, torch.bfloat16, dev)
     if lse is None:

@@ -30,6 +30,11 @@
 //   the next keys while the next scores are formed: 4 to 8 KB in flight per
 //   warp, 12 warps per SM.
 //
+// Measured (one call among others in a graph): 131,072 positions, 8 key heads
+// x 4, d=128, bf16: 84 us, 6.4 TB/s, of which the walk over the keys is 76; 32
+// sequences of up to 8,192, 8 key heads x 8, e4m3: 53 us for 264 MB; 500
+// positions of 16 heads: 7.2 us, 2.7 of them from the arrivals on.
+//
 // Rounding.  Scores, maxima, sums and outputs are fp32.  The weights p meet a
 // bf16 V as a sum of two bf16 numbers, 16 bits in all (2^-16; a second
 // instruction that costs nothing here), so the result's only rounding that
@@ -226,7 +231,8 @@ struct Warp {
       for (int c = 0; c < C::kChunks; ++c)
 #pragma unroll
         for (int x = 0; x < (FP8 ? 2 : 1); ++x) {
-          const uint4 w = live ? __ldg(src + (4 * c + q) * (FP8 ? 2 : 1) + x) : make_uint4(0, 0, 0, 0);
+          const uint4 w =
+              live ? __ldg(src + (4 * c + q) * (FP8 ? 2 : 1) + x) : make_uint4(0, 0, 0, 0);
           const int step = FP8 ? 4 * c + 2 * x : 2 * c;
           qf[g][step][0] = w.x;
           qf[g][step][1] = w.y;
@@ -282,8 +288,8 @@ struct Warp {
     }
   }
 
-  // The cache row of the first key of run `lane` (lanes below KT) of the step
-  // at key `tile`, or of the last run below len; -1 on a bad page.
+  // The cache row of the first key of run lane % KT of the step at key `tile`,
+  // or of the last run below len; -1 on a bad page.
   __device__ __forceinline__ int64_t find(const int* table, int kvh, int tile, int len) {
     const int pos = min(tile + 16 * (lane % KT), (len - 1) & ~(kPageQuantum - 1));
     const int pi = int(fast_div(pos, a.c.page_div));
@@ -297,8 +303,7 @@ struct Warp {
 
   // Whether every key of the step is visible and its pages are good.
   __device__ __forceinline__ bool full(int64_t rows, int tile, int lo, int len) const {
-    return tile >= lo && tile + 16 * KT <= len &&
-           __all_sync(0xffffffffu, rows >= 0);
+    return tile >= lo && tile + 16 * KT <= len && __all_sync(0xffffffffu, rows >= 0);
   }
   __device__ __forceinline__ static bool sees(int64_t row, int key, int lo, int len) {
     return row >= 0 && key >= lo && key < len;
@@ -307,9 +312,9 @@ struct Warp {
   // The loads of a step have no conditions: a run that is only partly visible
   // is read whole (it lies on one page), one past the length reads the last
   // run again, one on a bad page row 0, and what must not count is masked
-  // where it is used.  A
-  // branch here made the registers that wait for the loads meet at its end,
-  // and the loop wait with them (62 us became 76 for the e4m3 batch below).
+  // where it is used.  A branch here made the registers that wait for the
+  // loads meet at its end, and the loop wait with them (the e4m3 batch above:
+  // 62 us became 76).
   __device__ __forceinline__ void load_k(int64_t rows) {
     const uint8_t* cache = static_cast<const uint8_t*>(a.c.kc);
 #pragma unroll
@@ -492,6 +497,7 @@ struct Warp {
         }
       }
   }
+
   // One step's keys; MORE: with the loads of the next step's among it.
   template <bool MORE>
   __device__ __forceinline__ void step(int64_t rows, bool full, int tile, int lo, int len,
@@ -747,8 +753,8 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
   int pieces = 0;
   for (int turn = 0;; ++turn) {
     {
-    const Work w = sh_work[turn & 1];
-    const int units = w.units();
+      const Work w = sh_work[turn & 1];
+      const int units = w.units();
       if (tid == 0 && units != w.n) {
         const int64_t W = sh_W;
         const int G = int(W < int64_t(gridDim.x) ? W : int64_t(gridDim.x));

@@ -424,7 +424,8 @@ int kv_cache_read(const void* K_cache, const void* V_cache, const float* k_desca
  * Q, O: bf16 [B][Hq][d]; L: fp32 [B][Hq], natural log.  A sequence with
  * nothing to see (n = 0, or only skipped positions) gets O = 0 and L = -inf.
  * Values of the cache at positions that are not visible have no effect, NaN
- * and infinities included.  Hq is a multiple of Hkv.
+ * and infinities included; a NaN or an infinity at a visible position makes
+ * the outputs that use it infinite or NaN.  Hq is a multiple of Hkv.
  *
  * The work is split evenly over the GPU, whatever the lengths, and the parts
  * of a sequence are joined in a fixed order: results repeat bit for bit.  The

@@ -289,3 +289,27 @@ def test_a_stream_argument_is_used():
         step(s, stream=other)
     other.synchronize()
     assert torch.equal(s["o"], ref)
+
+
+def test_readme_example_runs():
+    """The README's answering example, a step further than it goes: two tokens
+    from empty sequences."""
+    import os
+    import re
+
+    import attention_backward_pass_attn_gb300 as attn
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "README.md")).read()
+    code = [b for b in re.findall(r"```python\n(.*?)```", text, flags=re.S) if "attn_decode" in b]
+    assert len(code) == 1
+    scope = {"torch": torch, "attn": attn}
+    exec(code[0], scope)
+    first = scope["o"]
+    x = torch.randn(2, 1, 48, 128, device="cuda").to(torch.bfloat16)
+    second, lens = scope["token"](x, scope["lens"])
+    assert first.shape == second.shape == (2, 32, 1, 128)
+    assert torch.isfinite(first).all() and torch.isfinite(second).all()
+    assert lens.tolist() == [2, 2]
+    # one position: the answer is that position's value, as e4m3 rounds it
+    assert torch.equal(first[:, ::4], first[:, 1::4])
