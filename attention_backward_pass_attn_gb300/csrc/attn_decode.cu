@@ -32,18 +32,17 @@
 //
 // Measured (one call among others in a graph): 131,072 positions, 8 key heads
 // x 4, d=128, bf16: 84 us, 6.4 TB/s, of which the walk over the keys is 76; 32
-// sequences of up to 8,192, 8 key heads x 8, e4m3: 53 us for 264 MB; 500
+// sequences of up to 8,192, 8 key heads x 8, e4m3: 54 us for 264 MB; 500
 // positions of 16 heads: 7.2 us, 2.7 of them from the arrivals on.
 //
-// Rounding.  Scores, maxima, sums and outputs are fp32.  The weights p meet a
-// bf16 V as a sum of two bf16 numbers, 16 bits in all (2^-16; a second
-// instruction that costs nothing here), so the result's only rounding that
-// counts is the last one to bf16.  For an e4m3 cache both products run in
-// fp16, which holds every e4m3 value: q is scaled by a power of two into
-// fp16's range (exact down to 2^-29 of its largest element), and the weights,
-// V's factors included, are scaled so that 2^15 is the most they can be and
-// rounded to fp16's 11 bits (2^-12 of the weight, down to 2^-29 of the
-// largest; a sixteenth of the last rounding's step).
+// Rounding.  Scores, maxima, sums and outputs are fp32.  The weights p (times
+// V's factor of an e4m3 row) meet V as a sum of two bf16 numbers, 16 bits in
+// all (2^-16), so the result's only rounding that counts is the last one to
+// bf16.  The second instruction costs nothing with a bf16 cache and 2 % with
+// an e4m3 one, where one fp16 number would do if the factors were known to be
+// of similar size.  An e4m3 K is widened to fp16 (exact) and meets a q scaled by
+// a power of two into fp16's range (exact down to 2^-29 of its largest
+// element); V is widened to bf16 (exact).
 #include <cuda_fp16.h>
 
 #include "f32x2.cuh"
@@ -103,11 +102,16 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   return y;
 }
 
-// Two e4m3 values (low 16 bits) as fp16, exactly.
+// Two e4m3 values (low 16 bits) as fp16 and as bf16; both exact.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(two)));
   return h;
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two) {
+  const uint32_t h = e4m3x2_to_f16x2(two);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return pack_bf16x2(f.x, f.y);
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -210,7 +214,6 @@ struct Warp {
   uint32_t kw[KT * 2 * C::kChunks][4];
   uint32_t vw[KT][4][C::kVWords];
   float kd[FP8 ? KT : 1][2], vd[FP8 ? KT : 1][2];
-  float v_top, v_up;  // e4m3: bound of V's factors so far (a power of two), 2^15 / v_top
   uint32_t qf[NG][D / 16][2];
   float factor[NG][2];
   float m[NG][2], l[NG][2];
@@ -245,7 +248,6 @@ struct Warp {
   // The running state's start; q in the products' type, and what turns a
   // product into a score.
   __device__ __forceinline__ void begin() {
-    v_top = v_up = 0.f;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       float f = a.scale_log2;
@@ -419,10 +421,9 @@ struct Warp {
   }
 
   // Weight the scores of the step's keys: running maximum and sum, rescaled
-  // accumulators, and P^T in the tensor core's layout (bf16 V: two parts).
-  static constexpr int kParts = FP8 ? 1 : 2;
+  // accumulators, and P^T as two bf16 parts in the tensor core's layout.
   __device__ __forceinline__ void weigh(float (&s)[KT][NG][4], bool full, int64_t rows, int tile,
-                                        int lo, int len, uint32_t (&p)[KT][NG][kParts][2]) {
+                                        int lo, int len, uint32_t (&p)[KT][NG][2][2]) {
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -446,29 +447,11 @@ struct Warp {
         grown |= mx != m[g][y];
         m[g][y] = mx;
       }
-    float v_down = 1.f;
-    if (FP8) {
-      float top = 0.f;
-#pragma unroll
-      for (int t = 0; t < KT; ++t) top = max3f(top, fabsf(vd[t][0]), fabsf(vd[t][1]));
-      if (__any_sync(0xffffffffu, top > v_top)) {
-        top = keys_max(top);
-        // the power of two above it, kept where 2^15 / v_top is a number too
-        const int e = max(int(__float_as_uint(top) >> 23) - 126, -111);
-        const float next = e > 127 ? 0x1p127f : pow2f(e);
-        v_down = v_top / next;
-        v_top = next;
-        v_up = e > 127 ? 0x1p-112f : pow2f(15 - e);
-        grown = true;
-      }
-    }
     if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         l[g][0] *= alpha[g][0];
         l[g][1] *= alpha[g][1];
-        alpha[g][0] *= v_down;
-        alpha[g][1] *= v_down;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -479,21 +462,19 @@ struct Warp {
     for (int t = 0; t < KT; ++t)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const float up = FP8 ? vd[t][x] * v_up : 1.f;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          const float w0 = ex2(s[t][g][2 * x] - ref[g][0]);
-          const float w1 = ex2(s[t][g][2 * x + 1] - ref[g][1]);
+          float w0 = ex2(s[t][g][2 * x] - ref[g][0]), w1 = ex2(s[t][g][2 * x + 1] - ref[g][1]);
           l[g][0] += w0;
           l[g][1] += w1;
           if (FP8) {
-            p[t][g][0][x] = transpose_8x8(pack_f16x2(w0 * up, w1 * up));
-          } else {
-            const uint32_t hi = pack_bf16x2(w0, w1);
-            p[t][g][0][x] = transpose_8x8(hi);
-            p[t][g][kParts - 1][x] =
-                transpose_8x8(pack_bf16x2(w0 - bf16lo_to_f32(hi), w1 - bf16hi_to_f32(hi)));
+            w0 *= vd[t][x];
+            w1 *= vd[t][x];
           }
+          const uint32_t hi = pack_bf16x2(w0, w1);
+          p[t][g][0][x] = transpose_8x8(hi);
+          p[t][g][1][x] =
+              transpose_8x8(pack_bf16x2(w0 - bf16lo_to_f32(hi), w1 - bf16hi_to_f32(hi)));
         }
       }
   }
@@ -505,7 +486,7 @@ struct Warp {
     float s[KT][NG][4];
 #pragma unroll
     for (int t = 0; t < KT; ++t) scores(t, s[t]);
-    uint32_t p[KT][NG][kParts][2];
+    uint32_t p[KT][NG][2][2];
     weigh(s, full, rows, tile, lo, len, p);
     if (MORE) load_k(next_rows);
     if (!full) mask_v(rows, tile, lo, len);
@@ -513,15 +494,12 @@ struct Warp {
     if (MORE) load_v(next_rows);
   }
 
-  // What turns an accumulator into sum_j p_j v_j.
-  __device__ __forceinline__ float unit() const { return FP8 ? v_top * 0x1p-15f : 1.f; }
-
   // O^T += V^T P^T over the step's keys.  Accumulator i of a thread covers
   // output columns column(i) and the next one.
   __device__ __forceinline__ int column(int i) const {
     return FP8 ? (D / 8) * r + 2 * i : (i / 4) * 64 + 8 * r + 2 * (i % 4);
   }
-  __device__ __forceinline__ void add(const uint32_t (&p)[KT][NG][kParts][2]) {
+  __device__ __forceinline__ void add(const uint32_t (&p)[KT][NG][2][2]) {
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -531,10 +509,10 @@ struct Warp {
           const uint32_t sel = i & 1 ? 0x7362u : 0x5140u;
           const uint32_t u = __byte_perm(vw[t][0][i / 2], vw[t][1][i / 2], sel);
           const uint32_t v = __byte_perm(vw[t][2][i / 2], vw[t][3][i / 2], sel);
-          a0 = e4m3x2_to_f16x2(u);
-          a1 = e4m3x2_to_f16x2(u >> 16);
-          a2 = e4m3x2_to_f16x2(v);
-          a3 = e4m3x2_to_f16x2(v >> 16);
+          a0 = e4m3x2_to_bf16x2(u);
+          a1 = e4m3x2_to_bf16x2(u >> 16);
+          a2 = e4m3x2_to_bf16x2(v);
+          a3 = e4m3x2_to_bf16x2(v >> 16);
         } else {
           a0 = __byte_perm(vw[t][0][i], vw[t][1][i], 0x5410);
           a1 = __byte_perm(vw[t][0][i], vw[t][1][i], 0x7632);
@@ -544,8 +522,8 @@ struct Warp {
 #pragma unroll
         for (int g = 0; g < NG; ++g)
 #pragma unroll
-          for (int x = 0; x < kParts; ++x)
-            mma_16x8x16<FP8>(acc[g][i], a0, a1, a2, a3, p[t][g][x][0], p[t][g][x][1]);
+          for (int x = 0; x < 2; ++x)
+            mma_16x8x16<false>(acc[g][i], a0, a1, a2, a3, p[t][g][x][0], p[t][g][x][1]);
       }
   }
 };
@@ -798,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
           *reinterpret_cast<float2*>(&sh_o[warp][head][wp.column(i)]) =
-              make_float2(wp.acc[g][i][y] * wp.unit(), wp.acc[g][i][2 + y] * wp.unit());
+              make_float2(wp.acc[g][i][y], wp.acc[g][i][2 + y]);
       }
     __syncthreads();
     const volatile Work& seen = sh_work[turn & 1];

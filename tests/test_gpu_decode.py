@@ -160,6 +160,33 @@ def test_decode_large_scores(fp8):
     check(o, lse, serving.decode(q, c["k64"], c["v64"], c["table"], lens, 1.0), d)
 
 
+def test_decode_factors_of_any_size():
+    """A huge row that the softmax leaves almost out, rows of zeros with factor
+    1 among tiny ones, and a range of 2^90 between factors: the small rows'
+    part of the output is as exact as if they stood alone."""
+    lens, Hkv, d, page = [96, 96, 96], 1, 64, 16
+    c = filled_cache(lens, page, Hkv, d, 55, True)
+    q = make_tensor((3, 4, 1, d), 56)
+    held = c["table"][:, :6].long()
+    for b in range(3):
+        c["vd"][held[b]] *= 2.0 ** -60 if b == 2 else 2.0 ** -40
+    # sequence 0: position 5 has a value of 2^0 and a weight of about e^-100
+    at = (held[0, 0], 0, 5)
+    c["vd"][at] = 1.0
+    c["kc"].view(torch.uint8)[at] = torch.from_numpy(serving.nearest_e4m3(-np.sign(f64(q)[0, 0, 0])))
+    c["kd"][at] = 100 * 8 / float(np.abs(f64(q)[0, 0, 0]).sum())
+    # sequence 1: every third row is zeros, factor 1; sequence 2: one row of 2^30
+    for p in range(0, 96, 3):
+        z = (held[1, p // page], 0, p % page)
+        c["vc"].view(torch.uint8)[z] = 0
+        c["vd"][z] = 1.0
+    c["vd"][held[2, 3], 0, 7] = 2.0 ** 30
+    c["k64"] = serving.cache_values(c["kc"], c["kd"])
+    c["v64"] = serving.cache_values(c["vc"], c["vd"])
+    o, lse = run(q, c, lens)
+    check(o, lse, serving.decode(q, c["k64"], c["v64"], c["table"], lens, 1 / 8), d)
+
+
 def test_decode_nan_and_inf_of_visible_rows_show():
     """A NaN or infinity at a visible position reaches the heads that read it,
     and no others."""
