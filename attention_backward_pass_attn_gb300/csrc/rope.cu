@@ -8,7 +8,7 @@
 // The gradient is the inverse turn, theta -> -theta, so one kernel serves
 // both.  Bound by HBM: every value is read and written once (4 bytes a
 // value), with 3 FLOPs a value.  Video's 16,384 tokens of 32 heads, d=128, out
-// of a fused projection: 48 us (5.6 TB/s).
+// of a fused projection: 46 us (5.9 TB/s).
 //
 // The angle.  pos * inv_freq in fp32 would be off by pos * inv_freq * 2^-24
 // radians, 0.06 at position 10^6.  What matters is the angle modulo one turn,
@@ -17,14 +17,17 @@
 // exponent of inv_freq (integer arithmetic, no FP64, whose rate on this chip
 // is two operations per clock and SM), and pos * F mod 2^64 is the turn:
 // an error of at most (|pos| inv_freq + |pos|) * 2^-64 turns.  Its upper 32
-// bits, read as a signed number of half turns / 2^31, go to sincospif.
+// bits are a quarter turn and a remainder of at most an eighth, x <= pi / 4 in
+// radians, whose sine and cosine are Taylor's polynomials to x^9 and x^8: off
+// by x^11 / 11! < 2^-29 and x^10 / 10! < 2^-25.
 //
-// A block takes a tile of tokens (a thread owns 8 pairs, two 16-byte pieces, of
-// one of them), forms their sines and cosines once and runs over a group of
-// heads of q and k with them.  Blocks that follow one another take tiles that
-// follow one another of the same heads, so that the GPU moves through memory
-// in order: 32,768 tokens of 32 heads, d=128, take 87 us so (6.2 TB/s, 91 % of
-// a copy), and 91 us where every block walked all heads of its tile.
+// A block turns its frequencies into fractions once, takes a tile of tokens (a
+// thread owns 8 pairs, two 16-byte pieces, of one of them), forms their sines
+// and cosines once and runs over a group of heads of q and k with them.  Blocks
+// that follow one another take tiles that follow one another of the same
+// heads, so that the GPU moves through memory in order: 32,768 tokens of 32
+// heads, d=128, take 85 us (6.3 TB/s, 93 % of a copy).  Blocks that walk all
+// heads of their tile took 91; sincospif and a fraction per thread 87.
 #include <algorithm>
 
 #include "kernels.h"
@@ -34,9 +37,9 @@
 namespace attn {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 64;
 constexpr int kPairs = 8;  // per thread
-constexpr int kBlocksPerSm = 10;  // resident
+constexpr int kBlocksPerSm = 20;  // resident
 constexpr int kHeadsPerBlock = 8;  // fewer where that leaves the GPU idle
 
 // floor(2^64 / (2 pi)): the turn of one radian.
@@ -57,12 +60,35 @@ __device__ __forceinline__ uint64_t turn_fraction(float f) {
   return (bits >> 31) ? 0ull - r : r;
 }
 
+// Sine and cosine of turn / 2^32 of a turn.
+__device__ __forceinline__ void sin_cos_of_turn(uint32_t turn, float* s, float* c) {
+  constexpr float kRadians = 1.46291807926715968e-9f;  // 2 pi / 2^32
+  const uint32_t quarter = (turn + 0x20000000u) >> 30;
+  const float x = float(int32_t(turn - (quarter << 30))) * kRadians, x2 = x * x;
+  float p = fmaf(x2, 1.f / 362880.f, -1.f / 5040.f);
+  p = fmaf(p, x2, 1.f / 120.f);
+  p = fmaf(p, x2, -1.f / 6.f);
+  const float sn = fmaf(p * x2, x, x);
+  float q = fmaf(x2, 1.f / 40320.f, -1.f / 720.f);
+  q = fmaf(q, x2, 1.f / 24.f);
+  q = fmaf(q, x2, -0.5f);
+  const float cs = fmaf(q, x2, 1.f);
+  // a quarter turn on: (s, c) -> (c, -s)
+  const float a = quarter & 1 ? cs : sn, b = quarter & 1 ? sn : cs;
+  *s = __uint_as_float(__float_as_uint(a) ^ (quarter & 2) << 30);
+  *c = __uint_as_float(__float_as_uint(b) ^ ((quarter + 1) & 2) << 30);
+}
+
 template <int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) rope_kernel(const RopeArgs a,
                                                                       int head_group) {
   constexpr int kPerToken = D / 2 / kPairs;  // threads of a token
   grid_dep_wait();
   grid_dep_launch();
+  __shared__ uint64_t fraction[D / 2];
+  static_assert(kThreads >= D / 2, "a thread for every frequency");
+  if (threadIdx.x < D / 2) fraction[threadIdx.x] = turn_fraction(__ldg(a.inv_freq + threadIdx.x));
+  __syncthreads();
   const int64_t token = int64_t(blockIdx.x) * (kThreads / kPerToken) + threadIdx.x / kPerToken;
   if (token >= int64_t(a.B) * a.N) return;
   const int part = threadIdx.x % kPerToken;
@@ -79,9 +105,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) rope_kernel(const Rope
       const int i = part * kPairs + j;
       const int at = i < a.axis_end[0] ? p[0] : i < a.axis_end[1] ? p[1]
                      : i < a.axis_end[2] ? p[2] : p[3];
-      const uint64_t turn = uint64_t(int64_t(at)) * turn_fraction(__ldg(a.inv_freq + i));
-      const float half_turns = float(int32_t(turn >> 32)) * 0x1p-31f;
-      sincospif(half_turns, &s[j], &c[j]);
+      const uint64_t turn = uint64_t(int64_t(at)) * fraction[i];
+      sin_cos_of_turn(uint32_t(turn >> 32), &s[j], &c[j]);
       if (a.backward) s[j] = -s[j];
     }
   }
@@ -126,11 +151,11 @@ cudaError_t launch(const RopeArgs& a, cudaStream_t stream) {
   const int64_t tiles = (int64_t(a.B) * a.N + kTokens - 1) / kTokens;
   const int64_t heads = int64_t(a.heads[0]) + a.heads[1];
   // Eight heads share a thread's sines; with few tokens, fewer, down to one,
-  // until every SM has three blocks (4,094 tokens of 32 heads, d=64: 8.6 us
-  // with eight, 10 with four; 64 tokens of 40 heads, d=128: 4.8 us with eight,
-  // 3.1 with one).
+  // until every SM has six blocks (4,094 tokens of 32 heads, d=64: 7.5 us with
+  // eight, 9.2 with four; 800 tokens of 40 heads, d=128: 5.1 us with eight, 4.5
+  // with four).
   int64_t group = kHeadsPerBlock;
-  while (group > 1 && tiles * ((heads + group - 1) / group) < 3 * int64_t(device_sm_count()))
+  while (group > 1 && tiles * ((heads + group - 1) / group) < 6 * int64_t(device_sm_count()))
     group /= 2;
   group = std::max(group, (heads + 65534) / 65535);
   return launch_kernel(rope_kernel<D, INTERLEAVED>,

@@ -1,11 +1,12 @@
 """Rotary positions and their gradient on the GPU against the fp64 oracle.
 
 Tolerance, per element: the result is rounded once to bf16 (half a step, 2^-8
-of the value).  Before that, the angle: its turn is read as float half turns,
-relative error 2^-25 of at most 1 half turn, so pi 2^-25 < 2^-23 radians, plus
-2^-32 turns of truncation; the sine and cosine are within 2 units of their last
-place, 2^-22; the two products and the sum round at 2^-24 each.  Together less
-than 2^-20 (|a| + |b|) for a pair (a, b).
+of the value).  Before that, the angle: its turn is known to 2^-32, 2^-29
+radians, and the remainder of a quarter turn, at most pi / 4, is converted and
+scaled in fp32, two roundings and a constant's, 3 pi/4 2^-24 < 2^-22 radians
+together; the sine and cosine of that are within 2^-22 (polynomials cut off
+below 2^-25, and their last roundings); the two products and the sum round at
+2^-24 each.  Together less than 2^-20 (|a| + |b|) for a pair (a, b).
 """
 
 import numpy as np
