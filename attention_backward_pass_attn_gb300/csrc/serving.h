@@ -92,8 +92,8 @@ struct DecodeArgs {
   float* part_o;         // workspace: [2 * blocks][16][d] unnormalised output
   int* err;
 };
-// Thread blocks the split's workspace provides for.
-constexpr int kDecodeMaxBlocks = 608;
+// Thread blocks the split's workspace provides for: three for each of 152 SMs.
+constexpr int kDecodeMaxBlocks = 456;
 constexpr int kDecodeHeads = 16;  // heads of one key/value head a block works on at most
 inline size_t decode_arrival_bytes() {
   return sizeof(unsigned long long) * 2 * size_t(kDecodeMaxBlocks);  // one of the two arrays
