@@ -15,7 +15,8 @@
  * The N x N matrices S, P, dP, dS are never stored: each kernel recomputes
  * them tile by tile on the tensor cores.
  *
- * Layout and types (every entry point).
+ * Layout and types (the attention entry points; the Mamba-2 layer and the
+ * answering path state their own).
  *   Q, K, V, O, dO, dQ, dK, dV : bf16 (raw uint16 bits), contiguous
  *                                [B][H][N][d], 16-byte aligned.
  *   L                          : fp32 [B][H][N], natural-log log-sum-exp.
@@ -453,7 +454,9 @@ int attn_last_device_error(void* stream);
 /*
  * Interface utility; the paper has no counterpart.
  * Like attn_last_device_error, but also stores the raw error word
- * ((code << 24) | site, 0 if none) in *word before clearing it.
+ * ((code << 24) | site, 0 if none) in *word before clearing it.  Code 4 is an
+ * index outside the paged cache: a length or position (site 0x501), or a page
+ * of attn_decode (0x502), kv_cache_write (0x503) or kv_cache_read (0x504).
  */
 int attn_device_error_word(void* stream, int* word);
 

@@ -220,7 +220,7 @@ def test_decode_bad_pages_and_lengths(fp8):
     c["table"][2, :] = 2 ** 31 - 1
     q = make_tensor((4, 6, 1, d), 26)
     o, lse = run(q, c, lens)
-    assert ab.attn_last_device_error() == ab.ATTN_ERR_DEVICE
+    assert ab.attn_device_error_word() == (ab.ATTN_ERR_DEVICE, 4 << 24 | 0x502)
     check(o, lse, serving.decode(q, c["k64"], c["v64"], c["table"], lens, 1 / 8), d)
     c = filled_cache(lens, page, Hkv, d, 25, fp8, slack=0)
     bad = [10 ** 9, -5, 30, 48]
@@ -235,7 +235,7 @@ def test_decode_bad_pages_and_lengths(fp8):
         else:
             c[n + "c"] = torch.nan_to_num(c[n + "c"])
     o, lse = run(q, c, bad)
-    assert ab.attn_last_device_error() == ab.ATTN_ERR_DEVICE
+    assert ab.attn_device_error_word() == (ab.ATTN_ERR_DEVICE, 4 << 24 | 0x501)
     check(o, lse, ref, d)
 
 
