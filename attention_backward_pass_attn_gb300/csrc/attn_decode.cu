@@ -32,8 +32,10 @@
 //
 // Measured (one call among others in a graph): 131,072 positions, 8 key heads
 // x 4, d=128, bf16: 84 us, 6.4 TB/s, of which the walk over the keys is 76; 32
-// sequences of up to 8,192, 8 key heads x 8, e4m3: 54 us for 264 MB; 500
-// positions of 16 heads: 7.2 us, 2.7 of them from the arrivals on.
+// sequences of up to 8,192, 8 key heads x 8, e4m3: 52 us for 264 MB; 500
+// positions of 16 heads: 7.2 us, 2.7 of them from the arrivals on.  256
+// sequences of up to 256, 8 key heads x 4, bound by the changes of sequence:
+// e4m3 32 us for 67 MB, bf16 37 us for 131 MB.
 //
 // Rounding.  Scores, maxima, sums and outputs are fp32.  The weights p (times
 // V's factor of an e4m3 row) meet V as a sum of two bf16 numbers, 16 bits in
@@ -118,6 +120,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
+
+// Magnitudes of two bf16 numbers compare as integers.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 
 // Reduction over the lanes that hold different keys of the same head.
 __device__ __forceinline__ float keys_max(float x) {
@@ -252,27 +261,35 @@ struct Warp {
     for (int g = 0; g < NG; ++g) {
       float f = a.scale_log2;
       if (FP8) {
-        float amax = 0.f;
+        // Largest finite magnitude, as bf16 bits, two at a time; infinities
+        // and NaN, which would sort above, are rare and sorted out apart.
+        uint32_t top = 0;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+          top = max_u16x2(top, max_u16x2(qf[g][s][0] & 0x7FFF7FFFu, qf[g][s][1] & 0x7FFF7FFFu));
+        if (((top & 0xFFFFu) >= 0x7F80u) | (top >= 0x7F800000u)) {
+          top = 0;
+#pragma unroll
+          for (int s = 0; s < D / 8; ++s) {
+            const uint32_t w = qf[g][s / 2][s % 2] & 0x7FFF7FFFu;
+            top = max_u16x2(top, ((w & 0xFFFFu) < 0x7F80u ? w & 0xFFFFu : 0u) |
+                                     (w < 0x7F800000u ? w & 0xFFFF0000u : 0u));
+          }
+        }
+        top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        top = max(top & 0xFFFFu, top >> 16);
+        // 2^e puts the largest element into [2^14, 2^15).  The product is
+        // exact in bf16 but for what lies far below fp16's smallest number.
+        const int e = min(14 - (int(top >> 7) - 127), 126);
+        const uint32_t up = uint32_t(e + 127) * 0x00800080u;  // as two bf16
 #pragma unroll
         for (int s = 0; s < D / 16; ++s)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const float u = fabsf(bf16lo_to_f32(qf[g][s][x]));
-            const float v = fabsf(bf16hi_to_f32(qf[g][s][x]));
-            if (u < INFINITY) amax = fmaxf(amax, u);
-            if (v < INFINITY) amax = fmaxf(amax, v);
+            const uint32_t w = mul_bf16x2(qf[g][s][x], up);
+            qf[g][s][x] = pack_f16x2(bf16lo_to_f32(w), bf16hi_to_f32(w));
           }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        // 2^e puts the largest element into [2^14, 2^15)
-        const int e = min(14 - (int(__float_as_uint(amax) >> 23) - 127), 126);
-        const float up = pow2f(e);
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s)
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            qf[g][s][x] = pack_f16x2(bf16lo_to_f32(qf[g][s][x]) * up,
-                                     bf16hi_to_f32(qf[g][s][x]) * up);
         f *= pow2f(-e);
       }
       // the lane of head 2q (+1) holds that column's factor
@@ -634,8 +651,9 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
   using C = Cfg<D, FP8>;
   constexpr int U = C::kUnit;
   constexpr int kHeadStride = D + 8;
-  __shared__ float sh_o[kWarps][NG * 8][kHeadStride];
-  __shared__ float sh_ml[kWarps][NG * 8][2];
+  __shared__ __align__(16) float sh_o[kWarps][NG * 8][kHeadStride];
+  __shared__ __align__(8) float sh_ml[kWarps][NG * 8][2];
+  static_assert(kWarps == 4, "the joins below take four warps' results");
   __shared__ int64_t sh_scan[kWarps];
   __shared__ int64_t sh_W;
   __shared__ Work sh_work[2];
@@ -711,17 +729,18 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
   Warp<D, FP8, NG> wp(a);
   int64_t rows;
   // A run's first loads.
+  auto key_head = [&](int h) { return int(fast_div(h, a.block_div)); };
   auto heads_of = [&](int h) {
-    return min(a.block_heads, a.group - h % a.group_blocks * a.block_heads);
+    return min(a.block_heads, a.group - (h - key_head(h) * a.group_blocks) * a.block_heads);
   };
   auto first_head = [&](int h) {
-    return h / a.group_blocks * a.group + h % a.group_blocks * a.block_heads;
+    return key_head(h) * a.group + (h - key_head(h) * a.group_blocks) * a.block_heads;
   };
   auto first_tile = [&](const Work& w) {
     return (w.lo & ~(kPageQuantum - 1)) + w.u * U + warp * C::KT * 16;
   };
   auto enter = [&](const Work& w) {
-    rows = wp.find(a.c.table + int64_t(w.b) * a.c.max_pages, w.h / a.group_blocks, first_tile(w),
+    rows = wp.find(a.c.table + int64_t(w.b) * a.c.max_pages, key_head(w.h), first_tile(w),
                    w.len);
     wp.load_q(w.b, first_head(w.h), heads_of(w.h));
     wp.load_k(rows);
@@ -747,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
       }
       wp.begin();
       const int* table = a.c.table + int64_t(w.b) * a.c.max_pages;
-      const int kvh = w.h / a.group_blocks;
+      const int kvh = key_head(w.h);
       int tile = first_tile(w);
       bool full = wp.full(rows, tile, w.lo, w.len);
       // The last step stands apart: it has nothing to load.
@@ -758,7 +777,8 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
         rows = next_rows;
         full = wp.full(rows, tile, w.lo, w.len);
       }
-      wp.template step<false>(rows, full, tile, w.lo, w.len, 0);
+      // ... and a warp past the end of a sequence no keys
+      if (tile < w.len) wp.template step<false>(rows, full, tile, w.lo, w.len, 0);
     }
 
     // The run's results leave the registers; the next run's first loads are
@@ -803,29 +823,34 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
     const int heads = heads_of(seen.h);
     const int64_t out = int64_t(seen.b) * a.Hq + first_head(seen.h);
     const int slot = 2 * blockIdx.x + (turn ? 1 : 0);
-    for (int i = tid; i < heads * (D / 2); i += kThreads) {
-      const int head = i / (D / 2), c = 2 * (i % (D / 2));
-      float M = -INFINITY;
+    for (int i = tid; i < heads * (D / 4); i += kThreads) {
+      const int head = i / (D / 4), c = 4 * (i % (D / 4));
+      float2 ml[kWarps];
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sh_ml[w][head][0]);
+      for (int w = 0; w < kWarps; ++w) ml[w] = *reinterpret_cast<float2*>(sh_ml[w][head]);
+      const float M = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
       const float ref = M == -INFINITY ? 0.f : M;
-      float sum = 0.f, o0 = 0.f, o1 = 0.f;
+      float sum = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float e = ex2(sh_ml[w][head][0] - ref);
-        sum += e * sh_ml[w][head][1];
-        o0 += e * sh_o[w][head][c];
-        o1 += e * sh_o[w][head][c + 1];
+        const float e = ex2(ml[w].x - ref);
+        const float4 v = *reinterpret_cast<const float4*>(&sh_o[w][head][c]);
+        sum += e * ml[w].y;
+        o.x += e * v.x;
+        o.y += e * v.y;
+        o.z += e * v.z;
+        o.w += e * v.w;
       }
       if (whole) {
         const int64_t row = out + head;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + row * D + c) =
-            pack_bf16x2(o0 * inv, o1 * inv);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + row * D + c) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
         if (c == 0) a.lse[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
       } else {
         const int64_t at = int64_t(slot) * kDecodeHeads + head;
-        *reinterpret_cast<float2*>(a.part_o + at * D + c) = make_float2(o0, o1);
+        *reinterpret_cast<float4*>(a.part_o + at * D + c) = o;
         if (c == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(M, sum);
       }
     }
@@ -894,6 +919,7 @@ cudaError_t launch_decode(const DecodeArgs& args, cudaStream_t stream) {
   a.group_blocks = (a.group + kDecodeHeads - 1) / kDecodeHeads;
   a.block_heads = (a.group + a.group_blocks - 1) / a.group_blocks;
   a.head_blocks = a.c.Hkv * a.group_blocks;
+  a.block_div = make_fast_div(a.group_blocks);
   if (a.c.d == 64)
     return a.c.kd ? launch_heads<64, true>(a, stream) : launch_heads<64, false>(a, stream);
   return a.c.kd ? launch_heads<128, true>(a, stream) : launch_heads<128, false>(a, stream);

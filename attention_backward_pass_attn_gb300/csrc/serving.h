@@ -86,6 +86,7 @@ struct DecodeArgs {
   // most kDecodeHeads (the last may have fewer)
   int group, group_blocks, block_heads;
   int head_blocks;       // of a sequence
+  FastDiv block_div;     // by group_blocks
   unsigned long long *arrivals, *arrivals2;  // workspace: a word per slot each, see arrive()
   unsigned long long tag;        // 48 bits, another one for every call
   float *part_ml, *part_ml2;  // workspace: [2 * blocks][16][2] running maximum and sum

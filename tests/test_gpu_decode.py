@@ -211,6 +211,29 @@ def test_decode_nan_and_inf_of_visible_rows_show():
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_queries_of_any_magnitude(fp8, d):
+    """Heads of one sequence from zero over subnormal numbers to ordinary ones,
+    large and tiny elements in one head; an infinite element leaves the other
+    heads bit for bit."""
+    lens, Hkv, group, page = [90, 300], 2, 8, 16
+    c = filled_cache(lens, page, Hkv, d, 17, fp8)
+    q = make_tensor((2, Hkv * group, 1, d), 18)
+    for h, e in enumerate([None, -133, -126, -100, -40, -14, -3, 0] * 2):
+        q[:, h] = 0 if e is None else (q[:, h].double() * 2.0 ** e).to(q.dtype)
+    q[:, 9, :, ::2] *= 2.0 ** -60
+    q[:, 10, :, 1::3] *= 2.0 ** 8
+    o, lse = run(q, c, lens)
+    check(o, lse, serving.decode(q, c["k64"], c["v64"], c["table"], lens, d ** -0.5), d)
+    bad = q.clone()
+    bad[1, 5, 0, 6], bad[1, 12, 0, d - 1] = float("inf"), float("-inf")
+    o2, lse2 = run(bad, c, lens)
+    others = [h for h in range(16) if h not in (5, 12)]
+    assert torch.equal(o2[:, others], o[:, others]) and torch.equal(lse2[:, others], lse[:, others])
+    assert torch.equal(o2[0], o[0]) and not torch.isfinite(lse2[1, [5, 12]]).any()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_decode_bad_pages_and_lengths(fp8):
     """Entries outside the cache and lengths outside the table: the positions
     are skipped, the error word says so, and good sequences are unharmed."""
