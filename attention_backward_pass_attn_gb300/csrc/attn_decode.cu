@@ -571,8 +571,11 @@ __device__ __forceinline__ void join_weights(const DecodeArgs& a, const Parts& p
   const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    x[i].x = lane + kLanes * i <= last ? ex2(x[i].x - ref) : 0.f;
-    sum += x[i].x == 0.f ? 0.f : x[i].x * x[i].y;
+    // What does not count is told by its index, not by its weight: a part whose
+    // scores are all NaN has no maximum, weight 0, and a sum that must show.
+    const bool counts = lane + kLanes * i <= last;
+    x[i].x = counts ? ex2(x[i].x - ref) : 0.f;
+    sum += counts ? x[i].x * x[i].y : 0.f;
   }
 #pragma unroll
   for (int s = kLanes / 2; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
