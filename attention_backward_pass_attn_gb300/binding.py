@@ -423,8 +423,13 @@ def ssd_bwd(x, dt, A, B, C, D, dy, workspace=None, out=None, stream=None):
 # its checks.
 _E4M3_DTYPES = (torch.float8_e4m3fn, torch.uint8)
 _DEVICES = [torch.device("cuda", i) for i in range(64)]  # cheaper to pass than an index
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+# PyTorch's own shortcuts where it has them; a build without CUDA does not, and
+# the host-side checks work there too.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing",
+                     torch.cuda.is_current_stream_capturing)
 
 
 def _device_index(t: torch.Tensor, name: str) -> int:
@@ -700,7 +705,7 @@ _decode_workspaces = {}
 
 def _decode_workspace(dev: int, stream):
     handle = _stream_on(stream, dev)
-    if stream is not None or torch._C._cuda_isCurrentStreamCapturing():
+    if stream is not None or _capturing():
         n = int(load_library().attn_decode_workspace_size(128))
         return _empty((n,), torch.uint8, dev, stream), handle
     ws = _decode_workspaces.get((dev, handle))
