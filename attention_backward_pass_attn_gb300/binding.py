@@ -698,18 +698,29 @@ def alloc_decode_workspace(d: int, device) -> torch.Tensor:
 
 
 # attn_decode's own workspaces, one for every stream it was called on without
-# one: calls on a stream follow one another.  A call that is being captured
-# gets memory of its graph instead, which may replay on any stream.
+# one: calls on a stream follow one another.  Only for streams that live as long
+# as the process, the default one and those of PyTorch's pool, whose handle is
+# theirs alone.  Any other owner may destroy its stream, and the handle then be
+# another stream's while work of the first still runs; such a call allocates,
+# as every call does for its results.  A call that is being captured gets
+# memory of its graph, which may replay on any stream.
 _decode_workspaces = {}
+_PER_THREAD_STREAM = 2  # cudaStreamPerThread: one handle, a stream in every thread
 
 
 def _decode_workspace(dev: int, stream):
     handle = _stream_on(stream, dev)
+    if handle == _PER_THREAD_STREAM:
+        # kept or freed and handed out again, it would reach another thread's stream
+        raise ValueError("workspace must be given on the per-thread default stream")
     if stream is not None or _capturing():
         n = int(load_library().attn_decode_workspace_size(128))
         return _empty((n,), torch.uint8, dev, stream), handle
     ws = _decode_workspaces.get((dev, handle))
     if ws is None:
+        if handle and torch.cuda.current_stream(dev).stream_id == handle:  # not PyTorch's own
+            n = int(load_library().attn_decode_workspace_size(128))
+            return _empty((n,), torch.uint8, dev, None), handle
         ws = _decode_workspaces[(dev, handle)] = alloc_decode_workspace(128, dev)
     return ws, handle
 
@@ -724,7 +735,9 @@ def attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, k_descale
     window > 0: only the last ``window`` positions are seen.
     Returns (O bf16 [B, Hq, 1, d], L fp32 [B, Hq, 1]); a sequence of length 0
     has O = 0 and L = -inf.  workspace: from alloc_decode_workspace; without
-    one, the call uses one that is kept for its stream.
+    one, the call uses one that is kept for its stream (7.5 MB; allocated anew
+    on a stream that is not PyTorch's, or in a graph), and is refused on the
+    per-thread default stream.
     """
     dev = _device_index(q, "q")
     P, Hkv, ps, d, B, mp = _check_cache(k_cache, v_cache, k_descale, v_descale, page_table, dev)

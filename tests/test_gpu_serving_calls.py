@@ -1,0 +1,84 @@
+"""Calls of the answering path that its documentation allows and whose sizes or
+streams are out of the ordinary."""
+
+import ctypes
+
+import pytest
+import torch
+
+from attention_backward_pass_attn_gb300 import binding as ab
+from attention_backward_pass_attn_gb300.inputs import make_tensor
+from test_gpu_decode import cuda_ready, i32  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def small(B=2, Hkv=2, d=64, page=16, n=70, seed=5):
+    """A cache with its table and lengths, and queries, on the GPU."""
+    mp = -(-n // page)
+    kc, vc, _, _ = ab.alloc_kv_cache(B * mp, Hkv, page, d, "cuda")
+    table = torch.arange(B * mp, dtype=torch.int32).view(B, mp).cuda()
+    x = make_tensor((B, Hkv, n, d), seed).cuda()
+    ab.kv_cache_write(x, x, kc, vc, table, torch.zeros(B, dtype=torch.int32, device="cuda"))
+    return make_tensor((B, 2 * Hkv, 1, d), seed + 1).cuda(), kc, vc, table, i32([n] * B).cuda()
+
+
+def same(a, b):
+    return torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_kept_workspaces_of_two_streams_at_once():
+    """Long sequences, so that every block leaves parts, on two streams of the
+    pool that take turns, without a workspace of the caller's."""
+    batches = [small(B=1, n=5000 + 900 * i, seed=20 + i) for i in range(2)]
+    ref = [ab.attn_decode(*x) for x in batches]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(30):
+        for x, s, g in zip(batches, streams, got):
+            with torch.cuda.stream(s):
+                g.append(ab.attn_decode(*x))
+    torch.cuda.synchronize()
+    for g, r in zip(got, ref):
+        assert all(same(x, r) for x in g)
+    held = {h for _, h in ab._decode_workspaces}
+    assert {s.cuda_stream for s in streams} <= held
+
+
+def external_stream():
+    cudart = torch.cuda.cudart()
+    handle = ctypes.c_void_p()
+    assert int(cudart.cudaStreamCreate(ctypes.addressof(handle))) == 0
+    return handle.value, cudart
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_streams_of_another_owner_have_no_kept_workspace(given):
+    args = small(n=3000)
+    ref = ab.attn_decode(*args)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        handle, cudart = external_stream()
+        if given:
+            got = ab.attn_decode(*args, stream=handle)
+        else:
+            with torch.cuda.stream(torch.cuda.ExternalStream(handle)):
+                got = ab.attn_decode(*args)
+        torch.cuda.synchronize()
+        assert same(got, ref)
+        assert handle not in {h for _, h in ab._decode_workspaces}
+        assert int(cudart.cudaStreamDestroy(handle)) == 0
+
+
+def test_the_per_thread_stream_takes_a_workspace():
+    args = small(n=3000)
+    ref = ab.attn_decode(*args)
+    ws = ab.alloc_decode_workspace(64, "cuda")
+    out, lse = torch.zeros_like(ref[0]), torch.zeros_like(ref[1])
+    torch.cuda.synchronize()
+    with pytest.raises(ValueError, match="workspace"):
+        ab.attn_decode(*args, stream=2)
+    ab.attn_decode(*args, out=out, lse=lse, workspace=ws, stream=2)
+    torch.cuda.synchronize()
+    assert same((out, lse), ref)
