@@ -757,9 +757,13 @@ def attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, k_descale
         _check_like(lse, "lse", (B, Hq, 1), torch.float32, dev)
     if workspace is None:
         workspace, handle = _decode_workspace(dev, stream)
-    elif workspace.get_device() != dev:
-        raise ValueError("workspace must be on CUDA device %d, like the first tensor" % dev)
     else:
+        if not isinstance(workspace, torch.Tensor):
+            raise TypeError("workspace must be a torch.Tensor")
+        if workspace.get_device() != dev:
+            raise ValueError("workspace must be on CUDA device %d, like the first tensor" % dev)
+        if not workspace.is_contiguous():  # its bytes would not be its memory
+            raise ValueError("workspace must be contiguous")
         handle = _stream_on(stream, dev)
     if k_descale is None:
         kd = vd = None

@@ -82,3 +82,16 @@ def test_the_per_thread_stream_takes_a_workspace():
     ab.attn_decode(*args, out=out, lse=lse, workspace=ws, stream=2)
     torch.cuda.synchronize()
     assert same((out, lse), ref)
+
+
+def test_a_workspace_that_is_not_its_own_memory_is_refused():
+    """An expanded byte has as many bytes as asked for, and memory for one."""
+    args = small()
+    n = ab.load_library().attn_decode_workspace_size(64)
+    one = torch.zeros(1, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError, match="contiguous"):
+        ab.attn_decode(*args, workspace=one.expand(n))
+    with pytest.raises(ValueError, match="contiguous"):
+        ab.attn_decode(*args, workspace=torch.zeros(n, 2, dtype=torch.uint8, device="cuda")[:, 0])
+    with pytest.raises(TypeError):
+        ab.attn_decode(*args, workspace=n)
