@@ -421,6 +421,7 @@ def ssd_bwd(x, dt, A, B, C, D, dy, workspace=None, out=None, stream=None):
 # The checks come first as one cheap test; only what fails it is looked at for
 # the reason, so that a call of a few microseconds on the GPU is not drowned by
 # its checks.
+_INT_MAX = 2 ** 31 - 1  # ctypes would drop the bits above
 _E4M3_DTYPES = (torch.float8_e4m3fn, torch.uint8)
 _DEVICES = [torch.device("cuda", i) for i in range(64)]  # cheaper to pass than an index
 # PyTorch's own shortcuts where it has them; a build without CUDA does not, and
@@ -769,9 +770,10 @@ def attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, k_descale
         kd = vd = None
     else:
         kd, vd = k_descale.data_ptr(), v_descale.data_ptr()
+    window = max(-1, min(int(window), _INT_MAX))  # what no length reaches hides nothing
     st = load_library().attn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kd, vd,
                                     page_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
-                                    lse.data_ptr(), B, Hq, Hkv, d, ps, P, mp, int(window),
+                                    lse.data_ptr(), B, Hq, Hkv, d, ps, P, mp, window,
                                     _default_scale(d, scale), workspace.data_ptr(),
                                     workspace.nbytes, handle)
     if st:

@@ -95,3 +95,15 @@ def test_a_workspace_that_is_not_its_own_memory_is_refused():
         ab.attn_decode(*args, workspace=torch.zeros(n, 2, dtype=torch.uint8, device="cuda")[:, 0])
     with pytest.raises(TypeError):
         ab.attn_decode(*args, workspace=n)
+
+
+def test_windows_beyond_32_bits_are_not_wrapped():
+    args = small()
+    whole = ab.attn_decode(*args)
+    for w in (70, 2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5, 2 ** 40):
+        assert same(ab.attn_decode(*args, window=w), whole)
+    assert not same(ab.attn_decode(*args, window=5), whole)
+    for w in (-1, -2 ** 31, -2 ** 32, -2 ** 32 + 5):
+        with pytest.raises(ab.AttnError) as e:
+            ab.attn_decode(*args, window=w)
+        assert e.value.status == ab.ATTN_ERR_INVALID_ARG
