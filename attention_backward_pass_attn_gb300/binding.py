@@ -656,6 +656,8 @@ def kv_cache_write(k, v, k_cache, v_cache, page_table, start, count=None, k_desc
     shape = (B, Hkv, T, d)
     strides = _check_rows(k, "k", shape, dev) + _check_rows(v, "v", shape, dev)
     _check_span(start, count, B, dev)
+    if B * Hkv * T > _INT_MAX:  # expanded rows take no memory
+        _check("kv_cache_write", ATTN_ERR_UNSUPPORTED)
     st = load_library().kv_cache_write(k.data_ptr(), v.data_ptr(),
                                        _array(ctypes.c_int64, strides),
                                        k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_descale),

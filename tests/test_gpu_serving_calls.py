@@ -107,3 +107,18 @@ def test_windows_beyond_32_bits_are_not_wrapped():
         with pytest.raises(ab.AttnError) as e:
             ab.attn_decode(*args, window=w)
         assert e.value.status == ab.ATTN_ERR_INVALID_ARG
+
+
+def test_an_append_beyond_32_bits_is_refused():
+    """One token in memory, expanded to more than an int's worth of tokens."""
+    _, kc, vc, table, _ = small()
+    before = kc.clone()
+    x = torch.ones(1, 1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    start = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for T in (2 ** 29, 2 ** 31, 2 ** 32 + 1):
+        x4 = x.expand(2, 2, T, 64)
+        with pytest.raises(ab.AttnError) as e:
+            ab.kv_cache_write(x4, x4, kc, vc, table, start)
+        assert e.value.status == ab.ATTN_ERR_UNSUPPORTED
+    torch.cuda.synchronize()
+    assert torch.equal(kc, before)
