@@ -700,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
     int lo, len;
     if (sequence_units<U>(a, b, &lo, &len)) continue;
     uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + int64_t(b) * a.Hq * D);
-    for (int i = tid; i < a.Hq * D / 2; i += kThreads) o[i] = 0;
+    for (int64_t i = tid; i < int64_t(a.Hq) * (D / 2); i += kThreads) o[i] = 0;
     for (int i = tid; i < a.Hq; i += kThreads) a.lse[int64_t(b) * a.Hq + i] = -INFINITY;
   }
 

@@ -122,3 +122,18 @@ def test_an_append_beyond_32_bits_is_refused():
         assert e.value.status == ab.ATTN_ERR_UNSUPPORTED
     torch.cuda.synchronize()
     assert torch.equal(kc, before)
+
+
+def test_heads_whose_values_pass_31_bits():
+    """2^24 heads of 128 values: an empty sequence's zeros, and a sequence of
+    one position, whose answer is its value."""
+    H, d = 1 << 24, 128
+    kc, vc, _, _ = ab.alloc_kv_cache(2, 1, 16, d, "cuda")
+    v = make_tensor((1, 1, 1, d), 3).cuda()
+    table = i32([[0], [1]]).cuda()
+    kc[1, 0, 0], vc[1, 0, 0] = v[0, 0, 0], v[0, 0, 0]
+    q = torch.zeros(2, H, 1, d, dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, float("nan"))
+    o, lse = ab.attn_decode(q, kc, vc, table, i32([0, 1]).cuda(), out=out)
+    assert bool((o[0] == 0).all()) and bool(torch.isneginf(lse[0]).all())
+    assert bool((o[1] == v[0]).all()) and bool((lse[1] == 0).all())
