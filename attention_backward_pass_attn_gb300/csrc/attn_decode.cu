@@ -43,9 +43,16 @@
 // bf16.  The second instruction costs nothing with a bf16 cache and 2 % with
 // an e4m3 one, where one fp16 number would do if the factors were known to be
 // of similar size.  An e4m3 K is widened to fp16 (exact) and meets a q scaled by
-// a power of two into fp16's range (exact down to 2^-29 of its largest
-// element); V is widened to bf16 (exact).
+// a power of two into fp16's range, where that is exact too: where the head's
+// nonzero elements lie within 31 binades.  Where they do not, K is widened to
+// bf16 (exact) and meets q's own numbers, scaled clear of overflow: exact down
+// to 2^-222 of the head's largest element.  fp16 is the faster of the two, one
+// conversion for a pair of values where bf16 takes four (the batch above with
+// a choice for every product: 58 us); telling them apart costs 0.4 % there, 2 %
+// for the 256 short sequences.  V is widened to bf16 (exact).
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "f32x2.cuh"
 #include "kernels.h"
@@ -59,6 +66,10 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kLn2 = 0.69314718055994531f;
+
+// How many binades below a head's largest element, scaled into [2^14, 2^15),
+// fp16 holds all 8 bits of a bf16 number: those of 2^-17 end at 2^-24.
+constexpr uint32_t kFp16Span = 31;
 
 // D, the cache's type and the number of 8-head column tiles (1 or 2) fix the
 // rest: KT runs of 16 keys per warp and step, so that a step's K (and its V)
@@ -125,6 +136,17 @@ __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t min_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t add_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 
@@ -223,6 +245,7 @@ struct Warp {
   uint32_t kw[KT * 2 * C::kChunks][4];
   uint32_t vw[KT][4][C::kVWords];
   float kd[FP8 ? KT : 1][2], vd[FP8 ? KT : 1][2];
+  bool wide;  // FP8: q is held in bf16, see kFp16Span
   uint32_t qf[NG][D / 16][2];
   float factor[NG][2];
   float m[NG][2], l[NG][2];
@@ -257,38 +280,53 @@ struct Warp {
   // The running state's start; q in the products' type, and what turns a
   // product into a score.
   __device__ __forceinline__ void begin() {
+    uint32_t top[NG];
+    wide = false;
+    if (FP8) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        // Largest finite and smallest nonzero magnitude, as bf16 bits, two at a
+        // time, the latter less one: a zero becomes the largest number.
+        // Infinities and NaN, which would sort above, are rare and sorted out
+        // apart.
+        uint32_t hi = 0, lo = 0xFFFFFFFFu;
+#pragma unroll
+        for (int s = 0; s < D / 8; ++s) {
+          const uint32_t w = qf[g][s / 2][s % 2] & 0x7FFF7FFFu;
+          hi = max_u16x2(hi, w);
+          lo = min_u16x2(lo, add_u16x2(w, 0xFFFFFFFFu));
+        }
+        if (((hi & 0xFFFFu) >= 0x7F80u) | (hi >= 0x7F800000u)) {
+          hi = 0;
+#pragma unroll
+          for (int s = 0; s < D / 8; ++s) {
+            const uint32_t w = qf[g][s / 2][s % 2] & 0x7FFF7FFFu;
+            hi = max_u16x2(hi, ((w & 0xFFFFu) < 0x7F80u ? w & 0xFFFFu : 0u) |
+                                   (w < 0x7F800000u ? w & 0xFFFF0000u : 0u));
+          }
+        }
+        hi = max_u16x2(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
+        hi = max_u16x2(hi, __shfl_xor_sync(0xffffffffu, hi, 2));
+        top[g] = max(hi & 0xFFFFu, hi >> 16) >> 7;
+        lo = min(lo & 0xFFFFu, lo >> 16) >> 7;
+        wide |= top[g] > lo + kFp16Span;
+      }
+      wide = __any_sync(0xffffffffu, wide);
+    }
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       float f = a.scale_log2;
       if (FP8) {
-        // Largest finite magnitude, as bf16 bits, two at a time; infinities
-        // and NaN, which would sort above, are rare and sorted out apart.
-        uint32_t top = 0;
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s)
-          top = max_u16x2(top, max_u16x2(qf[g][s][0] & 0x7FFF7FFFu, qf[g][s][1] & 0x7FFF7FFFu));
-        if (((top & 0xFFFFu) >= 0x7F80u) | (top >= 0x7F800000u)) {
-          top = 0;
-#pragma unroll
-          for (int s = 0; s < D / 8; ++s) {
-            const uint32_t w = qf[g][s / 2][s % 2] & 0x7FFF7FFFu;
-            top = max_u16x2(top, ((w & 0xFFFFu) < 0x7F80u ? w & 0xFFFFu : 0u) |
-                                     (w < 0x7F800000u ? w & 0xFFFF0000u : 0u));
-          }
-        }
-        top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        top = max(top & 0xFFFFu, top >> 16);
-        // 2^e puts the largest element into [2^14, 2^15).  The product is
-        // exact in bf16 but for what lies far below fp16's smallest number.
-        const int e = min(14 - (int(top >> 7) - 127), 126);
+        // 2^e puts the largest element into [2^14, 2^15) for fp16, into
+        // [2^96, 2^97) where bf16 has to hold the row.
+        const int e = min((wide ? 96 : 14) + 127 - int(top[g]), 126);
         const uint32_t up = uint32_t(e + 127) * 0x00800080u;  // as two bf16
 #pragma unroll
         for (int s = 0; s < D / 16; ++s)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const uint32_t w = mul_bf16x2(qf[g][s][x], up);
-            qf[g][s][x] = pack_f16x2(bf16lo_to_f32(w), bf16hi_to_f32(w));
+            qf[g][s][x] = wide ? w : pack_f16x2(bf16lo_to_f32(w), bf16hi_to_f32(w));
           }
         f *= pow2f(-e);
       }
@@ -410,6 +448,7 @@ struct Warp {
   }
 
   // S^T of one run of 16 keys.
+  template <bool WIDE>
   __device__ __forceinline__ void scores(int t, float (&s)[NG][4]) {
 #pragma unroll
     for (int g = 0; g < NG; ++g) s[g][0] = s[g][1] = s[g][2] = s[g][3] = 0.f;
@@ -420,6 +459,14 @@ struct Warp {
       if (FP8) {
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
+          if (WIDE) {
+            const uint32_t a0 = e4m3x2_to_bf16x2(x[w]), a2 = e4m3x2_to_bf16x2(x[w] >> 16);
+            const uint32_t a1 = e4m3x2_to_bf16x2(y[w]), a3 = e4m3x2_to_bf16x2(y[w] >> 16);
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+              mma_16x8x16<false>(s[g], a0, a1, a2, a3, qf[g][4 * c + w][0], qf[g][4 * c + w][1]);
+            continue;
+          }
           const uint32_t a0 = e4m3x2_to_f16x2(x[w]), a2 = e4m3x2_to_f16x2(x[w] >> 16);
           const uint32_t a1 = e4m3x2_to_f16x2(y[w]), a3 = e4m3x2_to_f16x2(y[w] >> 16);
 #pragma unroll
@@ -497,12 +544,12 @@ struct Warp {
   }
 
   // One step's keys; MORE: with the loads of the next step's among it.
-  template <bool MORE>
+  template <bool MORE, bool WIDE>
   __device__ __forceinline__ void step(int64_t rows, bool full, int tile, int lo, int len,
                                        int64_t next_rows) {
     float s[KT][NG][4];
 #pragma unroll
-    for (int t = 0; t < KT; ++t) scores(t, s[t]);
+    for (int t = 0; t < KT; ++t) scores<WIDE>(t, s[t]);
     uint32_t p[KT][NG][2][2];
     weigh(s, full, rows, tile, lo, len, p);
     if (MORE) load_k(next_rows);
@@ -770,18 +817,25 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
       wp.begin();
       const int* table = a.c.table + int64_t(w.b) * a.c.max_pages;
       const int kvh = key_head(w.h);
-      int tile = first_tile(w);
-      bool full = wp.full(rows, tile, w.lo, w.len);
-      // The last step stands apart: it has nothing to load.
-      for (int i = 1; i < units; ++i) {
-        const int64_t next_rows = wp.find(table, kvh, tile + U, w.len);
-        wp.template step<true>(rows, full, tile, w.lo, w.len, next_rows);
-        tile += U;
-        rows = next_rows;
-        full = wp.full(rows, tile, w.lo, w.len);
-      }
-      // ... and a warp past the end of a sequence no keys
-      if (tile < w.len) wp.template step<false>(rows, full, tile, w.lo, w.len, 0);
+      auto walk = [&](auto wide) {
+        constexpr bool kWide = decltype(wide)::value;
+        int tile = first_tile(w);
+        bool full = wp.full(rows, tile, w.lo, w.len);
+        // The last step stands apart: it has nothing to load.
+        for (int i = 1; i < units; ++i) {
+          const int64_t next_rows = wp.find(table, kvh, tile + U, w.len);
+          wp.template step<true, kWide>(rows, full, tile, w.lo, w.len, next_rows);
+          tile += U;
+          rows = next_rows;
+          full = wp.full(rows, tile, w.lo, w.len);
+        }
+        // ... and a warp past the end of a sequence no keys
+        if (tile < w.len) wp.template step<false, kWide>(rows, full, tile, w.lo, w.len, 0);
+      };
+      if (FP8 && wp.wide)
+        walk(std::true_type());
+      else
+        walk(std::false_type());
     }
 
     // The run's results leave the registers; the next run's first loads are

@@ -161,3 +161,25 @@ def test_weights_have_sixteen_bits(n, d, fp8):
     ref = reference(c, q, lens, scale)
     assert np.abs(ref["O"]).max() <= 2.0 ** -6  # little is left of values of one
     check(o, lse, ref, chain(lens, Hkv, group, d, fp8), d)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group", [2, 12])
+@pytest.mark.parametrize("far", [20, 30, 45, 90, 140])
+def test_queries_of_a_wide_range(far, group, d, fp8):
+    """Elements 2^far above the others, where every key is zero: the small
+    elements are the whole score.  One head has them, its neighbours have not."""
+    lens = [300, 17, 1000]
+    c = random_cache(lens, 32, 1, d, far, fp8)
+    c["kc"].view(torch.uint8 if fp8 else torch.int16)[..., 3::16] = 0
+    q = torch.randn((3, group, 1, d), generator=torch.Generator().manual_seed(far)).double()
+    q[:, 0] *= 2.0 ** (30 - far)
+    q[:, 0, :, 3::16] *= 2.0 ** far
+    q = q.to(torch.bfloat16)
+    assert torch.isfinite(q).all()
+    scale = 2.0 ** (far - 30) / math.sqrt(d)  # scores of ordinary size for that head
+    if far > 30:  # the neighbours' scores would be beyond any softmax
+        q[:, 1:] *= 2.0 ** (30 - far)
+    o, lse = answer(c, q, lens, scale=scale)
+    check(o, lse, reference(c, q, lens, scale), chain(lens, 1, group, d, fp8), d)
