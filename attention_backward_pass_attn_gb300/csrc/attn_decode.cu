@@ -184,38 +184,10 @@ __device__ __forceinline__ bool arrive(unsigned long long* word, unsigned long l
   return last;
 }
 
-// Partial results to be joined: part 0 lies in slot0, part k >= 1 in the first
-// slot of share share1 + (k - 1) stride.
-struct Parts {
-  int slot0, share1, stride, parts;
-  __device__ __forceinline__ int slot(int k) const {
-    return k == 0 ? slot0 : 2 * (share1 + (k - 1) * stride);
-  }
-};
-
-// More than kDirect parts of a head block are joined in two steps: first those
-// of each kGroup consecutive shares (share / kGroup), into the slot of the
-// first of them, then those results.  One block alone would read hundreds of
-// parts for longer than it computed.
-constexpr int kDirect = 32, kGroup = 16;
-
-// A head block that this block has a part of, with shares i0 .. i1.
-struct Piece {
-  int i0, i1, slot0, heads;
+// A head block that this block has a part of.
+struct SharedPiece : Piece {
+  int heads;
   int64_t out;  // its first output row
-  __device__ __forceinline__ bool direct() const { return i1 - i0 < kDirect; }
-  // The parts joined together with share i's.
-  __device__ __forceinline__ Parts group(int i) const {
-    const int g = i / kGroup * kGroup;
-    const int from = direct() || g < i0 ? i0 : g;
-    const int to = direct() || g + kGroup - 1 > i1 ? i1 : g + kGroup - 1;
-    return {from == i0 ? slot0 : 2 * from, from + 1, 1, to - from + 1};
-  }
-  // The groups' results.
-  __device__ __forceinline__ Parts groups() const {
-    const int g = i0 / kGroup;
-    return {slot0, (g + 1) * kGroup, kGroup, i1 / kGroup - g + 1};
-  }
 };
 
 // A run of units of one head block, and where it stands.  Kept in shared
@@ -598,7 +570,8 @@ struct Warp {
 // every thread.  w: the weights, kDecodeHeads x kPartsStride of shared memory.
 // `out` < 0: the result is a part of the second step, in slot ps.slot0, its
 // maximum and sum in an array of their own.
-constexpr int kPartsStride = 40;  // at least the parts of one join, a multiple of 8
+constexpr int kPartsStride = 40;  // a multiple of 8
+static_assert(kPartsStride >= max_join_parts(kDecodeMaxBlocks), "room for the parts of one join");
 
 __device__ __forceinline__ void join_weights(const DecodeArgs& a, const Parts& ps, int heads,
                                              int64_t out, float* w) {
@@ -708,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
   __shared__ int64_t sh_W;
   __shared__ Work sh_work[2];
   __shared__ bool sh_last[2];
-  __shared__ Piece sh_piece[2];
+  __shared__ SharedPiece sh_piece[2];
 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   grid_dep_wait();
@@ -805,11 +778,8 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
       if (tid == 0 && units != w.n) {
         const int64_t W = sh_W;
         const int G = int(W < int64_t(gridDim.x) ? W : int64_t(gridDim.x));
-        const int i0 = split_owner(w.first_unit, W, G);
-        const Piece pc = {i0, split_owner(w.first_unit + w.n - 1, W, G),
-                          // the first share may have come here after another head block
-                          2 * i0 + (split_begin(i0, W, G) < w.first_unit ? 1 : 0), heads_of(w.h),
-                          int64_t(w.b) * a.Hq + first_head(w.h)};
+        const SharedPiece pc = {split_piece(w.first_unit, w.n, W, G), heads_of(w.h),
+                                int64_t(w.b) * a.Hq + first_head(w.h)};
         sh_piece[pieces] = pc;
         open_count(a.arrivals + pc.group(blockIdx.x).slot0, a.tag);
         if (!pc.direct()) open_count(a.arrivals2 + pc.slot0, a.tag);
@@ -879,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
     }
     const int heads = heads_of(seen.h);
     const int64_t out = int64_t(seen.b) * a.Hq + first_head(seen.h);
-    const int slot = 2 * blockIdx.x + (turn ? 1 : 0);
+    const int slot = part_slot(blockIdx.x, turn);
     for (int i = tid; i < heads * (D / 4); i += kThreads) {
       const int head = i / (D / 4), c = 4 * (i % (D / 4));
       float2 ml[kWarps];
@@ -924,7 +894,7 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
     if (tid < 2) {
       bool last = false;
       if (waits) {
-        const Piece pc = sh_piece[tid];
+        const SharedPiece pc = sh_piece[tid];
         fence_acq_rel_gpu();
         last = step ? arrive(a.arrivals2 + pc.slot0, a.tag, pc.groups().parts)
                     : arrive(a.arrivals + pc.group(blockIdx.x).slot0, a.tag,
@@ -939,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
 #pragma unroll 1
     for (int x = 0; x < pieces; ++x) {
       if (!sh_last[x]) continue;
-      const Piece pc = sh_piece[x];
+      const SharedPiece pc = sh_piece[x];
       const bool whole = step || pc.direct();
       again |= !whole;
       join_parts<D>(a, step ? pc.groups() : pc.group(blockIdx.x), pc.heads, whole ? pc.out : -1,

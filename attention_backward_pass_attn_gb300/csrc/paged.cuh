@@ -58,6 +58,57 @@ ATTN_HD int64_t split_begin(int i, int64_t W, int G) { return int64_t(i) * W / G
 // i W / G < x + 1  <=>  i < (x + 1) G / W.
 ATTN_HD int split_owner(int64_t x, int64_t W, int G) { return int(((x + 1) * G - 1) / W); }
 
+// A head block (the units of one sequence and block of heads) that several
+// shares cover leaves a partial result in each.  A share has two slots for
+// them: `turn` counts the head blocks it has come through, and only its first
+// and its last can be shared with others.
+ATTN_HD int part_slot(int share, int turn) { return 2 * share + (turn ? 1 : 0); }
+
+// Partial results to be joined: part 0 lies in slot0, part k >= 1 in the first
+// slot of share share1 + (k - 1) stride.
+struct Parts {
+  int slot0, share1, stride, parts;
+  ATTN_HD int slot(int k) const {
+    return k == 0 ? slot0 : part_slot(share1 + (k - 1) * stride, 0);
+  }
+};
+
+// More than kDirect parts of a head block are joined in two steps: first those
+// of each kGroup consecutive shares (share / kGroup), into the slot of the
+// first of them, then those results.  One block alone would read hundreds of
+// parts for longer than it computed.
+constexpr int kDirect = 32, kGroup = 16;
+
+// The most parts that one join has, of either step, with G shares.
+constexpr int max_join_parts(int G) {
+  return (G - 1) / kGroup + 1 > kDirect ? (G - 1) / kGroup + 1 : kDirect;
+}
+
+// A head block with shares i0 .. i1; its first part lies in slot0.
+struct Piece {
+  int i0, i1, slot0;
+  ATTN_HD bool direct() const { return i1 - i0 < kDirect; }
+  // The parts joined together with share i's.
+  ATTN_HD Parts group(int i) const {
+    const int g = i / kGroup * kGroup;
+    const int from = direct() || g < i0 ? i0 : g;
+    const int to = direct() || g + kGroup - 1 > i1 ? i1 : g + kGroup - 1;
+    return {from == i0 ? slot0 : part_slot(from, 0), from + 1, 1, to - from + 1};
+  }
+  // The groups' results.
+  ATTN_HD Parts groups() const {
+    const int g = i0 / kGroup;
+    return {slot0, (g + 1) * kGroup, kGroup, i1 / kGroup - g + 1};
+  }
+};
+
+// The head block of units first .. first + n - 1, of W units in G shares.
+ATTN_HD Piece split_piece(int64_t first, int n, int64_t W, int G) {
+  const int i0 = split_owner(first, W, G);
+  // its first share may have come to it after another head block
+  return {i0, split_owner(first + n - 1, W, G), part_slot(i0, split_begin(i0, W, G) < first)};
+}
+
 // Division of 0 <= n < 2^31 by a fixed d >= 1, as a multiplication: with
 // s = ceil(log2 d) and mul = floor(2^(31 + s) / d) + 1 < 2^32, the product
 // exceeds n 2^(31 + s) / d by less than n <= 2^31, too little to reach the next
