@@ -406,7 +406,9 @@ int kv_cache_write(const void* K, const void* V, const int64_t* strides, void* K
  * Read back: K, V (bf16, contiguous [B][Hkv][T][d]) receive positions
  * start[b] .. start[b] + count[b] - 1 of each sequence, multiplied by their
  * factors and rounded once to bf16.  Rows at count[b] and beyond, and rows of
- * skipped positions, are zero.
+ * skipped positions, are zero.  (attn_fwd takes as many keys as queries and as
+ * many key heads as query heads: attention of further tokens over rows read back
+ * needs queries filled up to the keys' number, and key heads repeated.)
  */
 int kv_cache_read(const void* K_cache, const void* V_cache, const float* k_descale,
                   const float* v_descale, const int* page_table, const int* start,
@@ -425,8 +427,16 @@ int kv_cache_read(const void* K_cache, const void* V_cache, const float* k_desca
  * Q, O: bf16 [B][Hq][d]; L: fp32 [B][Hq], natural log.  A sequence with
  * nothing to see (n = 0, or only skipped positions) gets O = 0 and L = -inf.
  * Values of the cache at positions that are not visible have no effect, NaN
- * and infinities included; a NaN or an infinity at a visible position makes
- * the outputs that use it infinite or NaN.  Hq is a multiple of Hkv.
+ * and infinities included.  At a visible position, a score that is NaN or
+ * +inf makes L and O of its head NaN, one that is -inf (of an infinite key or
+ * factor) has weight 0, and where every score is -inf the result is O = 0 and
+ * L = -inf, as if there were nothing to see; a NaN or an infinity in V makes the
+ * outputs that use it NaN or infinite, and leaves L.  Hq is a multiple of Hkv.
+ *
+ * O and L differ from the formula's by fp32 rounding of scores and sums, by
+ * weights of 16 significant bits in O (2^-16 of sum_j exp(S_j - L) |v_j|), and
+ * by O's rounding to bf16.  The weighted sum is formed before it is divided:
+ * values of more than 2^127 / n may overflow.
  *
  * The work is split evenly over the GPU, whatever the lengths, and the parts
  * of a sequence are joined in a fixed order: results repeat bit for bit.  The
