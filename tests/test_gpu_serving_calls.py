@@ -2,10 +2,13 @@
 streams are out of the ordinary."""
 
 import ctypes
+import os
+import re
 
 import pytest
 import torch
 
+import attention_backward_pass_attn_gb300 as attn
 from attention_backward_pass_attn_gb300 import binding as ab
 from attention_backward_pass_attn_gb300.inputs import make_tensor
 from test_gpu_decode import cuda_ready, i32  # noqa: F401
@@ -137,3 +140,32 @@ def test_heads_whose_values_pass_31_bits():
     o, lse = ab.attn_decode(q, kc, vc, table, i32([0, 1]).cuda(), out=out)
     assert bool((o[0] == 0).all()) and bool(torch.isneginf(lse[0]).all())
     assert bool((o[1] == v[0]).all()) and bool((lse[1] == 0).all())
+
+
+def test_readme_prompt_and_tokens():
+    """The README's prompt with shared key heads and a padded batch, and the
+    prompt's last tokens once more as tokens after the rest of it: attn_fwd's
+    last rows, each kernel within 1e-2 of the largest value as its own tests
+    hold it, over a bf16 cache; and over the README's e4m3 one it runs."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "README.md")).read()
+    code = [b for b in re.findall(r"```python\n(.*?)```", text, flags=re.S)
+            if "kv_cache_write" in b]
+    assert len(code) == 2
+    scope = {"torch": torch, "attn": attn}
+    for b in code:
+        exec(b, scope)
+    x = make_tensor((2, 90, 48, 128), 12).cuda()
+    n = torch.tensor([90, 33], dtype=torch.int32).cuda()
+    last = x[torch.arange(2), (n - 1).long().cpu()].unsqueeze(1)
+    for e4m3 in (True, False):
+        if not e4m3:
+            scope["kc"], scope["vc"], scope["ks"], scope["vs"] = ab.alloc_kv_cache(
+                4096, 8, 64, 128, "cuda")
+        o, lens = scope["prompt"](x, n)
+        assert o.shape == (2, 32, 90, 128) and lens is n
+        o1, after = scope["token"](last, lens - 1)
+        assert torch.equal(after, n) and torch.isfinite(o1).all()
+    for b in range(2):
+        want, got = o[b, :, int(n[b]) - 1].float(), o1[b, :, 0].float()
+        assert float((want - got).abs().max()) <= 2e-2 * float(want.abs().max())
