@@ -4,6 +4,9 @@ streams are out of the ordinary."""
 import ctypes
 import os
 import re
+import subprocess
+import sys
+import threading
 
 import pytest
 import torch
@@ -169,3 +172,68 @@ def test_readme_prompt_and_tokens():
     for b in range(2):
         want, got = o[b, :, int(n[b]) - 1].float(), o1[b, :, 0].float()
         assert float((want - got).abs().max()) <= 2e-2 * float(want.abs().max())
+
+
+COLD = """
+import torch
+import attention_backward_pass_attn_gb300 as attn
+
+B, H, Hkv, d = 2, 4, 2, 64
+g = torch.Generator(device="cuda").manual_seed(1)
+x = torch.randn(B, 1, H + 2 * Hkv, d, device="cuda", generator=g).to(torch.bfloat16)
+freq = torch.ones(d // 2, device="cuda")
+table = torch.arange(8, dtype=torch.int32, device="cuda").view(B, 4)
+lens = torch.full((B,), 20, dtype=torch.int32, device="cuda")
+kc, vc, ks, vs = attn.alloc_kv_cache(8, Hkv, 16, d, "cuda", torch.float8_e4m3fn)
+after = lens + 1
+torch.cuda.synchronize()
+
+def step():
+    q, k, v = (t.transpose(1, 2) for t in x.split((H, Hkv, Hkv), dim=2))
+    q, k = attn.rope_fwd(q, k, lens.view(1, B, 1), freq)
+    attn.kv_cache_write(k, v, kc, vc, table, lens, k_descale=ks, v_descale=vs)
+    o, lse = attn.attn_decode(q, kc, vc, table, after, k_descale=ks, v_descale=vs)
+    kr, vr = attn.kv_cache_read(kc, vc, table, lens, 1, k_descale=ks, v_descale=vs)
+    return o, lse, kr, vr, attn.rope_bwd(q, k, lens.view(1, B, 1), freq)[0]
+
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in got]
+for a, b in zip(got, step()):
+    assert torch.equal(a, b)
+assert attn.attn_last_device_error() == 0
+"""
+
+
+def test_a_process_may_begin_with_a_capture():
+    """The first calls of a process, captured: nothing of their set-up is
+    forbidden there."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", COLD], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert p.returncode == 0, p.stderr
+
+
+def test_threads_on_streams_of_their_own():
+    """Host threads that call at once, each on a stream of the pool, without
+    workspaces of the caller's."""
+    batches = [small(B=1, n=4000 + 333 * i, seed=40 + i) for i in range(4)]
+    ref = [ab.attn_decode(*x) for x in batches]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got = [ab.attn_decode(*batches[i]) for _ in range(50)]
+            torch.cuda.current_stream().synchronize()
+        wrong.extend(i for g in got if not same(g, ref[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
