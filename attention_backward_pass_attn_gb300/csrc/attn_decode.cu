@@ -47,9 +47,10 @@
 // nonzero elements lie within 31 binades.  Where they do not, K is widened to
 // bf16 (exact) and meets q's own numbers, scaled clear of overflow: exact down
 // to 2^-222 of the head's largest element.  fp16 is the faster of the two, one
-// conversion for a pair of values where bf16 takes four (the batch above with
-// a choice for every product: 58 us); telling them apart costs 0.4 % there, 2 %
-// for the 256 short sequences.  V is widened to bf16 (exact).
+// conversion for a pair of keys' values where bf16 takes four.  V is widened to
+// bf16 (exact).  The choice is made for a run of keys at a time: every head in
+// bf16 takes the batch above to 56 us, telling the two apart costs it 0.5 %, and
+// 1.5 % of the 256 short sequences.  A choice for every product took 58 us.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -802,10 +803,12 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
         // ... and a warp past the end of a sequence no keys
         if (tile < w.len) wp.template step<false, kWide>(rows, full, tile, w.lo, w.len, 0);
       };
-      if (FP8 && wp.wide)
-        walk(std::true_type());
-      else
+      // The bf16 walk is the branch not expected: laid out the other way, its
+      // instructions cost an e4m3 call of 18 us (caches cold) 6 us more, not 2.
+      if (!FP8 || __builtin_expect(!wp.wide, 1))
         walk(std::false_type());
+      else
+        walk(std::true_type());
     }
 
     // The run's results leave the registers; the next run's first loads are
