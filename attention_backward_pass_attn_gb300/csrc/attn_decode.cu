@@ -23,9 +23,10 @@
 //   P^T) are the 16 rows and up to 8 query heads the 8 columns; the order of
 //   the contracted index is free as long as both operands use the same one,
 //   so a thread's 16-byte load of a K row is four or eight consecutive k
-//   indices, and the 2 x 2 transposes of V are byte permutes.  A tile of 128
-//   rows in tensor memory (tcgen05.mma) would waste 120 of its 128 rows on
-//   absent heads and cost a trip through shared memory.
+//   indices, and the 2 x 2 transposes of V are byte permutes.  128 keys (or
+//   output columns) would fill a tile of tcgen05.mma as well, but its operands
+//   lie in shared memory and its results in tensor memory: two trips more for
+//   every row in a kernel that HBM bounds, whose tensor pipe is 12 to 21 % busy.
 // - K of the next keys is loaded while the current scores are weighted, V of
 //   the next keys while the next scores are formed: 4 to 8 KB in flight per
 //   warp, 12 warps per SM.
@@ -35,7 +36,11 @@
 // sequences of up to 8,192, 8 key heads x 8, e4m3: 52 us for 264 MB; 500
 // positions of 16 heads: 7.2 us, 2.7 of them from the arrivals on.  256
 // sequences of up to 256, 8 key heads x 4, bound by the changes of sequence:
-// e4m3 32 us for 67 MB, bf16 37 us for 131 MB.
+// e4m3 32 us for 67 MB, bf16 37 us for 131 MB.  With 16 heads to a key head (two
+// blocks to an SM) 16 sequences of up to 8,192, 2 key heads, take 21 us for 31 MB
+// in e4m3 and 22 us for 60 MB in bf16, bound by latency (issue slots 21 to 23 %,
+// DRAM 13 to 30 %): eight warps an SM hide less than twelve, and 16 heads of
+// partial output are written, read back and joined where there were 8.
 //
 // Rounding.  Scores, maxima, sums and outputs are fp32.  The weights p (times
 // V's factor of an e4m3 row) meet V as a sum of two bf16 numbers, 16 bits in
