@@ -38,8 +38,8 @@
 // sequences of up to 256, 8 key heads x 4, bound by the changes of sequence:
 // e4m3 32 us for 67 MB, bf16 37 us for 131 MB.  With 16 heads to a key head (two
 // blocks to an SM) 16 sequences of up to 8,192, 2 key heads, take 21 us for 31 MB
-// in e4m3 and 22 us for 60 MB in bf16, bound by latency (issue slots 21 to 23 %,
-// DRAM 13 to 30 %): eight warps an SM hide less than twelve, and 16 heads of
+// in e4m3 and 22 us for 60 MB in bf16, bound by latency (issue slots 24 to 30 %,
+// DRAM 16 to 31 %): eight warps an SM hide less than twelve, and 16 heads of
 // partial output are written, read back and joined where there were 8.
 //
 // Rounding.  Scores, maxima, sums and outputs are fp32.  The weights p (times
