@@ -87,6 +87,8 @@ def load_library(path: str | None = None):
             "kv_cache_read": (i, [vp] * 9 + [i] * 7 + [vp]),
             "attn_decode_workspace_size": (sz, [i]),
             "attn_decode": (i, [vp] * 9 + [i] * 8 + [f, vp, sz, vp]),
+            "attn_fwd_score": (i, [vp] * 6 + [i] * 7 + [vp, vp, f, vp, f, vp]),
+            "attn_bwd_score": (i, [vp] * 10 + [i] * 7 + [vp, vp, f, vp, f, vp, sz, vp]),
             "attn_last_device_error": (i, [vp]),
             "attn_device_error_word": (i, [vp, ctypes.POINTER(ctypes.c_int)]),
             "attn_watchdog_selftest": (i, [ctypes.c_uint64, vp]),
@@ -615,6 +617,111 @@ def rope_bwd(dq, dk, pos, inv_freq, sections=None, interleaved=False, out=None, 
     """The gradients of rope_fwd's q and k from those of its results (the turn
     by the negative angles); arguments as for rope_fwd."""
     return _rope(_ROPE_BWD, dq, dk, pos, inv_freq, sections, interleaved, out, stream)
+
+
+# ------------------------------------------------------------------ changed scores
+def _score_problem(q, k, v, causal, scale, softcap, slopes, window, doc, prefix):
+    """(device, (B, Hq, Hkv, N, d), arguments of the C calls: strides, then
+    those between the sizes and the stream)."""
+    dev = _device_index(q, "q")
+    shape = _shape4(q, "q")
+    B, Hq, N, d = shape
+    Hkv = _shape4(k, "k")[1]
+    if Hkv < 1 or Hq % Hkv:
+        raise ValueError("q's %d heads must be a multiple of k's %d" % (Hq, Hkv))
+    keys = (B, Hkv, N, d)
+    strides = _check_rows(q, "q", shape, dev) + _check_rows(k, "k", keys, dev) \
+        + _check_rows(v, "v", keys, dev)
+    for i, (name, n) in enumerate((x, n) for x in "qkv" for n in (B, Hq if x == "q" else Hkv, N)):
+        if n > 1 and strides[i] < 1:
+            raise ValueError("%s must not be expanded: its strides must be positive" % name)
+    if slopes is not None:
+        _check_like(slopes, "slopes", (Hq,), torch.float32, dev)
+    if doc is not None:
+        _check_like(doc, "doc", (B, N), torch.int32, dev)
+    if prefix is not None:
+        _check_like(prefix, "prefix", (B,), torch.int32, dev)
+    window = max(-1, min(int(window), _INT_MAX))  # what no length reaches hides nothing
+    rest = (int(bool(causal)), window, _ptr(doc), _ptr(prefix), float(softcap), _ptr(slopes),
+            _default_scale(d, scale))
+    return dev, (B, Hq, Hkv, N, d), _array(ctypes.c_int64, strides), rest
+
+
+def attn_fwd_score(q, k, v, causal: bool, scale=None, softcap=0.0, slopes=None, window=0, doc=None,
+                   prefix=None, out=None, lse=None, stream=None):
+    """O and the row log-sum-exp L of attention with changed scores.
+
+    q: bf16 CUDA tensor [B, Hq, N, d] (d = 64 or 128), k and v [B, Hkv, N, d],
+    Hq a multiple of Hkv; contiguous in d, other strides positive multiples of
+    8 (so heads of a fused projection are taken as they lie).
+    softcap > 0: scores become softcap * tanh(score / softcap).
+    slopes: fp32 [Hq]; scores lose slopes[h] * |i - j| (after the cap).
+    window, doc (causal only): as for attn_fwd.
+    prefix (causal only, without window and doc): int32 [B]; every query also
+    sees the keys j < prefix[b].
+    Returns (O bf16 [B, Hq, N, d], L fp32 [B, Hq, N]), contiguous.
+    """
+    dev, dims, strides, rest = _score_problem(q, k, v, causal, scale, softcap, slopes, window, doc,
+                                              prefix)
+    B, Hq, _, N, d = dims
+    if out is None:
+        out = _empty((B, Hq, N, d), torch.bfloat16, dev, stream)
+    else:
+        _check_like(out, "out", (B, Hq, N, d), torch.bfloat16, dev)
+    if lse is None:
+        lse = _empty((B, Hq, N), torch.float32, dev, stream)
+    else:
+        _check_like(lse, "lse", (B, Hq, N), torch.float32, dev)
+    st = load_library().attn_fwd_score(q.data_ptr(), k.data_ptr(), v.data_ptr(), strides,
+                                       out.data_ptr(), lse.data_ptr(), *dims, *rest,
+                                       _stream_on(stream, dev))
+    if st:
+        _check("attn_fwd_score", st)
+    return out, lse
+
+
+def attn_bwd_score(q, k, v, o, do, lse, causal: bool, scale=None, softcap=0.0, slopes=None,
+                   window=0, doc=None, prefix=None, dq=None, dk=None, dv=None, workspace=None,
+                   stream=None):
+    """dQ [B, Hq, N, d] and dK, dV [B, Hkv, N, d] (bf16, contiguous) of
+    attn_fwd_score, whose arguments these are; dK and dV are summed over the
+    query heads that share a key head.
+
+    o, lse: the forward's results; do: the gradient of o; contiguous.
+    workspace: from alloc_workspace(B, Hq, N, d, device); allocated by the call
+    without one.
+    """
+    dev, dims, strides, rest = _score_problem(q, k, v, causal, scale, softcap, slopes, window, doc,
+                                              prefix)
+    B, Hq, Hkv, N, d = dims
+    rows, keys = (B, Hq, N, d), (B, Hkv, N, d)
+    _check_like(o, "o", rows, torch.bfloat16, dev)
+    _check_like(do, "do", rows, torch.bfloat16, dev)
+    _check_like(lse, "lse", (B, Hq, N), torch.float32, dev)
+    got = []
+    for t, name, shape in ((dq, "dq", rows), (dk, "dk", keys), (dv, "dv", keys)):
+        if t is None:
+            t = _empty(shape, torch.bfloat16, dev, stream)
+        else:
+            _check_like(t, name, shape, torch.bfloat16, dev)
+        got.append(t)
+    if workspace is None:
+        workspace = _empty((max(attn_bwd_workspace_size(B, Hq, N, d), 256),), torch.uint8, dev,
+                           stream)
+    else:
+        if not isinstance(workspace, torch.Tensor):
+            raise TypeError("workspace must be a torch.Tensor")
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous and on CUDA device %d, like the first "
+                             "tensor" % dev)
+    st = load_library().attn_bwd_score(q.data_ptr(), k.data_ptr(), v.data_ptr(), strides,
+                                       o.data_ptr(), do.data_ptr(), lse.data_ptr(),
+                                       *(t.data_ptr() for t in got), *dims, *rest,
+                                       workspace.data_ptr(), workspace.nbytes,
+                                       _stream_on(stream, dev))
+    if st:
+        _check("attn_bwd_score", st)
+    return tuple(got)
 
 
 def alloc_kv_cache(num_pages: int, Hkv: int, page_size: int, d: int, device,

@@ -1,0 +1,86 @@
+// score.cuh -- device side of the changed scores: the cap, the visible range of
+// a row, and the TMA copies of strided rows.
+//
+// The cap.  x = cap tanh(s / cap) for the scaled product s, in base 2.  Near
+// zero, |s / cap| <= 0.8, tanh is an odd polynomial of six terms, fitted to the
+// smallest relative error (6e-8, fp32's own): two scores to an instruction of
+// the FMA pipe.  Beyond it, tanh(y) = 1 - 2 / (1 + e^2y): an exponential and a
+// reciprocal for each score, absolute error some 2^-23 of the cap.  A warp
+// takes the polynomial for a tile whose scores all allow it: models that cap
+// their scores at 30 or 50 have most of them well below, and the special
+// function unit is the busier pipe of a softmax (figures in score_fwd.cu).
+// With a cap far above every score the polynomial is also the exact one, where
+// 1 - 2 / (1 + e^2y) would lose the score in the cap's last bits.
+#pragma once
+
+#include "f32x2.cuh"
+#include "mask.cuh"
+#include "ptx.cuh"
+#include "score.h"
+
+namespace attn {
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t f32x2(float x) { return f32x2(x, x); }
+
+// Two capped scores in base 2 by the polynomial.
+__device__ __forceinline__ uint64_t cap_poly(const ScoreMap& m, uint64_t u) {
+  const uint64_t z = mul_f32x2(u, u);
+  uint64_t h = f32x2(m.poly[kTanhTerms - 1]);
+#pragma unroll
+  for (int k = kTanhTerms - 2; k >= 0; --k) h = fma_f32x2(h, z, f32x2(m.poly[k]));
+  return mul_f32x2(u, h);
+}
+
+// 1 / (1 + e^2y) of y = u scale / cap; the capped score is cap_log2 (1 - 2 r).
+__device__ __forceinline__ float cap_r(const ScoreMap& m, float u) {
+  return rcp_approx(1.f + ex2(u * m.exp_scale));
+}
+
+// The row range [lo, hi) of keys that query q sees.  doc: the batch element's
+// map or null; prefix: its length or 0.
+struct RowMask {
+  int N, causal, window;
+  const int* doc;
+  int prefix;
+  __device__ __forceinline__ int lo(int q) const {
+    return causal ? first_visible_key(q, doc, window, N) : 0;
+  }
+  __device__ __forceinline__ int hi(int q) const {
+    return causal ? min(N, max(q + 1, prefix)) : N;
+  }
+};
+
+// Tiled load and L2 prefetch through a 4-D map (head dim, row, head, batch).
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int x, int y, int z,
+                                                int w) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+
+}  // namespace attn

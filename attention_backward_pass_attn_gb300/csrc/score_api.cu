@@ -1,0 +1,179 @@
+// score_api.cu -- the C ABI of attention with changed scores (declared in
+// include/attn.h): argument validation, the constants of the score map, tensor
+// maps, and the calls into the kernel launchers.
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/attn.h"
+#include "score.h"
+
+namespace attn {
+
+// tanh(y) = y (c0 + c1 y^2 + ... + c5 y^10) on |y| <= 0.8, the polynomial of
+// the smallest relative error (5.8e-8), found by Remez exchange.
+namespace {
+constexpr double kTanh[kTanhTerms] = {0.999999942083,   -0.333326749194, 0.133210482804,
+                                      -0.0531143154981, 0.0190933004507, -0.0043552995703};
+constexpr double kTanhReach = 0.8;
+constexpr double kLog2e = 1.4426950408889634;
+}  // namespace
+
+bool make_score_map(float scale, float softcap, const float* slopes, ScoreMap* m) {
+  *m = {};
+  m->scale_log2 = float(scale * kLog2e);
+  m->slopes = slopes;
+  m->poly_limit = -1.f;
+  if (!std::isfinite(m->scale_log2) || softcap == 0.f) return std::isfinite(m->scale_log2);
+  const double c = double(scale) / softcap;
+  m->exp_scale = float(2 * kLog2e * c);
+  m->cap_log2 = float(softcap * kLog2e);
+  m->inv_cap_log2_sq = float(1 / (softcap * kLog2e * softcap * kLog2e));
+  if (!std::isfinite(m->exp_scale) || !std::isfinite(2 * m->cap_log2)) return false;
+  bool good = std::isfinite(m->inv_cap_log2_sq);
+  double power = scale * kLog2e;  // x = u (scale log2e) sum_k c_k (c u)^2k
+  for (int k = 0; k < kTanhTerms; ++k, power *= c * c) {
+    m->poly[k] = float(kTanh[k] * power);
+    good = good && std::isfinite(m->poly[k]);
+  }
+  const float limit = float(kTanhReach / c);
+  if (good) m->poly_limit = std::isfinite(limit) ? limit : 3.4e38f;
+  return true;
+}
+
+namespace {
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+bool good(const void* p, uintptr_t n) { return p && aligned(p, n); }
+int status_of(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
+
+// Sizes, masks and the score map; *empty: nothing to do.
+int make_problem(int B, int Hq, int Hkv, int N, int d, int causal, int window, const int* doc,
+                 const int* prefix, float softcap, const float* slopes, float scale,
+                 ScoreProblem* p, bool* empty) {
+  if (B < 0 || Hq < 0 || Hkv < 1 || Hq % Hkv || N < 0 || d < 0) return ATTN_ERR_INVALID_ARG;
+  if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
+  if (window < 0 || (!causal && (window || doc || prefix))) return ATTN_ERR_INVALID_ARG;
+  if (prefix && (window || doc)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(doc, 4) || !aligned(prefix, 4) || !aligned(slopes, 4)) return ATTN_ERR_INVALID_ARG;
+  if (!(std::isfinite(scale) && scale > 0.f) || !(std::isfinite(softcap) && softcap >= 0.f))
+    return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  *p = {};
+  if (!make_score_map(scale, softcap, slopes, &p->map)) return ATTN_ERR_INVALID_ARG;
+  *empty = B == 0 || Hq == 0 || N == 0;
+  if (*empty) return ATTN_OK;
+  const long long n_tiles = (N + 127LL) / 128;
+  // every row index, and the grid, inside 31 bits
+  if ((long long)B * Hq > INT_MAX || (long long)B * Hq * n_tiles * 128 > INT_MAX)
+    return ATTN_ERR_UNSUPPORTED;
+  p->B = B;
+  p->Hq = Hq;
+  p->Hkv = Hkv;
+  p->group = Hq / Hkv;
+  p->N = N;
+  p->d = d;
+  p->n_tiles = int(n_tiles);
+  p->Npad = int(n_tiles * 128);
+  p->causal = causal;
+  p->window = window >= N ? 0 : window;
+  p->doc = doc;
+  p->prefix = prefix;
+  p->cap = softcap > 0.f;
+  return ATTN_OK;
+}
+
+// The plain kernels' shape for H heads.
+Shape shape_of(const ScoreProblem& p, int H) {
+  Shape s = {};
+  s.BH = p.B * H;
+  s.N = p.N;
+  s.d = p.d;
+  s.causal = p.causal;
+  s.n_tiles = p.n_tiles;
+  s.Npad = p.Npad;
+  s.H = H;
+  return s;
+}
+
+// The map of operand `which` (0: Q, 1: K, 2: V) with the caller's strides
+// (batch, head, token of each) or contiguous rows.
+int rows_map(CUtensorMap* map, const void* ptr, const int64_t* strides, int which,
+             const ScoreProblem& p) {
+  const int H = which ? p.Hkv : p.Hq;
+  const int64_t rows[3] = {int64_t(H) * p.N * p.d, int64_t(p.N) * p.d, p.d};
+  const int n[3] = {p.B, H, p.N};
+  int64_t s[3];
+  for (int k = 0; k < 3; ++k) {
+    // a dimension of one index has no stride to speak of
+    s[k] = strides && n[k] > 1 ? strides[3 * which + k] : rows[k];
+    if (s[k] < 1 || s[k] % 8) return ATTN_ERR_INVALID_ARG;
+    if (s[k] >= int64_t(1) << 39) return ATTN_ERR_UNSUPPORTED;  // 2^40 bytes
+  }
+  return make_rows_map(map, ptr, s, p.B, H, p.N, p.d) ? ATTN_ERR_CUDA : ATTN_OK;
+}
+
+}  // namespace
+}  // namespace attn
+
+using namespace attn;
+
+extern "C" {
+
+int attn_fwd_score(const void* Q, const void* K, const void* V, const int64_t* strides, void* O,
+                   float* L, int B, int Hq, int Hkv, int N, int d, int causal, int window,
+                   const int* doc_start, const int* prefix, float softcap, const float* slopes,
+                   float scale, void* stream) {
+  ScoreProblem p;
+  bool empty = false;
+  int st = make_problem(B, Hq, Hkv, N, d, causal, window, doc_start, prefix, softcap, slopes,
+                        scale, &p, &empty);
+  if (st != ATTN_OK || empty) return st;
+  if (!good(Q, 16) || !good(K, 16) || !good(V, 16) || !good(O, 16) || !good(L, 4))
+    return ATTN_ERR_INVALID_ARG;
+  CUtensorMap mq, mk, mv;
+  if ((st = rows_map(&mq, Q, strides, 0, p)) || (st = rows_map(&mk, K, strides, 1, p)) ||
+      (st = rows_map(&mv, V, strides, 2, p)))
+    return st;
+  int* err = error_word_ptr();
+  if (!err) return ATTN_ERR_CUDA;
+  return status_of(launch_score_fwd(mq, mk, mv, O, L, p, err, (cudaStream_t)stream));
+}
+
+int attn_bwd_score(const void* Q, const void* K, const void* V, const int64_t* strides,
+                   const void* O, const void* dO, const float* L, void* dQ, void* dK, void* dV,
+                   int B, int Hq, int Hkv, int N, int d, int causal, int window,
+                   const int* doc_start, const int* prefix, float softcap, const float* slopes,
+                   float scale, void* workspace, size_t bytes, void* stream) {
+  ScoreProblem p;
+  bool empty = false;
+  int st = make_problem(B, Hq, Hkv, N, d, causal, window, doc_start, prefix, softcap, slopes,
+                        scale, &p, &empty);
+  if (st != ATTN_OK) return st;
+  // without query heads there is no gradient for the keys to sum
+  if (empty) return B > 0 && N > 0 ? ATTN_ERR_INVALID_ARG : ATTN_OK;
+  for (const void* x : {Q, K, V, O, dO, (const void*)dQ, (const void*)dK, (const void*)dV})
+    if (!good(x, 16)) return ATTN_ERR_INVALID_ARG;
+  if (!good(L, 4)) return ATTN_ERR_INVALID_ARG;
+  const Shape rows = shape_of(p, p.Hq), keys = shape_of(p, p.Hkv);
+  if (!good(workspace, 256) || bytes < workspace_bytes(rows)) return ATTN_ERR_WORKSPACE;
+  const Workspace ws = carve_workspace(workspace, rows);
+  ScoreBwdMaps m;
+  if ((st = rows_map(&m.q, Q, strides, 0, p)) || (st = rows_map(&m.k, K, strides, 1, p)) ||
+      (st = rows_map(&m.v, V, strides, 2, p)))
+    return st;
+  if (make_tile_map(&m.dout, dO, rows) || make_tile_map(&m.dk, dK, keys) ||
+      make_tile_map(&m.dv, dV, keys) || make_acc_map(&m.acc, ws.acc, rows))
+    return ATTN_ERR_CUDA;
+  int* err = error_word_ptr();
+  if (!err) return ATTN_ERR_CUDA;
+  const cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e = launch_bwd_preprocess(O, dO, L, ws, rows, true, s);
+  if (e == cudaSuccess && p.doc) e = launch_score_bwd_tables(ws, p, s);
+  if (e == cudaSuccess && p.doc) e = launch_bwd_order(ws, shape_of(p, 1), s);
+  if (e == cudaSuccess) e = launch_score_bwd_main(m, ws, p, scale, err, s);
+  if (e == cudaSuccess) e = launch_bwd_dq_convert(dQ, ws, rows, scale, s);
+  return status_of(e);
+}
+
+}  // extern "C"

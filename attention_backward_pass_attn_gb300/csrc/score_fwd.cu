@@ -1,0 +1,529 @@
+// score_fwd.cu -- attention forward with changed scores: capped by a tanh, with
+// a bias that falls with distance, a prefix that sees itself whole, and key
+// heads that several query heads share.
+//
+//   x_ij = f(<q_i, k_j>),  f(u) = s u, or cap tanh(s u / cap)
+//   x_ij -= slope_h |i - j|            (with slopes)
+//   l_i = logsumexp_j x_ij,  o_i = sum_j exp(x_ij - l_i) v_j
+//
+// over the keys j that row i sees (RowMask in score.cuh).
+//
+// The frame is the plain forward's (attn_fwd.cu): a task is two 128-row query
+// tiles of one head, whose 128-row key/value tiles run through a two-stage TMA
+// ring; warps 0-3 and 4-7 run the softmax of the two tiles, a thread to a row,
+// warp 8 issues copies and warp 9 the tensor core's instructions; S and P
+// share tensor-memory columns, and the grid is fwd_grid's.  What differs:
+//
+//  * Scores are changed where they lie, in registers, before the row maximum.
+//    Tiles that no row's mask cuts skip the mask; tiles wholly in their rows'
+//    past or future take the bias's distance without its absolute value.
+//  * A query head reads key head h / group, through 4-D tensor maps with the
+//    caller's strides: heads of a fused projection are taken as they lie.  The
+//    heads of a group run side by side, so the L2 serves all but one of them.
+#include "score.cuh"
+
+namespace attn {
+namespace score_fwd {
+
+constexpr int kThreads = 320;
+constexpr int kProducerWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr int kStages = 2;
+constexpr uint32_t kTmemCols = 512;
+
+// Barrier indices.
+constexpr int kBarQFull = 0;
+constexpr int kBarQEmpty = 1;
+constexpr int kBarKFull = 2;                     // + stage
+constexpr int kBarKEmpty = kBarKFull + kStages;  // + stage
+constexpr int kBarVFull = kBarKEmpty + kStages;  // + stage
+constexpr int kBarVEmpty = kBarVFull + kStages;  // + stage
+constexpr int kBarSFull = kBarVEmpty + kStages;  // + tile (0 = A, 1 = B)
+constexpr int kBarPReady = kBarSFull + 2;        // + tile
+constexpr int kBarOFull = kBarPReady + 2;        // + tile
+constexpr int kBarDrain = kBarOFull + 2;
+constexpr int kNumBars = kBarDrain + 1;
+
+template <int HD>
+struct Layout {
+  static constexpr int kTileBytes = 128 * HD * 2;  // one 128-row bf16 tile
+  static constexpr int kQ = 0;                      // two query tiles
+  static constexpr int kK = kQ + 2 * kTileBytes;    // kStages key tiles
+  static constexpr int kV = kK + kStages * kTileBytes;
+  static constexpr int kBar = kV + kStages * kTileBytes;
+  static constexpr int kTmemSlot = kBar + kNumBars * 8;
+  static constexpr int kAbort = kTmemSlot + 4;
+  // Padded past half of the SM's shared memory: one CTA, which allocates all
+  // 512 tensor-memory columns, per SM.
+  static constexpr int kRaw = (kAbort + 4 + 15) / 16 * 16;
+  static constexpr int kBytes = kRaw > 118784 ? kRaw : 118784;
+  static constexpr uint32_t kColO = 0;       // + tile * HD
+  static constexpr uint32_t kColS = 2 * HD;  // + tile * 128
+};
+
+// One task: query tiles qt_a (A) and qt_a + 1 (B, when N reaches it) of query
+// head h of batch element b against key/value tiles kv_lo .. kv_lo + n_kv - 1.
+struct Task {
+  int b, h, qt_a, kv_lo, n_kv;
+  bool has_b;
+};
+
+// Task i of B * Hq * n_pairs.  Causal: heaviest first (a later pair sees more
+// key/value tiles), heads interleaved, a group's side by side.  Without the
+// mask every task costs the same and tasks run head by head.
+struct TaskMap {
+  const ScoreProblem& p;
+  int n_pairs;
+
+  __device__ __forceinline__ RowMask mask(int b) const {
+    return {p.N, p.causal, p.window, p.doc ? p.doc + size_t(b) * p.N : nullptr,
+            p.prefix ? __ldg(p.prefix + b) : 0};
+  }
+  __device__ __forceinline__ Task task(int i) const {
+    const int BH = p.B * p.Hq;
+    const int bh = p.causal ? i % BH : i / n_pairs;
+    const int pair = p.causal ? n_pairs - 1 - i / BH : i % n_pairs;
+    Task t;
+    t.b = bh / p.Hq;
+    t.h = bh - t.b * p.Hq;
+    t.qt_a = 2 * pair;
+    t.has_b = t.qt_a + 1 < p.n_tiles;
+    // The first row of tile A bounds the first key tile (lower bounds never
+    // decrease), the last row of the last tile the last one.
+    const RowMask m = mask(t.b);
+    const int last = min(p.N, (t.qt_a + (t.has_b ? 2 : 1)) * 128) - 1;
+    t.kv_lo = m.lo(t.qt_a * 128) / 128;
+    t.n_kv = (m.hi(last) + 127) / 128 - t.kv_lo;
+    return t;
+  }
+};
+
+// CTA b of G takes tasks b, 2G-1-b, 2G+b, 4G-1-b, ...: a snake over rounds,
+// which evens out the heavy-first order; -1 past the last task.
+__device__ __forceinline__ int snake_task(int k, int b, int G, int n_tasks) {
+  const long long idx = (k & 1) ? (long long)k * G + (G - 1 - b) : (long long)k * G + b;
+  return idx < n_tasks ? int(idx) : -1;
+}
+
+// Descriptor conventions (128-byte swizzle, tiles of 128 rows in 64-column
+// blocks of 16 KB): a K-major operand advances 32 bytes per 16-element k-step
+// within a block and 16 KB across blocks; an MN-major operand advances 2 KB
+// (16 rows) per k-step, its MN extent spanning blocks 16 KB apart (LBO).
+
+template <int HD, bool CAP, bool SLOPES>
+__global__ void __launch_bounds__(kThreads, 1)
+    score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
+                     const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, __nv_bfloat16* __restrict__ O,
+                     float* __restrict__ Lout, const __grid_constant__ ScoreProblem p, int* err) {
+  using Ly = Layout<HD>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if (sbase & 1023u) {  // uniform over the CTA: every thread returns here
+    if (threadIdx.x == 0) report_error(err, kDevSmemAlign, 0x600);
+    return;
+  }
+
+  const int N = p.N;
+  const int n_pairs = (p.n_tiles + 1) >> 1;
+  const int n_tasks = p.B * p.Hq * n_pairs;
+  const int G = int(gridDim.x), cta = int(blockIdx.x);
+  const TaskMap tm{p, n_pairs};
+
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly::kAbort);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::kTmemSlot);
+  auto bar = [&](int i) -> uint32_t { return sbase + Ly::kBar + 8 * i; };
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < kNumBars; ++i)
+      mbar_init(bar(i), i == kBarPReady || i == kBarPReady + 1 ? 128 : 1);
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == kProducerWarp && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+  const WaitCtx ctx{abort_flag, err, kWaitLimitNs};
+  // Everything above overlaps the previous kernel; its results are read below.
+  grid_dep_wait();
+  grid_dep_launch();
+  if (warp == kProducerWarp) {
+    // ------------------------------------------------------------ TMA producer
+    // The whole warp runs the loop (warp-uniform operands); one lane issues.
+    // Key/value tiles run through the ring across tasks (g counts them), so
+    // the next task's first tiles load while this one finishes.
+    bool ok = true;
+    int g = 0;
+    for (int k = 0, i = snake_task(0, cta, G, n_tasks); ok && i >= 0;
+         i = snake_task(++k, cta, G, n_tasks)) {
+      const Task tk = tm.task(i);
+      const int hk = tk.h / p.group;
+      // Both query tiles are free once the previous task's last S completed.
+      if (k > 0 && !(ok = mbar_wait_warp(bar(kBarQEmpty), (k - 1) & 1, ctx, 0x612))) break;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(bar(kBarQFull), (tk.has_b ? 2 : 1) * Ly::kTileBytes);
+        for (int t = 0; t < (tk.has_b ? 2 : 1); ++t)
+#pragma unroll
+          for (int cb = 0; cb < HD / 64; ++cb)
+            tma_load_4d(sbase + Ly::kQ + t * Ly::kTileBytes + cb * 16384, &tmQ, bar(kBarQFull),
+                        cb * 64, (tk.qt_a + t) * 128, tk.h, tk.b);
+      }
+      __syncwarp();
+      for (int j = 0; j < tk.n_kv; ++j, ++g) {
+        const int s = g % kStages, n = g / kStages;
+        if (g >= kStages && !(ok = mbar_wait_warp(bar(kBarKEmpty + s), (n - 1) & 1, ctx, 0x610)))
+          break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(bar(kBarKFull + s), Ly::kTileBytes);
+#pragma unroll
+          for (int cb = 0; cb < HD / 64; ++cb)
+            tma_load_4d(sbase + Ly::kK + s * Ly::kTileBytes + cb * 16384, &tmK,
+                        bar(kBarKFull + s), cb * 64, (tk.kv_lo + j) * 128, hk, tk.b);
+        }
+        __syncwarp();
+        if (g >= kStages && !(ok = mbar_wait_warp(bar(kBarVEmpty + s), (n - 1) & 1, ctx, 0x611)))
+          break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(bar(kBarVFull + s), Ly::kTileBytes);
+#pragma unroll
+          for (int cb = 0; cb < HD / 64; ++cb)
+            tma_load_4d(sbase + Ly::kV + s * Ly::kTileBytes + cb * 16384, &tmV,
+                        bar(kBarVFull + s), cb * 64, (tk.kv_lo + j) * 128, hk, tk.b);
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issuer
+    // The whole warp runs the loop and waits; one elected lane issues.  Every
+    // descriptor is a per-tile base plus a compile-time k-step offset.
+    constexpr uint32_t kIdS = make_idesc_bf16(128, 128, 0, 0);  // S = Q K^T
+    constexpr uint32_t kIdO = make_idesc_bf16(128, HD, 0, 1);   // O += P V
+    const uint64_t dQa = make_sdesc_sw128(sbase + Ly::kQ, 16, 1024);
+    const uint64_t dQb = make_sdesc_sw128(sbase + Ly::kQ + Ly::kTileBytes, 16, 1024);
+    auto issue_s = [&](int t, int stage) {  // elected lane only
+      const uint64_t dq = t == 0 ? dQa : dQb;
+      const uint64_t dk = make_sdesc_sw128(sbase + Ly::kK + stage * Ly::kTileBytes, 16, 1024);
+      const uint32_t d = tbase + Ly::kColS + 128 * t;
+#pragma unroll
+      for (int k = 0; k < HD / 16; ++k) {
+        const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
+        mma_ss(d, sdesc_add(dq, off), sdesc_add(dk, off), kIdS, k > 0 ? 1u : 0u);
+      }
+      tc_commit(bar(kBarSFull + t));
+    };
+    auto issue_pv = [&](int t, int stage, uint32_t acc) {  // elected lane only
+      const uint64_t dv = make_sdesc_sw128(sbase + Ly::kV + stage * Ly::kTileBytes, 16384, 1024);
+      const uint32_t d = tbase + Ly::kColO + HD * t;
+      const uint32_t pc = tbase + Ly::kColS + 128 * t;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)  // 128 keys, 16 per step; P packed 2 per column
+        mma_ts(d, pc + 8 * k, sdesc_add(dv, k * 2048), kIdO, k > 0 ? 1u : acc);
+    };
+    // Handshake counts across tasks: g key/value tiles, ca (cb) S/P rounds of
+    // tile A (B).  A task's first P V overwrites O_t; the softmax warps of
+    // tile t read the previous task's O_t before they signal the first P of
+    // this one, so the P-ready wait covers that hazard.  Tensor-core
+    // instructions of this thread run in issue order, so an S written into
+    // the columns that hold P comes after the P V that reads them.
+    bool ok = true;
+    int g = 0, ca = 0, cb = 0;
+    for (int k = 0, i = snake_task(0, cta, G, n_tasks); ok && i >= 0;
+         i = snake_task(++k, cta, G, n_tasks)) {
+      const Task tk = tm.task(i);
+      const int n_kv = tk.n_kv;
+      if (!(ok = mbar_wait_warp(bar(kBarQFull), k & 1, ctx, 0x620))) break;
+      if (!(ok = mbar_wait_warp(bar(kBarKFull + g % kStages), (g / kStages) & 1, ctx, 0x621)))
+        break;
+      tc_fence_after();
+      if (elect_one()) {
+        issue_s(0, g % kStages);
+        if (tk.has_b) issue_s(1, g % kStages);
+        if (n_kv == 1) tc_commit(bar(kBarQEmpty));  // the task's last S
+        tc_commit(bar(kBarKEmpty + g % kStages));
+      }
+      __syncwarp();
+      for (int j = 0; j < n_kv; ++j, ++g) {
+        const int s = g % kStages;
+        const bool next = j + 1 < n_kv;
+        const int s1 = (g + 1) % kStages, n1 = (g + 1) / kStages;
+        const uint32_t acc = j > 0 ? 1u : 0u;
+        if (!(ok = mbar_wait_warp(bar(kBarVFull + s), (g / kStages) & 1, ctx, 0x622))) break;
+        if (!(ok = mbar_wait_warp(bar(kBarPReady + 0), (ca + j) & 1, ctx, 0x623))) break;
+        tc_fence_after();
+        if (elect_one()) issue_pv(0, s, acc);
+        __syncwarp();
+        if (next) {
+          if (!(ok = mbar_wait_warp(bar(kBarKFull + s1), n1 & 1, ctx, 0x624))) break;
+          tc_fence_after();
+          if (elect_one()) issue_s(0, s1);
+          __syncwarp();
+        }
+        if (tk.has_b) {
+          if (!(ok = mbar_wait_warp(bar(kBarPReady + 1), (cb + j) & 1, ctx, 0x625))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            issue_pv(1, s, acc);
+            if (next) issue_s(1, s1);
+          }
+          __syncwarp();
+        }
+        if (elect_one()) {
+          if (j + 2 == n_kv) tc_commit(bar(kBarQEmpty));  // the task's last S was issued above
+          tc_commit(bar(kBarVEmpty + s));
+          if (next) tc_commit(bar(kBarKEmpty + s1));
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (elect_one()) {
+        tc_commit(bar(kBarOFull + 0));
+        if (tk.has_b) tc_commit(bar(kBarOFull + 1));
+      }
+      __syncwarp();
+      ca += n_kv;
+      if (tk.has_b) cb += n_kv;
+    }
+    // Wait until every MMA issued above has completed before teardown.
+    if (elect_one()) tc_commit(bar(kBarDrain));
+    __syncwarp();
+    volatile int never = 0;  // this wait ignores the CTA abort flag
+    const WaitCtx own{&never, err, kWaitLimitNs};
+    mbar_wait_warp(bar(kBarDrain), 0, own, 0x62F);
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int t = (warp >> 2) & 1;  // 0 = tile A, 1 = tile B
+    const int r = threadIdx.x & 127;
+    const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t tS = tbase + lane_off + Ly::kColS + 128 * t;
+    const uint32_t tO = tbase + lane_off + Ly::kColO + HD * t;
+    const ScoreMap& mp = p.map;
+    bool ok = true;
+    int c = 0;   // S/P rounds of this tile so far
+    int no = 0;  // outputs of this tile so far
+    for (int k = 0, i = snake_task(0, cta, G, n_tasks); ok && i >= 0;
+         i = snake_task(++k, cta, G, n_tasks)) {
+      const Task tk = tm.task(i);
+      if (t == 1 && !tk.has_b) continue;
+      const int q_tile0 = (tk.qt_a + t) * 128;
+      const int q = q_tile0 + r;
+      const RowMask mask = tm.mask(tk.b);
+      // The row sees keys lo_q <= j < hi_q; every row of the warp sees those
+      // of [any_lo, all_hi).
+      const int lo_q = mask.lo(q), hi_q = mask.hi(q);
+      const int all_lo = __reduce_max_sync(0xffffffffu, lo_q);
+      const int all_hi = __reduce_min_sync(0xffffffffu, hi_q);
+      const float slope = SLOPES ? __ldg(mp.slopes + tk.h) * 1.4426950408889634f : 0.f;
+      float m = -INFINITY;  // running max of the base-2 scores
+      float l = 0.f;        // running sum of 2^(x - m)
+      for (int j = 0; j < tk.n_kv; ++j) {
+        if (!(ok = mbar_wait_warp(bar(kBarSFull + t), (c + j) & 1, ctx, 0x630 + t))) break;
+        tc_fence_after();
+        uint32_t u[128];
+        tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&u[0]));
+        tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&u[32]));
+        tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&u[64]));
+        tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&u[96]));
+        tmem_wait_ld();
+        const int kv0 = (tk.kv_lo + j) * 128;
+        auto f = [&](int e) { return __uint_as_float(u[e]); };
+        auto pair = [&](int e) { return f32x2(f(e), f(e + 1)); };
+        auto put = [&](int e, uint64_t x) {
+          float a, b;
+          f32x2_split(x, a, b);
+          u[e] = __float_as_uint(a);
+          u[e + 1] = __float_as_uint(b);
+        };
+        // u -> x, in place
+        if constexpr (CAP) {
+          float a8[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) a8[e] = fabsf(f(e));
+#pragma unroll
+          for (int e = 8; e < 128; e += 2)
+            a8[(e >> 1) & 7] = max3f(a8[(e >> 1) & 7], fabsf(f(e)), fabsf(f(e + 1)));
+          const float top = max3f(max3f(a8[0], a8[1], a8[2]), max3f(a8[3], a8[4], a8[5]),
+                                  fmaxf(a8[6], a8[7]));
+          if (__all_sync(0xffffffffu, top <= mp.poly_limit)) {
+#pragma unroll
+            for (int e = 0; e < 128; e += 2) put(e, cap_poly(mp, pair(e)));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 128; ++e)
+              u[e] = __float_as_uint(fmaf(cap_r(mp, f(e)), -2.f * mp.cap_log2, mp.cap_log2));
+          }
+        } else {
+          const uint64_t sc = f32x2(mp.scale_log2);
+#pragma unroll
+          for (int e = 0; e < 128; e += 2) put(e, mul_f32x2(pair(e), sc));
+        }
+        // Distances are whole numbers, exact below 2^24.
+        if constexpr (SLOPES) {
+          const float d0 = float(q - kv0);
+          const int w0 = q_tile0 + 32 * (warp & 3);  // the warp's first row
+          if (kv0 + 127 <= w0 || kv0 >= w0 + 31) {
+            const uint64_t sl = f32x2(kv0 + 127 <= w0 ? -slope : slope), two = f32x2(-2.f);
+            uint64_t dist = f32x2(d0, d0 - 1.f);
+#pragma unroll
+            for (int e = 0; e < 128; e += 2) {
+              put(e, fma_f32x2(sl, dist, pair(e)));
+              dist = add_f32x2(dist, two);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 128; ++e)
+              u[e] = __float_as_uint(fmaf(-slope, fabsf(d0 - float(e)), f(e)));
+          }
+        }
+        if (kv0 < all_lo || kv0 + 128 > all_hi) {
+          const int e_lo = lo_q - kv0, e_hi = hi_q - kv0;
+#pragma unroll
+          for (int e = 0; e < 128; ++e)
+            if (e >= e_hi || e < e_lo) u[e] = __float_as_uint(-INFINITY);
+        }
+        // row maximum: eight chains of three-input maxima (two scores each)
+        float m8[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m8[e] = f(e);
+#pragma unroll
+        for (int e = 8; e < 128; e += 2)
+          m8[(e >> 1) & 7] = max3f(m8[(e >> 1) & 7], f(e), f(e + 1));
+        const float mx = max3f(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], m8[5]),
+                               fmaxf(m8[6], m8[7]));
+        const float m_new = fmaxf(m, mx);
+        // Lazy rescale: move the reference maximum (and rescale l and O by
+        // 2^(m - m_new)) only when the maximum grew by more than 8 in base 2.
+        const bool rescale = m_new > m + 8.f;
+        const float alpha = rescale ? ex2(m - m_new) : 1.f;
+        if (rescale) {
+          l *= alpha;
+          m = m_new;
+        }
+        const uint64_t mb = f32x2((m == -INFINITY) ? 0.f : -m);
+        float rs[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int c2 = 0; c2 < 32; ++c2) {
+            float x0, x1;
+            f32x2_split(add_f32x2(pair(64 * h + 2 * c2), mb), x0, x1);
+            const float p0 = ex2(x0);
+            const float p1 = ex2(x1);
+            rs[c2 & 3] += p0 + p1;
+            pk[c2] = pack_bf16x2(p0, p1);
+          }
+          tmem_st32(tS + 32 * h, pk);
+        }
+        l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
+        // tcgen05.ld/st are warp-collective: if any row of the warp moved its
+        // maximum, the whole warp rescales (alpha = 1 leaves the other rows
+        // unchanged).  O holds P V of earlier tiles; PV(j-1) has completed.
+        if (j > 0 && __any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+          for (int c4 = 0; c4 < HD / 32; ++c4) {
+            uint32_t o[32];
+            tmem_ld32(tO + 32 * c4, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st32(tO + 32 * c4, o);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(kBarPReady + t));
+      }
+      if (!ok) break;
+      c += tk.n_kv;
+      if (!(ok = mbar_wait_warp(bar(kBarOFull + t), no & 1, ctx, 0x638 + t))) break;
+      ++no;
+      tc_fence_after();
+      const float inv_l = 1.f / l;
+      const size_t row = (size_t(tk.b) * p.Hq + tk.h) * N + q;
+      __nv_bfloat16* orow = O + row * HD;
+#pragma unroll
+      for (int c4 = 0; c4 < HD / 32; ++c4) {
+        uint32_t o[32];
+        tmem_ld32(tO + 32 * c4, o);
+        tmem_wait_ld();
+        if (q < N) {
+#pragma unroll
+          for (int c8 = 0; c8 < 4; ++c8) {
+            uint32_t w4[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w4[e] = pack_bf16x2(__uint_as_float(o[8 * c8 + 2 * e]) * inv_l,
+                                  __uint_as_float(o[8 * c8 + 2 * e + 1]) * inv_l);
+            st_global_v4(orow + 32 * c4 + 8 * c8, w4[0], w4[1], w4[2], w4[3]);
+          }
+        }
+      }
+      if (q < N) Lout[row] = (m + log2f(l)) * 0.69314718055994530942f;
+      // O_t has been read into registers (tmem_wait_ld above) before this
+      // warp signals the next task's first P.
+      tc_fence_before();
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  if (*abort_flag && threadIdx.x == 0) {
+    // Give copies still in flight time to land before the CTA retires.
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) {
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tbase, kTmemCols);
+  }
+}
+
+template <int HD, bool CAP, bool SLOPES>
+static cudaError_t launch_t(const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                            const CUtensorMap& tmV, void* O, float* L, const ScoreProblem& p,
+                            int* err, cudaStream_t stream) {
+  using Ly = Layout<HD>;
+  cudaError_t e = set_smem_limit_once<score_fwd_kernel<HD, CAP, SLOPES>>(Ly::kBytes);
+  if (e != cudaSuccess) return e;
+  const long long n_tasks = (long long)((p.n_tiles + 1) / 2) * p.B * p.Hq;
+  const dim3 grid(unsigned(fwd_grid(n_tasks, p.causal)));
+  return launch_kernel(score_fwd_kernel<HD, CAP, SLOPES>, grid, dim3(kThreads), Ly::kBytes, stream,
+                       tmQ, tmK, tmV, static_cast<__nv_bfloat16*>(O), L, p, err);
+}
+
+template <int HD>
+static cudaError_t launch_d(const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                            const CUtensorMap& tmV, void* O, float* L, const ScoreProblem& p,
+                            int* err, cudaStream_t stream) {
+  if (p.cap)
+    return p.map.slopes ? launch_t<HD, true, true>(tmQ, tmK, tmV, O, L, p, err, stream)
+                        : launch_t<HD, true, false>(tmQ, tmK, tmV, O, L, p, err, stream);
+  return p.map.slopes ? launch_t<HD, false, true>(tmQ, tmK, tmV, O, L, p, err, stream)
+                      : launch_t<HD, false, false>(tmQ, tmK, tmV, O, L, p, err, stream);
+}
+
+}  // namespace score_fwd
+
+cudaError_t launch_score_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                             const CUtensorMap& tmV, void* O, float* L, const ScoreProblem& p,
+                             int* err, cudaStream_t stream) {
+  return p.d == 64 ? score_fwd::launch_d<64>(tmQ, tmK, tmV, O, L, p, err, stream)
+                   : score_fwd::launch_d<128>(tmQ, tmK, tmV, O, L, p, err, stream);
+}
+
+}  // namespace attn

@@ -452,6 +452,61 @@ int attn_decode(const void* Q, const void* K_cache, const void* V_cache, const f
                 void* stream);
 
 /*
+ * Attention with changed scores, forward and backward: scores capped by a
+ * tanh, a bias that falls with distance, a prefix that sees itself whole, and
+ * key heads that several query heads share.  The pages list such variants of
+ * attention ("Training - CUDA Moat Still Alive", section on attention
+ * variants) without their formulas.  With u_ij = scale <q_i, k_j>:
+ *
+ *   softcap > 0:  x_ij = softcap tanh(u_ij / softcap), else x_ij = u_ij
+ *   slopes:       x_ij -= slopes[h] |i - j|, after the cap; fp32 [Hq], any
+ *                 finite sign; NULL = none
+ *   L_i = logsumexp_j x_ij,  O_i = sum_j exp(x_ij - L_i) v_j
+ *
+ * over the keys j that query i sees: all without the causal mask; with it
+ * j <= i, and
+ *
+ *   window, doc_start  as in attn_fwd_ex (doc_start int32 [B][N])
+ *   prefix             int32 [B], device memory: also every j < prefix[b]
+ *                      (0 or less: the causal mask; N or more: all).  Not
+ *                      together with window or doc_start.
+ *
+ * All three need causal = 1 (ATTN_ERR_INVALID_ARG otherwise).
+ *
+ *   Q, K, V     bf16 [B][Hq][N][d] and [B][Hkv][N][d]; query head h reads key
+ *               head h / (Hq / Hkv), Hq a multiple of Hkv >= 1
+ *   strides     host array of 9 element strides: batch, head and token stride
+ *               of Q, then K's, then V's; the head dimension is contiguous.
+ *               Every stride of a dimension longer than 1 is a positive
+ *               multiple of 8, below 2^39.  NULL = contiguous.  So heads of a
+ *               fused projection [B][N][heads][d] are taken as they lie.
+ *   O, L        bf16 [B][Hq][N][d], contiguous, and fp32 [B][Hq][N]
+ *
+ * The backward takes the forward's inputs, O and L and the gradient dO
+ * (contiguous, like O) and writes dQ [B][Hq][N][d] and dK, dV [B][Hkv][N][d],
+ * contiguous, the latter two summed over the query heads that share a key
+ * head.  The slopes have no gradient.  Workspace:
+ * attn_bwd_workspace_size(B, Hq, N, d) bytes, 256-byte aligned.  dK and dV
+ * repeat bit for bit; dQ is summed in an order that varies, in fp32, as
+ * attn_bwd's is.
+ *
+ * Precision: scores, maxima and sums are fp32 (a cap's tanh to 6e-8 of itself
+ * where every score of a tile is below 0.8 softcap, else to some 2^-22 of the
+ * cap); P and dx meet the tensor core in bf16, each rounded once.  As in
+ * attn_fwd_ex, a value of V (dO, Q, K in the backward) that the mask hides
+ * from a row must be finite: its weight is 0, and 0 times infinity is NaN.
+ */
+int attn_fwd_score(const void* Q, const void* K, const void* V, const int64_t* strides, void* O,
+                   float* L, int B, int Hq, int Hkv, int N, int d, int causal, int window,
+                   const int* doc_start, const int* prefix, float softcap, const float* slopes,
+                   float scale, void* stream);
+int attn_bwd_score(const void* Q, const void* K, const void* V, const int64_t* strides,
+                   const void* O, const void* dO, const float* L, void* dQ, void* dK, void* dV,
+                   int B, int Hq, int Hkv, int N, int d, int causal, int window,
+                   const int* doc_start, const int* prefix, float softcap, const float* slopes,
+                   float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Interface utility of this library's boundary (failure detection); the paper
  * has no counterpart.
  * Synchronise `stream`, then read and clear the current device's error word.
