@@ -87,6 +87,9 @@ def load_library(path: str | None = None):
             "kv_cache_read": (i, [vp] * 9 + [i] * 7 + [vp]),
             "attn_decode_workspace_size": (sz, [i]),
             "attn_decode": (i, [vp] * 9 + [i] * 8 + [f, vp, sz, vp]),
+            "int4_cache_write": (i, [vp] * 10 + [i] * 7 + [vp]),
+            "int4_cache_read": (i, [vp] * 9 + [i] * 7 + [vp]),
+            "attn_score_decode": (i, [vp] * 5 + [i] + [vp] * 4 + [i] * 8 + [f, vp, f, vp, sz, vp]),
             "attn_fwd_score": (i, [vp] * 6 + [i] * 7 + [vp, vp, f, vp, f, vp]),
             "attn_bwd_score": (i, [vp] * 10 + [i] * 7 + [vp, vp, f, vp, f, vp, sz, vp]),
             "attn_last_device_error": (i, [vp]),
@@ -424,6 +427,8 @@ def ssd_bwd(x, dt, A, B, C, D, dy, workspace=None, out=None, stream=None):
 # the reason, so that a call of a few microseconds on the GPU is not drowned by
 # its checks.
 _INT_MAX = 2 ** 31 - 1  # ctypes would drop the bits above
+_INT4_GROUP = 32  # values of a 4-bit row that share a factor
+_CACHE_BF16, _CACHE_E4M3, _CACHE_INT4 = 0, 1, 2  # attn_cache_type_t
 _E4M3_DTYPES = (torch.float8_e4m3fn, torch.uint8)
 _DEVICES = [torch.device("cuda", i) for i in range(64)]  # cheaper to pass than an index
 # PyTorch's own shortcuts where it has them; a build without CUDA does not, and
@@ -520,26 +525,40 @@ def _check_rows(t: torch.Tensor, name: str, shape, dev: int):
     return sb, sh, sn
 
 
+def _is_int4(k_descale) -> bool:
+    """Whether a cache's factors say that it holds four bits a value."""
+    return k_descale is not None and k_descale.dtype is torch.bfloat16
+
+
 def _check_cache(k_cache, v_cache, k_descale, v_descale, page_table, dev):
     """(pages, Hkv, page_size, d, B, max_pages) of a cache and its page table."""
     shape = k_cache.shape
     if len(shape) != 4:
         raise ValueError("k_cache must be [pages, Hkv, page_size, d], got %s" % (tuple(shape),))
     dtype = k_cache.dtype
+    held = shape
     if k_descale is None or v_descale is None:
         if k_descale is not v_descale:
             raise ValueError("k_descale and v_descale come together")
         if dtype is not torch.bfloat16:
             raise ValueError("k_cache must be torch.bfloat16 without descale factors, got %s"
                              % dtype)
+    elif _is_int4(k_descale):
+        if dtype is not torch.uint8:
+            raise ValueError("k_cache must be torch.uint8, two values to a byte, with bf16 "
+                             "factors, got %s" % dtype)
+        shape = (*shape[:3], 2 * shape[3])
+        factors = (*shape[:3], shape[3] // _INT4_GROUP)
+        _check_like(k_descale, "k_descale", factors, torch.bfloat16, dev)
+        _check_like(v_descale, "v_descale", factors, torch.bfloat16, dev)
     else:
         if dtype not in _E4M3_DTYPES:
             raise ValueError("k_cache must hold e4m3 bytes (float8_e4m3fn or uint8) with descale "
                              "factors, got %s" % dtype)
         _check_like(k_descale, "k_descale", shape[:3], torch.float32, dev)
         _check_like(v_descale, "v_descale", shape[:3], torch.float32, dev)
-    _check_like(k_cache, "k_cache", shape, dtype, dev)
-    _check_like(v_cache, "v_cache", shape, dtype, dev)
+    _check_like(k_cache, "k_cache", held, dtype, dev)
+    _check_like(v_cache, "v_cache", held, dtype, dev)
     table = page_table.shape
     if len(table) != 2:
         raise ValueError("page_table must be [B, max_pages], got %s" % (tuple(table),))
@@ -726,11 +745,24 @@ def attn_bwd_score(q, k, v, o, do, lse, causal: bool, scale=None, softcap=0.0, s
 
 def alloc_kv_cache(num_pages: int, Hkv: int, page_size: int, d: int, device,
                    dtype=torch.bfloat16):
-    """(k_cache, v_cache, k_descale, v_descale), zeroed: a bf16 cache (factors
-    None), or an e4m3 one (dtype torch.float8_e4m3fn) with its fp32 factors."""
-    if dtype not in (torch.bfloat16, torch.float8_e4m3fn):
-        raise ValueError("dtype must be torch.bfloat16 or torch.float8_e4m3fn, got %s" % dtype)
+    """(k_cache, v_cache, k_descale, v_descale), all values zero: a bf16 cache
+    (factors None), an e4m3 one (dtype torch.float8_e4m3fn) with its fp32
+    factors [pages, Hkv, page_size], or a 4-bit one (dtype "int4"), bytes
+    [pages, Hkv, page_size, d / 2] with bf16 factors [pages, Hkv, page_size,
+    d / 32]."""
     shape = (num_pages, Hkv, page_size, d)
+    if dtype == "int4":
+        if d % _INT4_GROUP:
+            raise ValueError("d must be a multiple of %d in a 4-bit cache, got %d"
+                             % (_INT4_GROUP, d))
+        caches = [torch.full((*shape[:3], d // 2), 0x88, dtype=torch.uint8, device=device)
+                  for _ in range(2)]
+        factors = [torch.ones((*shape[:3], d // _INT4_GROUP), dtype=torch.bfloat16, device=device)
+                   for _ in range(2)]
+        return caches[0], caches[1], factors[0], factors[1]
+    if dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise ValueError('dtype must be torch.bfloat16, torch.float8_e4m3fn or "int4", got %s'
+                         % (dtype,))
     fp8 = dtype == torch.float8_e4m3fn
     caches = [torch.zeros(shape, dtype=torch.uint8 if fp8 else dtype, device=device)
               for _ in range(2)]
@@ -753,9 +785,10 @@ def kv_cache_write(k, v, k_cache, v_cache, page_table, start, count=None, k_desc
     k, v: bf16 [B, Hkv, T, d], strides as free as rope_fwd's.  Token t <
     count[b] (default: all T) becomes position start[b] + t of sequence b.
     k_cache, v_cache: [pages, Hkv, page_size, d], bf16, or e4m3 with fp32
-    factors k_descale, v_descale [pages, Hkv, page_size], which the call
-    chooses for every row it writes.  page_table: int32 [B, max_pages];
-    start, count: int32 [B].
+    factors k_descale, v_descale [pages, Hkv, page_size], or uint8 [pages, Hkv,
+    page_size, d / 2], four bits a value, with bf16 factors [pages, Hkv,
+    page_size, d / 32]; the call chooses the factors of every row it writes.
+    page_table: int32 [B, max_pages]; start, count: int32 [B].
     """
     dev = _device_index(k_cache, "k_cache")
     P, Hkv, ps, d, B, mp = _check_cache(k_cache, v_cache, k_descale, v_descale, page_table, dev)
@@ -765,12 +798,11 @@ def kv_cache_write(k, v, k_cache, v_cache, page_table, start, count=None, k_desc
     _check_span(start, count, B, dev)
     if B * Hkv * T > _INT_MAX:  # expanded rows take no memory
         _check("kv_cache_write", ATTN_ERR_UNSUPPORTED)
-    st = load_library().kv_cache_write(k.data_ptr(), v.data_ptr(),
-                                       _array(ctypes.c_int64, strides),
-                                       k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_descale),
-                                       _ptr(v_descale), page_table.data_ptr(), start.data_ptr(),
-                                       _ptr(count), B, Hkv, T, d, ps, P, mp,
-                                       _stream_on(stream, dev))
+    lib = load_library()
+    write = lib.int4_cache_write if _is_int4(k_descale) else lib.kv_cache_write
+    st = write(k.data_ptr(), v.data_ptr(), _array(ctypes.c_int64, strides), k_cache.data_ptr(),
+               v_cache.data_ptr(), _ptr(k_descale), _ptr(v_descale), page_table.data_ptr(),
+               start.data_ptr(), _ptr(count), B, Hkv, T, d, ps, P, mp, _stream_on(stream, dev))
     if st:
         _check("kv_cache_write", st)
 
@@ -791,10 +823,11 @@ def kv_cache_read(k_cache, v_cache, page_table, start, T: int, count=None, k_des
         k, v = out
         _check_like(k, "out[0]", shape, torch.bfloat16, dev)
         _check_like(v, "out[1]", shape, torch.bfloat16, dev)
-    st = load_library().kv_cache_read(k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_descale),
-                                      _ptr(v_descale), page_table.data_ptr(), start.data_ptr(),
-                                      _ptr(count), k.data_ptr(), v.data_ptr(), B, Hkv, int(T), d,
-                                      ps, P, mp, _stream_on(stream, dev))
+    lib = load_library()
+    read = lib.int4_cache_read if _is_int4(k_descale) else lib.kv_cache_read
+    st = read(k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_descale), _ptr(v_descale),
+              page_table.data_ptr(), start.data_ptr(), _ptr(count), k.data_ptr(), v.data_ptr(), B,
+              Hkv, int(T), d, ps, P, mp, _stream_on(stream, dev))
     if st:
         _check("kv_cache_read", st)
     return k, v
@@ -836,13 +869,17 @@ def _decode_workspace(dev: int, stream):
 
 
 def attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, k_descale=None,
-                v_descale=None, window=0, out=None, lse=None, workspace=None, stream=None):
+                v_descale=None, window=0, out=None, lse=None, workspace=None, stream=None,
+                softcap=0.0, slopes=None):
     """O and the log-sum-exp L of one new token per sequence over a paged cache.
 
     q: bf16 [B, Hq, 1, d], contiguous, Hq a multiple of the cache's Hkv;
     cache arguments as for kv_cache_write; seq_lens: int32 [B], the sequences'
     lengths with the new token (whose k and v are in the cache already).
     window > 0: only the last ``window`` positions are seen.
+    softcap > 0: scores become softcap * tanh(score / softcap).  slopes: fp32
+    [Hq]; scores then lose slopes[h] * (distance from the new token), as
+    attn_fwd_score's do.
     Returns (O bf16 [B, Hq, 1, d], L fp32 [B, Hq, 1]); a sequence of length 0
     has O = 0 and L = -inf.  workspace: from alloc_decode_workspace; without
     one, the call uses one that is kept for its stream (7.5 MB; allocated anew
@@ -880,6 +917,18 @@ def attn_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, k_descale
     else:
         kd, vd = k_descale.data_ptr(), v_descale.data_ptr()
     window = max(-1, min(int(window), _INT_MAX))  # what no length reaches hides nothing
+    if softcap or slopes is not None or _is_int4(k_descale):
+        if slopes is not None:
+            _check_like(slopes, "slopes", (Hq,), torch.float32, dev)
+        kind = _CACHE_INT4 if _is_int4(k_descale) else _CACHE_BF16 if kd is None else _CACHE_E4M3
+        st = load_library().attn_score_decode(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kd, vd, kind,
+            page_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, Hkv,
+            d, ps, P, mp, window, float(softcap), _ptr(slopes), _default_scale(d, scale),
+            workspace.data_ptr(), workspace.nbytes, handle)
+        if st:
+            _check("attn_score_decode", st)
+        return out, lse
     st = load_library().attn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kd, vd,
                                     page_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
                                     lse.data_ptr(), B, Hq, Hkv, d, ps, P, mp, window,

@@ -1,0 +1,206 @@
+// kv_cache_int4.cu -- the paged key/value cache in four bits (int4.cuh), as it is
+// written and as it is read back.
+//
+// Of a group of 32 values, amax its largest finite magnitude:
+//
+//   f = amax / 7 rounded to five significant bits, ties to even; at least
+//       2^-120; 1 where amax = 0; NaN where the group holds a NaN
+//   c = round(x / f), ties to even, clamped to -7 .. 7
+//
+// f is within 1/33 of amax / 7, so the largest value still rounds to 7 and no
+// finite one is clamped.  Both roundings are of the exact quotient.  amax / 7
+// is a fp32 division, whose result is a tie of five bits only if the quotient
+// is (a quotient of a bf16 number by 7 that is not one lies at least 2^-12 of
+// itself away).  x / f, a division for every value, is a product with the
+// reciprocal and Markstein's correction (P. Markstein, 1990: with r = 1 / f
+// rounded to nearest and q = x r, q + r (x - q f) is the quotient rounded to
+// nearest), which ties need: x r alone misses 7.5 by a last bit.  Adding
+// 1.5 2^23 + 8 rounds it to a whole number, ties to even, and leaves c + 8 in
+// the low bits; eight of them join by multiplications.
+//
+// A value that is read back, c f, is a bf16 number: no rounding at all.
+//
+// Bound by HBM: a written row is read once (2 d bytes) and written once (d / 2
+// and d / 16 of factors); reading back is the reverse.
+#include "f32x2.cuh"
+#include "int4.cuh"
+#include "kv_rows.cuh"
+
+namespace attn {
+namespace {
+
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Largest finite magnitude of a lane's eight values as bf16 bits; 0xFFFF where
+// one is a NaN.  *inf: whether there is an infinity.
+__device__ __forceinline__ uint32_t amax8(const uint4& x, bool* inf) {
+  const uint32_t w[4] = {x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu, x.z & 0x7FFF7FFFu,
+                         x.w & 0x7FFF7FFFu};
+  uint32_t m = max_u16x2(max_u16x2(w[0], w[1]), max_u16x2(w[2], w[3]));
+  m = max(m & 0xFFFFu, m >> 16);
+  *inf = false;
+  if (m < 0x7F80u) return m;
+  if (m > 0x7F80u) return 0xFFFFu;
+  *inf = true;
+  m = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t lo = w[k] & 0xFFFFu, hi = w[k] >> 16;
+    m = max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+  }
+  return m;
+}
+
+// The group's factor from amax's bf16 bits.
+__device__ __forceinline__ float factor_of(uint32_t amax) {
+  if (amax == 0) return 1.f;
+  uint32_t q = __float_as_uint(__uint_as_float(amax << 16) / 7.f);
+  q += 0x3FFFFu + ((q >> 19) & 1u);  // to five significant bits, ties to even
+  return fmaxf(__uint_as_float(q & ~0x7FFFFu), 7.5231638452626401e-37f /* 2^-120 */);
+}
+
+// Eight values as nibbles.
+__device__ __forceinline__ uint32_t codes8(const uint4& v, float f, bool inf) {
+  const float r = 1.f / f, top = 7.f * f;
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t out = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float x0 = bf16lo_to_f32(w[k]), x1 = bf16hi_to_f32(w[k]);
+    if (inf) {
+      x0 = fminf(fmaxf(x0, -top), top);
+      x1 = fminf(fmaxf(x1, -top), top);
+    }
+    const uint64_t x = f32x2(x0, x1), rr = f32x2(r, r);
+    const uint64_t q = mul_f32x2(x, rr);
+    const uint64_t rest = fma_f32x2(q, f32x2(-f, -f), x);
+    const float bias = 12582920.f;  // 1.5 2^23 + 8
+    float a, b;
+    f32x2_split(add_f32x2(fma_f32x2(rest, rr, q), f32x2(bias, bias)), a, b);
+    out += __float_as_uint(a) * (1u << (8 * k)) + __float_as_uint(b) * (16u << (8 * k));
+  }
+  return out - 0x4B400000u * 0x11111111u;  // the bits of 1.5 2^23, eight times
+}
+
+// As kv_cache.cu's e4m3 rows: D / 16 lanes take a row of K and of V, eight
+// values of either half each.  Four lanes share a group.
+template <int D>
+__global__ void __launch_bounds__(kThreads)
+    kv_write_int4_kernel(const CacheArgs c, const CacheRows r, unsigned rows, int* err) {
+  constexpr int kLanes = D / 16, kGroups = kThreads / kLanes;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x % kLanes;
+  const unsigned i = blockIdx.x * kGroups + threadIdx.x / kLanes;
+  uint4 x[2][2] = {};
+  int64_t dst = -1;
+  if (i < rows) {
+    const Row w = row_of(i, c, r);
+    dst = locate(c, r, w, kSiteWritePage, lane, err);
+    if (dst >= 0) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(r.x[s]) +
+                                                          w.b * r.sb[s] + w.h * r.sh[s] +
+                                                          w.t * r.st[s]);
+        x[s][0] = __ldg(src + lane);
+        x[s][1] = __ldg(src + kLanes + lane);
+      }
+    }
+  }
+  if (!__any_sync(0xffffffffu, dst >= 0)) return;  // a padded batch's filling
+  bool inf[2][2];
+  uint32_t amax[2];  // of either half: K's in the low 16 bits, V's in the high ones
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    amax[half] = amax8(x[0][half], &inf[0][half]) | amax8(x[1][half], &inf[1][half]) << 16;
+#pragma unroll
+    for (int o = 2; o > 0; o >>= 1)
+      amax[half] = max_u16x2(amax[half], __shfl_xor_sync(0xffffffffu, amax[half], o));
+  }
+  if (dst < 0) return;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    uint32_t* codes = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(s ? c.vc : c.kc) +
+                                                  dst * (D / 2));
+    uint16_t* factors = (s ? c.vf : c.kf) + dst * (D / kInt4Group);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const uint32_t m = s ? amax[half] >> 16 : amax[half] & 0xFFFFu;
+      const bool nan = m == 0xFFFFu;
+      const float f = factor_of(nan ? 0u : m);
+      codes[half * kLanes + lane] = codes8(x[s][half], f, inf[s][half] || nan);
+      if (lane % 4 == 0)
+        factors[(half * kLanes + lane) / 4] = nan ? 0x7FFFu : uint16_t(__float_as_uint(f) >> 16);
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads)
+    kv_read_int4_kernel(const CacheArgs c, const CacheRows r, unsigned rows, int* err) {
+  constexpr int kLanes = D / 16, kGroups = kThreads / kLanes;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x % kLanes;
+  const unsigned i = blockIdx.x * kGroups + threadIdx.x / kLanes;
+  if (i >= rows) return;
+  uint4 y[2][2] = {};
+  const int64_t src = locate(c, r, row_of(i, c, r), kSiteReadPage, lane, err);
+  if (src >= 0) {
+    uint32_t u[2][2], f[2][2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const uint32_t* codes = reinterpret_cast<const uint32_t*>(
+          static_cast<const uint8_t*>(s ? c.vc : c.kc) + src * (D / 2));
+      const uint16_t* factors = (s ? c.vf : c.kf) + src * (D / kInt4Group);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        u[s][half] = __ldg(codes + half * kLanes + lane);
+        f[s][half] = __ldg(factors + (half * kLanes + lane) / 4) * 0x00010001u;
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        // elements p and p + 4, put back in order
+        uint32_t z[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) z[p] = int4_pair(u[s][half], p, f[s][half]);
+        y[s][half] = make_uint4(__byte_perm(z[0], z[1], 0x5410), __byte_perm(z[2], z[3], 0x5410),
+                                __byte_perm(z[0], z[1], 0x7632), __byte_perm(z[2], z[3], 0x7632));
+      }
+  }
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {  // the output is contiguous: row i of [B][Hkv][T]
+    uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(r.x[s]) + int64_t(i) * D);
+    out[lane] = y[s][0];
+    out[kLanes + lane] = y[s][1];
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_write_int4(const CacheArgs& c, const CacheRows& r, int* err,
+                                 cudaStream_t stream) {
+  return c.d == 64 ? launch(kv_write_int4_kernel<64>, c, r, err, stream)
+                   : launch(kv_write_int4_kernel<128>, c, r, err, stream);
+}
+
+cudaError_t launch_kv_read_int4(const CacheArgs& c, const CacheRows& r, int* err,
+                                cudaStream_t stream) {
+  return c.d == 64 ? launch(kv_read_int4_kernel<64>, c, r, err, stream)
+                   : launch(kv_read_int4_kernel<128>, c, r, err, stream);
+}
+
+}  // namespace attn

@@ -10,14 +10,12 @@
 #include <stdint.h>
 
 #include "kernels.h"
+#include "score_tanh.h"
 
 namespace attn {
 
 // The current device's error word (attn_api.cu); null if it has none.
 int* error_word_ptr();
-
-// Below this |y| the kernels take tanh(y) from an odd polynomial.
-constexpr int kTanhTerms = 6;
 
 // What turns a raw product u = <q, k> into a score in base 2.
 struct ScoreMap {

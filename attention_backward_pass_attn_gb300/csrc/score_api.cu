@@ -10,14 +10,7 @@
 
 namespace attn {
 
-// tanh(y) = y (c0 + c1 y^2 + ... + c5 y^10) on |y| <= 0.8, the polynomial of
-// the smallest relative error (5.8e-8), found by Remez exchange.
-namespace {
-constexpr double kTanh[kTanhTerms] = {0.999999942083,   -0.333326749194, 0.133210482804,
-                                      -0.0531143154981, 0.0190933004507, -0.0043552995703};
-constexpr double kTanhReach = 0.8;
-constexpr double kLog2e = 1.4426950408889634;
-}  // namespace
+static constexpr double kLog2e = 1.4426950408889634;
 
 bool make_score_map(float scale, float softcap, const float* slopes, ScoreMap* m) {
   *m = {};
@@ -33,7 +26,7 @@ bool make_score_map(float scale, float softcap, const float* slopes, ScoreMap* m
   bool good = std::isfinite(m->inv_cap_log2_sq);
   double power = scale * kLog2e;  // x = u (scale log2e) sum_k c_k (c u)^2k
   for (int k = 0; k < kTanhTerms; ++k, power *= c * c) {
-    m->poly[k] = float(kTanh[k] * power);
+    m->poly[k] = float(tanh_poly(k) * power);
     good = good && std::isfinite(m->poly[k]);
   }
   const float limit = float(kTanhReach / c);
@@ -96,21 +89,32 @@ Shape shape_of(const ScoreProblem& p, int H) {
   return s;
 }
 
-// The map of operand `which` (0: Q, 1: K, 2: V) with the caller's strides
-// (batch, head, token of each) or contiguous rows.
-int rows_map(CUtensorMap* map, const void* ptr, const int64_t* strides, int which,
-             const ScoreProblem& p) {
-  const int H = which ? p.Hkv : p.Hq;
-  const int64_t rows[3] = {int64_t(H) * p.N * p.d, int64_t(p.N) * p.d, p.d};
-  const int n[3] = {p.B, H, p.N};
-  int64_t s[3];
-  for (int k = 0; k < 3; ++k) {
-    // a dimension of one index has no stride to speak of
-    s[k] = strides && n[k] > 1 ? strides[3 * which + k] : rows[k];
-    if (s[k] < 1 || s[k] % 8) return ATTN_ERR_INVALID_ARG;
-    if (s[k] >= int64_t(1) << 39) return ATTN_ERR_UNSUPPORTED;  // 2^40 bytes
+// Strides of Q, K and V (batch, head, token): the caller's, or contiguous rows'.
+struct RowStrides {
+  int64_t s[3][3];
+};
+int set_strides(const int64_t* given, const ScoreProblem& p, RowStrides* out) {
+  for (int w = 0; w < 3; ++w) {
+    const int H = w ? p.Hkv : p.Hq;
+    const int64_t rows[3] = {int64_t(H) * p.N * p.d, int64_t(p.N) * p.d, p.d};
+    const int n[3] = {p.B, H, p.N};
+    for (int k = 0; k < 3; ++k) {
+      // a dimension of one index has no stride to speak of
+      const int64_t s = given && n[k] > 1 ? given[3 * w + k] : rows[k];
+      if (s < 1 || s % 8) return ATTN_ERR_INVALID_ARG;
+      if (s >= int64_t(1) << 39) return ATTN_ERR_UNSUPPORTED;  // 2^40 bytes
+      out->s[w][k] = s;
+    }
   }
-  return make_rows_map(map, ptr, s, p.B, H, p.N, p.d) ? ATTN_ERR_CUDA : ATTN_OK;
+  return ATTN_OK;
+}
+
+// The three operands' maps; false if one cannot be encoded.
+bool make_maps(CUtensorMap* q, CUtensorMap* k, CUtensorMap* v, const void* Q, const void* K,
+               const void* V, const RowStrides& st, const ScoreProblem& p) {
+  return !make_rows_map(q, Q, st.s[0], p.B, p.Hq, p.N, p.d) &&
+         !make_rows_map(k, K, st.s[1], p.B, p.Hkv, p.N, p.d) &&
+         !make_rows_map(v, V, st.s[2], p.B, p.Hkv, p.N, p.d);
 }
 
 }  // namespace
@@ -131,12 +135,11 @@ int attn_fwd_score(const void* Q, const void* K, const void* V, const int64_t* s
   if (st != ATTN_OK || empty) return st;
   if (!good(Q, 16) || !good(K, 16) || !good(V, 16) || !good(O, 16) || !good(L, 4))
     return ATTN_ERR_INVALID_ARG;
-  CUtensorMap mq, mk, mv;
-  if ((st = rows_map(&mq, Q, strides, 0, p)) || (st = rows_map(&mk, K, strides, 1, p)) ||
-      (st = rows_map(&mv, V, strides, 2, p)))
-    return st;
+  RowStrides rows;
+  if ((st = set_strides(strides, p, &rows)) != ATTN_OK) return st;
   int* err = error_word_ptr();
-  if (!err) return ATTN_ERR_CUDA;
+  CUtensorMap mq, mk, mv;
+  if (!err || !make_maps(&mq, &mk, &mv, Q, K, V, rows, p)) return ATTN_ERR_CUDA;
   return status_of(launch_score_fwd(mq, mk, mv, O, L, p, err, (cudaStream_t)stream));
 }
 
@@ -155,18 +158,17 @@ int attn_bwd_score(const void* Q, const void* K, const void* V, const int64_t* s
   for (const void* x : {Q, K, V, O, dO, (const void*)dQ, (const void*)dK, (const void*)dV})
     if (!good(x, 16)) return ATTN_ERR_INVALID_ARG;
   if (!good(L, 4)) return ATTN_ERR_INVALID_ARG;
+  RowStrides operands;
+  if ((st = set_strides(strides, p, &operands)) != ATTN_OK) return st;
   const Shape rows = shape_of(p, p.Hq), keys = shape_of(p, p.Hkv);
   if (!good(workspace, 256) || bytes < workspace_bytes(rows)) return ATTN_ERR_WORKSPACE;
   const Workspace ws = carve_workspace(workspace, rows);
+  int* err = error_word_ptr();
   ScoreBwdMaps m;
-  if ((st = rows_map(&m.q, Q, strides, 0, p)) || (st = rows_map(&m.k, K, strides, 1, p)) ||
-      (st = rows_map(&m.v, V, strides, 2, p)))
-    return st;
+  if (!err || !make_maps(&m.q, &m.k, &m.v, Q, K, V, operands, p)) return ATTN_ERR_CUDA;
   if (make_tile_map(&m.dout, dO, rows) || make_tile_map(&m.dk, dK, keys) ||
       make_tile_map(&m.dv, dV, keys) || make_acc_map(&m.acc, ws.acc, rows))
     return ATTN_ERR_CUDA;
-  int* err = error_word_ptr();
-  if (!err) return ATTN_ERR_CUDA;
   const cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e = launch_bwd_preprocess(O, dO, L, ws, rows, true, s);
   if (e == cudaSuccess && p.doc) e = launch_score_bwd_tables(ws, p, s);

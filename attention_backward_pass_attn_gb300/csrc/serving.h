@@ -47,12 +47,19 @@ struct RopeArgs {
 };
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream);
 
-// The paged cache as the kernels see it.  descale pointers are null for bf16.
+// What a row of the cache is held in: bf16; e4m3 with an fp32 factor a row; four
+// bits with a bf16 factor for every 32 values (int4.cuh).
+enum CacheType { kCacheBf16 = 0, kCacheE4m3 = 1, kCacheInt4 = 2 };
+
+// The paged cache as the kernels see it.
 struct CacheArgs {
   void* kc;
   void* vc;
-  float* kd;
+  float* kd;     // e4m3: [num_pages][Hkv][page_size]
   float* vd;
+  uint16_t* kf;  // int4: [num_pages][Hkv][page_size][d / 32]
+  uint16_t* vf;
+  int type;
   const int* table;  // [B][max_pages]
   int num_pages, Hkv, page_size, d, max_pages, B;
   int capacity;      // max_pages * page_size
@@ -71,6 +78,20 @@ struct CacheRows {
 };
 cudaError_t launch_kv_write(const CacheArgs& c, const CacheRows& r, int* err, cudaStream_t stream);
 cudaError_t launch_kv_read(const CacheArgs& c, const CacheRows& r, int* err, cudaStream_t stream);
+// kv_cache_int4.cu
+cudaError_t launch_kv_write_int4(const CacheArgs& c, const CacheRows& r, int* err,
+                                 cudaStream_t stream);
+cudaError_t launch_kv_read_int4(const CacheArgs& c, const CacheRows& r, int* err,
+                                cudaStream_t stream);
+
+// How scores are changed before the softmax, on scores in base 2.
+struct DecodeScore {
+  float cap_log2;      // cap log2(e); 0: none
+  float inv_cap_log2;  // its reciprocal
+  float exp_scale;     // 2 log2(e) / cap_log2: e^2y of a score
+  float reach;         // |score| up to which the polynomial holds
+  const float* slopes;  // [Hq] or null
+};
 
 // attn_decode.cu.
 struct DecodeArgs {
@@ -82,6 +103,7 @@ struct DecodeArgs {
   int Hq;
   int window;
   float scale_log2;      // scale * log2(e)
+  DecodeScore score;
   // set by launch_decode: the query heads of a key head, cut into blocks of at
   // most kDecodeHeads (the last may have fewer)
   int group, group_blocks, block_heads;
@@ -106,5 +128,8 @@ inline size_t decode_o_bytes(int d) {
   return sizeof(float) * d * kDecodeHeads * 2 * size_t(kDecodeMaxBlocks);
 }
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
+// launch_decode's, with the heads' division filled in
+cudaError_t launch_decode_int4(const DecodeArgs& a, cudaStream_t stream);
+cudaError_t launch_decode_score(const DecodeArgs& a, cudaStream_t stream);
 
 }  // namespace attn

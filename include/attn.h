@@ -452,6 +452,50 @@ int attn_decode(const void* Q, const void* K_cache, const void* V_cache, const f
                 void* stream);
 
 /*
+ * The paged cache in four bits.  As above, but K_cache and V_cache are bytes
+ * [num_pages][Hkv][page_size][d / 2], 16-byte aligned, and k_factor, v_factor
+ * bf16 [num_pages][Hkv][page_size][d / 32], 2-byte aligned: 32 neighbouring
+ * values of a row share a factor.  Byte i of a row holds element 2i in its low
+ * four bits and 2i + 1 in its high ones, each a whole number c in -7 .. 7 plus
+ * 8, and stands for c x factor.
+ *
+ * A row is rounded group by group: factor = amax / 7 rounded to five
+ * significant bits (ties to even), amax the largest finite |x| of the group;
+ * at least 2^-120, and 1 for a group of zeros; c = round(x / factor), ties to
+ * even.  Infinities become +-7, and a group with a NaN gets a NaN for its
+ * factor.  c has three bits and the factor five, so every value of the cache
+ * is a bf16 number: reading back does not round.  A value is off by at most
+ * half a factor, 1/13.5 of the group's largest.
+ *
+ * Everything else (positions, counts, bad pages, shared pages) is as in
+ * kv_cache_write and kv_cache_read.
+ */
+int int4_cache_write(const void* K, const void* V, const int64_t* strides, void* K_cache,
+                     void* V_cache, void* k_factor, void* v_factor, const int* page_table,
+                     const int* start, const int* count, int B, int Hkv, int T, int d,
+                     int page_size, int num_pages, int max_pages, void* stream);
+int int4_cache_read(const void* K_cache, const void* V_cache, const void* k_factor,
+                    const void* v_factor, const int* page_table, const int* start,
+                    const int* count, void* K, void* V, int B, int Hkv, int T, int d,
+                    int page_size, int num_pages, int max_pages, void* stream);
+
+/*
+ * attn_decode over a cache of any type, with the scores changed as
+ * attn_fwd_score does: capped by softcap > 0, then less slopes[h] x (n - 1 - j)
+ * (fp32 [Hq], NULL = none).  k_factor and v_factor: NULL (bf16), fp32 (e4m3)
+ * or bf16 (int4), as the cache has them.  An infinite score is capped like any
+ * other; a NaN stays one.  Otherwise as attn_decode, which is this call with
+ * softcap = 0 and slopes = NULL.
+ */
+typedef enum { ATTN_CACHE_BF16 = 0, ATTN_CACHE_E4M3 = 1, ATTN_CACHE_INT4 = 2 } attn_cache_type_t;
+int attn_score_decode(const void* Q, const void* K_cache, const void* V_cache,
+                      const void* k_factor, const void* v_factor, int cache_type,
+                      const int* page_table, const int* seq_lens, void* O, float* L, int B, int Hq,
+                      int Hkv, int d, int page_size, int num_pages, int max_pages, int window,
+                      float softcap, const float* slopes, float scale, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
  * Attention with changed scores, forward and backward: scores capped by a
  * tanh, a bias that falls with distance, a prefix that sees itself whole, and
  * key heads that several query heads share.  The pages list such variants of

@@ -130,3 +130,41 @@ def backward(q, k, v, o, do, lse, causal=True, scale=1.0, cap=0.0, slopes=None, 
     for n, e in (("dQ", "eQ"), ("dK", "eK"), ("dV", "eV")):
         out[e] += BF16 * np.abs(out[n]) + 2.0 ** -133  # the result's own rounding
     return out
+
+
+def decode(q, kvals, vvals, page_table, seq_lens, scale, window=0, cap=0.0, slopes=None):
+    """The newest token of each sequence over its pages: dict of O [B, H, d],
+    L [B, H] and bounds dO, dL.  kvals, vvals: float64 [pages, Hkv, page_size,
+    d].  Bounds: scores off by score_error, exponentials to 2^-21, weights of
+    16 bits for V, sums of n terms in fp32, O's rounding to bf16."""
+    q = _f64(q)
+    B, H, d = q.shape[0], q.shape[1], q.shape[-1]
+    q = q.reshape(B, H, d)
+    table = np.asarray(_f64(page_table)).astype(np.int64)
+    page = kvals.shape[2]
+    g = H // kvals.shape[1]
+    out = {"O": np.zeros((B, H, d)), "L": np.full((B, H), -np.inf), "dO": np.zeros((B, H, d)),
+           "dL": np.zeros((B, H))}
+    for b in range(B):
+        n = int(seq_lens[b])
+        at = np.arange(max(0, n - window) if window else 0, n)
+        if not len(at):
+            continue
+        rows = table[b, at // page], at % page
+        for h in range(H):
+            k, v = kvals[rows[0], h // g, rows[1]], vvals[rows[0], h // g, rows[1]]
+            sl = 0.0 if slopes is None else float(_f64(slopes)[h])
+            x, _ = change(scale * (k @ q[b, h]), cap, sl, n - 1 - at)
+            m = np.max(x)
+            e = np.exp(x - m)
+            p = e / np.sum(e)
+            mag = scale * (np.abs(k) @ np.abs(q[b, h]))
+            err = float(score_error(mag, np.ones(len(at), dtype=bool), d, cap,
+                                    None if slopes is None else [sl], n))
+            err += 2.0 ** -21 + len(at) * FP32
+            out["O"][b, h], out["L"][b, h] = p @ v, m + np.log(np.sum(e))
+            out["dL"][b, h] = err + 4 * FP32 * (abs(out["L"][b, h]) + abs(m))
+            out["dO"][b, h] = BF16 * np.abs(out["O"][b, h]) \
+                + (2 * err + 2.0 ** -15 + len(at) * 2.0 ** -22) * 1.01 * (p @ np.abs(v)) \
+                + 2.0 ** -133  # a zero's own
+    return out
