@@ -2,15 +2,15 @@
 // a row, and the TMA copies of strided rows.
 //
 // The cap.  x = cap tanh(s / cap) for the scaled product s, in base 2.  Near
-// zero, |s / cap| <= 0.8, tanh is an odd polynomial of six terms, fitted to the
-// smallest relative error (6e-8, fp32's own): two scores to an instruction of
-// the FMA pipe.  Beyond it, tanh(y) = 1 - 2 / (1 + e^2y): an exponential and a
-// reciprocal for each score, absolute error some 2^-23 of the cap.  A warp
-// takes the polynomial for a tile whose scores all allow it: models that cap
-// their scores at 30 or 50 have most of them well below, and the special
-// function unit is the busier pipe of a softmax (figures in score_fwd.cu).
-// With a cap far above every score the polynomial is also the exact one, where
-// 1 - 2 / (1 + e^2y) would lose the score in the cap's last bits.
+// zero, |s / cap| <= 0.65, tanh is an odd polynomial of five terms: two scores
+// to an instruction of the FMA pipe.  Beyond it, tanh(y) = 1 - 2 / (1 + e^2y):
+// an exponential and a reciprocal for each score, absolute error some 2^-23 of
+// the cap.  A warp takes the polynomial for a piece of a tile whose scores all
+// allow it: models that cap their scores at 30 or 50 have most of them well
+// below, and the special function unit is the busier pipe of a softmax
+// (figures in score_fwd.cu).  With a cap far above every score the polynomial
+// is also the exact one, where 1 - 2 / (1 + e^2y) would lose the score in the
+// cap's last bits.
 #pragma once
 
 #include "f32x2.cuh"
@@ -45,6 +45,19 @@ __device__ __forceinline__ uint64_t cap_poly(const ScoreMap& m, uint64_t u) {
 #pragma unroll
   for (int k = kTanhTerms - 2; k >= 0; --k) h = fma_f32x2(h, z, f32x2(m.poly[k]));
   return mul_f32x2(u, h);
+}
+
+// Whether the polynomial holds for all of the warp's raw products (n each).
+template <int n>
+__device__ __forceinline__ bool near_zero(const uint32_t (&u)[n], float limit) {
+  float a[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) a[e] = fabsf(__uint_as_float(u[e]));
+#pragma unroll
+  for (int e = 4; e < n; e += 2)
+    a[(e >> 1) & 3] = max3f(a[(e >> 1) & 3], fabsf(__uint_as_float(u[e])),
+                            fabsf(__uint_as_float(u[e + 1])));
+  return __all_sync(0xffffffffu, max3f(a[0], a[1], fmaxf(a[2], a[3])) <= limit);
 }
 
 // 1 / (1 + e^2y) of y = u scale / cap; the capped score is cap_log2 (1 - 2 r).

@@ -10,26 +10,35 @@
 //
 // The frame is the plain forward's (attn_fwd.cu): a task is two 128-row query
 // tiles of one head, whose 128-row key/value tiles run through a two-stage TMA
-// ring; warps 0-3 and 4-7 run the softmax of the two tiles, a thread to a row,
-// warp 8 issues copies and warp 9 the tensor core's instructions; S and P
-// share tensor-memory columns, and the grid is fwd_grid's.  What differs:
+// ring; S and P share tensor-memory columns, and the grid is fwd_grid's.  What
+// differs:
 //
 //  * Scores are changed where they lie, in registers, before the row maximum.
-//    Tiles that no row's mask cuts skip the mask; tiles wholly in their rows'
-//    past or future take the bias's distance without its absolute value.
+//  * A cap bounds the scores, |x| <= cap log2(e) in base 2.  Up to kBoundedLog2
+//    (a cap of 55) every 2^x and their sums are fp32 (and bf16) numbers
+//    without a maximum to subtract: no maximum and no rescaling, so a row's
+//    halves need not wait for one another, and sixteen warps, each with half
+//    the columns of 32 rows, take the place of eight.
+//  * The bias -slope |i - j| of a tile wholly in its rows' past or future is a
+//    number of the row plus or minus slope times the column: a table of 128
+//    numbers a head in shared memory, added in the multiply-add that scales the
+//    score.
 //  * A query head reads key head h / group, through 4-D tensor maps with the
 //    caller's strides: heads of a fused projection are taken as they lie.  The
 //    heads of a group run side by side, so the L2 serves all but one of them.
+#include <type_traits>
+
 #include "score.cuh"
 
 namespace attn {
 namespace score_fwd {
 
-constexpr int kThreads = 320;
-constexpr int kProducerWarp = 8;
-constexpr int kMmaWarp = 9;
+constexpr int kTileBarrier = 1;  // named barriers of the tiles' softmax threads, + tile
 constexpr int kStages = 2;
 constexpr uint32_t kTmemCols = 512;
+// Scores of at most this in base 2 need no maximum: weights from 2^-80 to 2^80,
+// sums of 2^31 of them, and their products with values up to 2^15, are finite.
+constexpr float kBoundedLog2 = 80.f;
 
 // Barrier indices.
 constexpr int kBarQFull = 0;
@@ -51,7 +60,9 @@ struct Layout {
   static constexpr int kK = kQ + 2 * kTileBytes;    // kStages key tiles
   static constexpr int kV = kK + kStages * kTileBytes;
   static constexpr int kBar = kV + kStages * kTileBytes;
-  static constexpr int kTmemSlot = kBar + kNumBars * 8;
+  static constexpr int kSum = kBar + (kNumBars * 8 + 15) / 16 * 16;  // [tile][half][128] fp32
+  static constexpr int kBias = kSum + 2 * 2 * 128 * 4;               // [tile][sign][128] fp32
+  static constexpr int kTmemSlot = kBias + 2 * 2 * 128 * 4;
   static constexpr int kAbort = kTmemSlot + 4;
   // Padded past half of the SM's shared memory: one CTA, which allocates all
   // 512 tensor-memory columns, per SM.
@@ -110,13 +121,26 @@ __device__ __forceinline__ int snake_task(int k, int b, int G, int n_tasks) {
 // within a block and 16 KB across blocks; an MN-major operand advances 2 KB
 // (16 rows) per k-step, its MN extent spanning blocks 16 KB apart (LBO).
 
-template <int HD, bool CAP, bool SLOPES>
-__global__ void __launch_bounds__(kThreads, 1)
+// CAP, SLOPES: how scores are changed; BOUNDED: by a cap of at most
+// kBoundedLog2, and no slopes.
+template <bool BOUNDED>
+struct Warps {
+  static constexpr int kSoftmax = BOUNDED ? 16 : 8;
+  static constexpr int kTileThreads = 16 * kSoftmax;  // softmax threads of a query tile
+  static constexpr int kProducer = kSoftmax;
+  static constexpr int kMma = kSoftmax + 1;
+  static constexpr int kThreads = 32 * (kSoftmax + 2);
+};
+
+template <int HD, bool CAP, bool SLOPES, bool BOUNDED>
+__global__ void __launch_bounds__(Warps<BOUNDED>::kThreads, 1)
     score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, __nv_bfloat16* __restrict__ O,
                      float* __restrict__ Lout, const __grid_constant__ ScoreProblem p, int* err) {
   using Ly = Layout<HD>;
+  constexpr int kProducerWarp = Warps<BOUNDED>::kProducer, kMmaWarp = Warps<BOUNDED>::kMma;
+  constexpr int kTileThreads = Warps<BOUNDED>::kTileThreads;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5;
@@ -139,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(bar(i), i == kBarPReady || i == kBarPReady + 1 ? 128 : 1);
+      mbar_init(bar(i), i == kBarPReady || i == kBarPReady + 1 ? kTileThreads : 1);
     fence_barrier_init();
   }
   if (warp == kMmaWarp) {
@@ -229,8 +253,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t d = tbase + Ly::kColO + HD * t;
       const uint32_t pc = tbase + Ly::kColS + 128 * t;
 #pragma unroll
-      for (int k = 0; k < 8; ++k)  // 128 keys, 16 per step; P packed 2 per column
-        mma_ts(d, pc + 8 * k, sdesc_add(dv, k * 2048), kIdO, k > 0 ? 1u : acc);
+      for (int k = 0; k < 8; ++k)  // 128 keys, 16 per step; P packed 2 per column of its half
+        mma_ts(d, pc + 64 * (k >> 2) + 8 * (k & 3), sdesc_add(dv, k * 2048), kIdO,
+               k > 0 ? 1u : acc);
     };
     // Handshake counts across tasks: g key/value tiles, ca (cb) S/P rounds of
     // tile A (B).  A task's first P V overwrites O_t; the softmax warps of
@@ -304,10 +329,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_wait_warp(bar(kBarDrain), 0, own, 0x62F);
   } else {
     // ------------------------------------------------------------ softmax
-    const int t = (warp >> 2) & 1;  // 0 = tile A, 1 = tile B
+    // 0 = tile A, 1 = tile B; without BOUNDED a thread has its whole row, with
+    // it columns 64 half .. 64 half + 63.
+    const int t = (warp / (Warps<BOUNDED>::kSoftmax / 2)) & 1;
+    const int half = BOUNDED ? (warp >> 2) & 1 : 0;
     const int r = threadIdx.x & 127;
     const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
-    const uint32_t tS = tbase + lane_off + Ly::kColS + 128 * t;
+    const uint32_t tS = tbase + lane_off + Ly::kColS + 128 * t + 64 * half;
     const uint32_t tO = tbase + lane_off + Ly::kColO + HD * t;
     const ScoreMap& mp = p.map;
     bool ok = true;
@@ -321,143 +349,222 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int q = q_tile0 + r;
       const RowMask mask = tm.mask(tk.b);
       // The row sees keys lo_q <= j < hi_q; every row of the warp sees those
-      // of [any_lo, all_hi).
+      // of [all_lo, all_hi).
       const int lo_q = mask.lo(q), hi_q = mask.hi(q);
       const int all_lo = __reduce_max_sync(0xffffffffu, lo_q);
       const int all_hi = __reduce_min_sync(0xffffffffu, hi_q);
-      const float slope = SLOPES ? __ldg(mp.slopes + tk.h) * 1.4426950408889634f : 0.f;
-      float m = -INFINITY;  // running max of the base-2 scores
-      float l = 0.f;        // running sum of 2^(x - m)
-      for (int j = 0; j < tk.n_kv; ++j) {
-        if (!(ok = mbar_wait_warp(bar(kBarSFull + t), (c + j) & 1, ctx, 0x630 + t))) break;
-        tc_fence_after();
-        uint32_t u[128];
-        tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&u[0]));
-        tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&u[32]));
-        tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&u[64]));
-        tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&u[96]));
-        tmem_wait_ld();
-        const int kv0 = (tk.kv_lo + j) * 128;
-        auto f = [&](int e) { return __uint_as_float(u[e]); };
-        auto pair = [&](int e) { return f32x2(f(e), f(e + 1)); };
-        auto put = [&](int e, uint64_t x) {
-          float a, b;
-          f32x2_split(x, a, b);
-          u[e] = __float_as_uint(a);
-          u[e + 1] = __float_as_uint(b);
-        };
-        // u -> x, in place
-        if constexpr (CAP) {
-          float a8[8];
+      float m = BOUNDED ? 0.f : -INFINITY;  // running max of the base-2 scores
+      float l = 0.f;                        // running sum of 2^(x - m)
+      if constexpr (BOUNDED) {
+        for (int j = 0; j < tk.n_kv; ++j) {
+          if (!(ok = mbar_wait_warp(bar(kBarSFull + t), (c + j) & 1, ctx, 0x630 + t))) break;
+          tc_fence_after();
+          const int kv0 = (tk.kv_lo + j) * 128 + 64 * half;  // this half's first key
+          const int e_lo = lo_q - kv0, e_hi = hi_q - kv0;    // the row's columns
+          uint64_t sum[2] = {0, 0};
 #pragma unroll
-          for (int e = 0; e < 8; ++e) a8[e] = fabsf(f(e));
+          for (int ch = 0; ch < 2; ++ch) {
+            uint32_t u[32], pk[16];
+            tmem_ld32(tS + 32 * ch, u);
+            tmem_wait_ld();
+            auto pair = [&](int e) {
+              return f32x2(__uint_as_float(u[e]), __uint_as_float(u[e + 1]));
+            };
+            auto weigh = [&](int e, uint64_t x, auto edge) {
+              float p0, p1;
+              f32x2_split(x, p0, p1);
+              p0 = ex2(p0);
+              p1 = ex2(p1);
+              if constexpr (decltype(edge)::value) {
+                const int col = 32 * ch + e;
+                if (col < e_lo || col >= e_hi) p0 = 0.f;
+                if (col + 1 < e_lo || col + 1 >= e_hi) p1 = 0.f;
+              }
+              sum[(e >> 1) & 1] = add_f32x2(sum[(e >> 1) & 1], f32x2(p0, p1));
+              pk[e / 2] = pack_bf16x2(p0, p1);
+            };
+            auto all = [&](auto edge) {
+              if (near_zero<32>(u, mp.poly_limit)) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) weigh(e, cap_poly(mp, pair(e)), edge);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 32; e += 2)
+                  weigh(e, fma_f32x2(f32x2(cap_r(mp, __uint_as_float(u[e])),
+                                           cap_r(mp, __uint_as_float(u[e + 1]))),
+                                     f32x2(-2.f * mp.cap_log2), f32x2(mp.cap_log2)),
+                        edge);
+              }
+            };
+            if (kv0 + 32 * ch < all_lo || kv0 + 32 * ch + 32 > all_hi)
+              all(std::true_type());
+            else
+              all(std::false_type());
+            tmem_st16(tS + 16 * ch, pk);  // onto columns that have been read
+          }
+          float s0, s1;
+          f32x2_split(add_f32x2(sum[0], sum[1]), s0, s1);
+          l += s0 + s1;
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(kBarPReady + t));
+        }
+        // The halves' sums; a wait that gave up in one warp stops the tile's
+        // eight.  (What was read here a task ago was read before that thread
+        // signalled this task's first P.)
+        float* sums = reinterpret_cast<float*>(smem + Ly::kSum) + 256 * t + r;
+        sums[128 * half] = l;
+        ok = ok && mbar_wait_warp(bar(kBarOFull + t), no & 1, ctx, 0x638 + t);
+        if (!(ok = named_barrier_and(kTileBarrier + t, kTileThreads, ok))) break;
+        l += sums[128 * (1 - half)];
+      } else {
+        constexpr bool kChanged = CAP || SLOPES;  // u becomes the score itself
+        float slope = 0.f;
+        float* bias = reinterpret_cast<float*>(smem + Ly::kBias) + 256 * t;
+        if constexpr (SLOPES) {
+          slope = __ldg(mp.slopes + tk.h) * 1.4426950408889634f;
+          bias[r] = slope * float(r);
+          bias[128 + r] = -slope * float(r);
+          named_barrier_sync(kTileBarrier + t, kTileThreads);
+        }
+        for (int j = 0; j < tk.n_kv; ++j) {
+          if (!(ok = mbar_wait_warp(bar(kBarSFull + t), (c + j) & 1, ctx, 0x630 + t))) break;
+          tc_fence_after();
+          uint32_t u[128];
+          tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&u[0]));
+          tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&u[32]));
+          tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&u[64]));
+          tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&u[96]));
+          tmem_wait_ld();
+          const int kv0 = (tk.kv_lo + j) * 128;
+          const bool edge = kv0 < all_lo || kv0 + 128 > all_hi;
+          auto f = [&](int e) { return __uint_as_float(u[e]); };
+          auto pair = [&](int e) { return f32x2(f(e), f(e + 1)); };
+          auto put = [&](int e, uint64_t x) {
+            float a, b;
+            f32x2_split(x, a, b);
+            u[e] = __float_as_uint(a);
+            u[e + 1] = __float_as_uint(b);
+          };
+          const uint64_t sc = f32x2(mp.scale_log2);
+          if constexpr (CAP) {
+            if (near_zero<128>(u, mp.poly_limit)) {
+#pragma unroll
+              for (int e = 0; e < 128; e += 2) put(e, cap_poly(mp, pair(e)));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 128; ++e)
+                u[e] = __float_as_uint(fmaf(cap_r(mp, f(e)), -2.f * mp.cap_log2, mp.cap_log2));
+            }
+          }
+          float row = 0.f;  // the row's share of the bias: x = u + row
+          if constexpr (SLOPES) {
+            const float d0 = float(q - kv0);
+            const int w0 = q_tile0 + 32 * (warp & 3);  // the warp's first row
+            const bool past = kv0 + 127 <= w0;
+            if (past || kv0 >= w0 + 31) {  // one sign for every distance of the warp
+              row = past ? -slope * d0 : slope * d0;
+              const float4* b4 = reinterpret_cast<const float4*>(bias + (past ? 0 : 128));
+#pragma unroll
+              for (int e = 0; e < 128; e += 4) {
+                const float4 b = b4[e / 4];
+                if constexpr (CAP) {
+                  put(e, add_f32x2(pair(e), f32x2(b.x, b.y)));
+                  put(e + 2, add_f32x2(pair(e + 2), f32x2(b.z, b.w)));
+                } else {
+                  put(e, fma_f32x2(pair(e), sc, f32x2(b.x, b.y)));
+                  put(e + 2, fma_f32x2(pair(e + 2), sc, f32x2(b.z, b.w)));
+                }
+              }
+            } else {  // distances are whole numbers, exact below 2^24
+#pragma unroll
+              for (int e = 0; e < 128; ++e)
+                u[e] = __float_as_uint(
+                    fmaf(-slope, fabsf(d0 - float(e)), CAP ? f(e) : f(e) * mp.scale_log2));
+            }
+          }
+          if (edge) {
+            const int e_lo = lo_q - kv0, e_hi = hi_q - kv0;
+#pragma unroll
+            for (int e = 0; e < 128; ++e)
+              if (e >= e_hi || e < e_lo) u[e] = __float_as_uint(-INFINITY);
+          }
+          // row maximum: eight chains of three-input maxima (two scores each)
+          float m8[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m8[e] = f(e);
 #pragma unroll
           for (int e = 8; e < 128; e += 2)
-            a8[(e >> 1) & 7] = max3f(a8[(e >> 1) & 7], fabsf(f(e)), fabsf(f(e + 1)));
-          const float top = max3f(max3f(a8[0], a8[1], a8[2]), max3f(a8[3], a8[4], a8[5]),
-                                  fmaxf(a8[6], a8[7]));
-          if (__all_sync(0xffffffffu, top <= mp.poly_limit)) {
-#pragma unroll
-            for (int e = 0; e < 128; e += 2) put(e, cap_poly(mp, pair(e)));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 128; ++e)
-              u[e] = __float_as_uint(fmaf(cap_r(mp, f(e)), -2.f * mp.cap_log2, mp.cap_log2));
+            m8[(e >> 1) & 7] = max3f(m8[(e >> 1) & 7], f(e), f(e + 1));
+          const float mx = max3f(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], m8[5]),
+                                 fmaxf(m8[6], m8[7]));
+          // scale > 0, so the maximum commutes with it
+          const float m_new = fmaxf(m, kChanged ? mx + row : mx * mp.scale_log2);
+          // Lazy rescale: move the reference maximum (and rescale l and O by
+          // 2^(m - m_new)) only when the maximum grew by more than 8 in base 2.
+          const bool rescale = m_new > m + 8.f;
+          const float alpha = rescale ? ex2(m - m_new) : 1.f;
+          if (rescale) {
+            l *= alpha;
+            m = m_new;
           }
-        } else {
-          const uint64_t sc = f32x2(mp.scale_log2);
+          const uint64_t mb = f32x2(m == -INFINITY ? 0.f : row - m);
+          uint64_t sum[2] = {0, 0};
 #pragma unroll
-          for (int e = 0; e < 128; e += 2) put(e, mul_f32x2(pair(e), sc));
-        }
-        // Distances are whole numbers, exact below 2^24.
-        if constexpr (SLOPES) {
-          const float d0 = float(q - kv0);
-          const int w0 = q_tile0 + 32 * (warp & 3);  // the warp's first row
-          if (kv0 + 127 <= w0 || kv0 >= w0 + 31) {
-            const uint64_t sl = f32x2(kv0 + 127 <= w0 ? -slope : slope), two = f32x2(-2.f);
-            uint64_t dist = f32x2(d0, d0 - 1.f);
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[32];
 #pragma unroll
-            for (int e = 0; e < 128; e += 2) {
-              put(e, fma_f32x2(sl, dist, pair(e)));
-              dist = add_f32x2(dist, two);
+            for (int e = 0; e < 64; e += 2) {
+              float p0, p1;
+              f32x2_split(kChanged ? add_f32x2(pair(64 * h + e), mb)
+                                   : fma_f32x2(pair(64 * h + e), sc, mb), p0, p1);
+              p0 = ex2(p0);
+              p1 = ex2(p1);
+              sum[(e >> 1) & 1] = add_f32x2(sum[(e >> 1) & 1], f32x2(p0, p1));
+              pk[e / 2] = pack_bf16x2(p0, p1);
             }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 128; ++e)
-              u[e] = __float_as_uint(fmaf(-slope, fabsf(d0 - float(e)), f(e)));
+            tmem_st32(tS + 64 * h, pk);
           }
-        }
-        if (kv0 < all_lo || kv0 + 128 > all_hi) {
-          const int e_lo = lo_q - kv0, e_hi = hi_q - kv0;
+          float s0, s1;
+          f32x2_split(add_f32x2(sum[0], sum[1]), s0, s1);
+          l += s0 + s1;
+          // tcgen05.ld/st are warp-collective: if any row of the warp moved its
+          // maximum, the whole warp rescales (alpha = 1 leaves the other rows
+          // unchanged).  O holds P V of earlier tiles; PV(j-1) has completed.
+          if (j > 0 && __any_sync(0xffffffffu, rescale)) {
 #pragma unroll
-          for (int e = 0; e < 128; ++e)
-            if (e >= e_hi || e < e_lo) u[e] = __float_as_uint(-INFINITY);
-        }
-        // row maximum: eight chains of three-input maxima (two scores each)
-        float m8[8];
+            for (int c4 = 0; c4 < HD / 32; ++c4) {
+              uint32_t o[32];
+              tmem_ld32(tO + 32 * c4, o);
+              tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m8[e] = f(e);
-#pragma unroll
-        for (int e = 8; e < 128; e += 2)
-          m8[(e >> 1) & 7] = max3f(m8[(e >> 1) & 7], f(e), f(e + 1));
-        const float mx = max3f(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], m8[5]),
-                               fmaxf(m8[6], m8[7]));
-        const float m_new = fmaxf(m, mx);
-        // Lazy rescale: move the reference maximum (and rescale l and O by
-        // 2^(m - m_new)) only when the maximum grew by more than 8 in base 2.
-        const bool rescale = m_new > m + 8.f;
-        const float alpha = rescale ? ex2(m - m_new) : 1.f;
-        if (rescale) {
-          l *= alpha;
-          m = m_new;
-        }
-        const uint64_t mb = f32x2((m == -INFINITY) ? 0.f : -m);
-        float rs[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int c2 = 0; c2 < 32; ++c2) {
-            float x0, x1;
-            f32x2_split(add_f32x2(pair(64 * h + 2 * c2), mb), x0, x1);
-            const float p0 = ex2(x0);
-            const float p1 = ex2(x1);
-            rs[c2 & 3] += p0 + p1;
-            pk[c2] = pack_bf16x2(p0, p1);
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st32(tO + 32 * c4, o);
+            }
           }
-          tmem_st32(tS + 32 * h, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(kBarPReady + t));
         }
-        l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
-        // tcgen05.ld/st are warp-collective: if any row of the warp moved its
-        // maximum, the whole warp rescales (alpha = 1 leaves the other rows
-        // unchanged).  O holds P V of earlier tiles; PV(j-1) has completed.
-        if (j > 0 && __any_sync(0xffffffffu, rescale)) {
-#pragma unroll
-          for (int c4 = 0; c4 < HD / 32; ++c4) {
-            uint32_t o[32];
-            tmem_ld32(tO + 32 * c4, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st32(tO + 32 * c4, o);
-          }
+        if constexpr (SLOPES) {
+          // All of the tile's warps stop or none, and the table has been read.
+          ok = ok && mbar_wait_warp(bar(kBarOFull + t), no & 1, ctx, 0x638 + t);
+          if (!(ok = named_barrier_and(kTileBarrier + t, kTileThreads, ok))) break;
+        } else {
+          if (!ok || !(ok = mbar_wait_warp(bar(kBarOFull + t), no & 1, ctx, 0x638 + t))) break;
         }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(bar(kBarPReady + t));
       }
-      if (!ok) break;
       c += tk.n_kv;
-      if (!(ok = mbar_wait_warp(bar(kBarOFull + t), no & 1, ctx, 0x638 + t))) break;
       ++no;
       tc_fence_after();
       const float inv_l = 1.f / l;
       const size_t row = (size_t(tk.b) * p.Hq + tk.h) * N + q;
-      __nv_bfloat16* orow = O + row * HD;
+      constexpr int kCols = BOUNDED ? HD / 2 : HD;  // of this thread
+      __nv_bfloat16* orow = O + row * HD + kCols * half;
 #pragma unroll
-      for (int c4 = 0; c4 < HD / 32; ++c4) {
+      for (int c4 = 0; c4 < kCols / 32; ++c4) {
         uint32_t o[32];
-        tmem_ld32(tO + 32 * c4, o);
+        tmem_ld32(tO + kCols * half + 32 * c4, o);
         tmem_wait_ld();
         if (q < N) {
 #pragma unroll
@@ -471,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (q < N) Lout[row] = (m + log2f(l)) * 0.69314718055994530942f;
+      if (q < N && half == 0) Lout[row] = (m + log2f(l)) * 0.69314718055994530942f;
       // O_t has been read into registers (tmem_wait_ld above) before this
       // warp signals the next task's first P.
       tc_fence_before();
@@ -493,28 +600,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int HD, bool CAP, bool SLOPES>
+template <int HD, bool CAP, bool SLOPES, bool BOUNDED>
 static cudaError_t launch_t(const CUtensorMap& tmQ, const CUtensorMap& tmK,
                             const CUtensorMap& tmV, void* O, float* L, const ScoreProblem& p,
                             int* err, cudaStream_t stream) {
   using Ly = Layout<HD>;
-  cudaError_t e = set_smem_limit_once<score_fwd_kernel<HD, CAP, SLOPES>>(Ly::kBytes);
+  constexpr auto kern = score_fwd_kernel<HD, CAP, SLOPES, BOUNDED>;
+  constexpr int kThreads = Warps<BOUNDED>::kThreads;
+  cudaError_t e = set_smem_limit_once<kern>(Ly::kBytes);
   if (e != cudaSuccess) return e;
   const long long n_tasks = (long long)((p.n_tiles + 1) / 2) * p.B * p.Hq;
   const dim3 grid(unsigned(fwd_grid(n_tasks, p.causal)));
-  return launch_kernel(score_fwd_kernel<HD, CAP, SLOPES>, grid, dim3(kThreads), Ly::kBytes, stream,
-                       tmQ, tmK, tmV, static_cast<__nv_bfloat16*>(O), L, p, err);
+  return launch_kernel(kern, grid, dim3(kThreads), Ly::kBytes, stream, tmQ, tmK, tmV,
+                       static_cast<__nv_bfloat16*>(O), L, p, err);
 }
 
 template <int HD>
 static cudaError_t launch_d(const CUtensorMap& tmQ, const CUtensorMap& tmK,
                             const CUtensorMap& tmV, void* O, float* L, const ScoreProblem& p,
                             int* err, cudaStream_t stream) {
+  const bool slopes = p.map.slopes;
+  if (p.cap && !slopes && p.map.cap_log2 <= kBoundedLog2)
+    return launch_t<HD, true, false, true>(tmQ, tmK, tmV, O, L, p, err, stream);
   if (p.cap)
-    return p.map.slopes ? launch_t<HD, true, true>(tmQ, tmK, tmV, O, L, p, err, stream)
-                        : launch_t<HD, true, false>(tmQ, tmK, tmV, O, L, p, err, stream);
-  return p.map.slopes ? launch_t<HD, false, true>(tmQ, tmK, tmV, O, L, p, err, stream)
-                      : launch_t<HD, false, false>(tmQ, tmK, tmV, O, L, p, err, stream);
+    return slopes ? launch_t<HD, true, true, false>(tmQ, tmK, tmV, O, L, p, err, stream)
+                  : launch_t<HD, true, false, false>(tmQ, tmK, tmV, O, L, p, err, stream);
+  return slopes ? launch_t<HD, false, true, false>(tmQ, tmK, tmV, O, L, p, err, stream)
+                : launch_t<HD, false, false, false>(tmQ, tmK, tmV, O, L, p, err, stream);
 }
 
 }  // namespace score_fwd

@@ -1,18 +1,18 @@
 // score_tanh.h -- the polynomial that takes the place of a tanh near zero:
 //
-//   tanh(y) = y (c0 + c1 y^2 + ... + c5 y^10),  |y| <= 0.8
+//   tanh(y) = y (c0 + c1 y^2 + ... + c4 y^8),  |y| <= 0.65
 //
-// with the smallest relative error that six terms reach (5.8e-8, found by
-// Remez exchange), as small as fp32's own steps.
+// with the smallest relative error that five terms reach (1.5e-7, found by
+// Remez exchange), some steps of fp32.
 #pragma once
 
 namespace attn {
 
-constexpr int kTanhTerms = 6;
-constexpr double kTanhReach = 0.8;
+constexpr int kTanhTerms = 5;
+constexpr double kTanhReach = 0.65;
 constexpr float tanh_poly(int k) {
-  constexpr float c[kTanhTerms] = {0.999999942083f,   -0.333326749194f, 0.133210482804f,
-                                   -0.0531143154981f, 0.0190933004507f, -0.0043552995703f};
+  constexpr float c[kTanhTerms] = {0.999999846455f, -0.333315001912f, 0.132978737432f,
+                                   -0.0515179163995f, 0.0146250854857f};
   return c[k];
 }
 
