@@ -12,8 +12,8 @@
 // that sees it, dK and dV in tensor memory until the tile is done, dQ's
 // partial tiles added into an fp32 accumulator by TMA reduce-adds (their order
 // varies: dQ repeats to fp32 rounding, dK and dV bit for bit).  Warps 0-3
-// drain dQ, 4-11 own 64 query columns each of S^T and dP^T, a thread to a key
-// row, 12 issues copies and 13 the tensor core's instructions.  The steps
+// drain dQ, 4-19 own 32 query columns each of S^T and dP^T, a thread to a key
+// row, 20 issues copies and 21 the tensor core's instructions.  The steps
 // before and after (D, L log2 e and zeroed accumulators; dQ to bf16) are the
 // plain backward's.  What differs:
 //
@@ -34,9 +34,10 @@
 namespace attn {
 namespace score_bwd {
 
-constexpr int kThreads = 448;
-constexpr int kProducerWarp = 12;
-constexpr int kMmaWarp = 13;
+constexpr int kThreads = 704;
+constexpr int kSoftmaxThreads = 512;
+constexpr int kProducerWarp = 20;
+constexpr int kMmaWarp = 21;
 constexpr uint32_t kTmemCols = 512;
 
 // Item-level barriers (one phase per work item of the CTA).
@@ -204,13 +205,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < kNumBars; ++i) {
-      // arrivals per phase: the 256 softmax threads, the 128 drain threads,
-      // or one (a TMA transaction or a tcgen05.commit)
+      // arrivals per phase: the softmax threads, the 128 drain threads, or one
+      // (a TMA transaction or a tcgen05.commit)
       const uint32_t count =
-          (i == kBarPReady || i == kBarDSReady || i == kBarAccEmpty) ? 256
+          (i == kBarPReady || i == kBarDSReady || i == kBarAccEmpty) ? kSoftmaxThreads
           : (i == kBarDQFree)                                          ? 128
-          : (i == kBarEpiFull || i == kBarEpiFull + 1)                 ? 256 / Ly::kEpiTurns
-                                                                       : 1;
+          : (i == kBarEpiFull || i == kBarEpiFull + 1) ? kSoftmaxThreads / Ly::kEpiTurns
+                                                       : 1;
       mbar_init(bar(i), count);
     }
     fence_barrier_init();
@@ -395,9 +396,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (last) tc_commit(bar(kBarVEmpty));
         }
         __syncwarp();
-        // dV += P^T dO, P^T read from tensor memory: query block kk/4 was
-        // packed by the softmax warps of that half into its own first 32
-        // columns.  The first dV of an item overwrites the accumulator: the
+        // dV += P^T dO, P^T read from tensor memory: the softmax warps of 32
+        // query columns packed them into the first 16 of their own.  The first dV of an item overwrites the accumulator: the
         // previous item's epilogue must have read it.
         if (!(ok = mbar_wait_warp(bar(kBarPReady), g & 1, ctx, 0x724))) break;
         if (it == 0 && k > 0 &&
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_ts(tDV, tS + 64 * (kk >> 2) + 8 * (kk & 3), sdesc_add(dO_mn, kk * 2048), kIdV,
+            mma_ts(tDV, tS + 32 * (kk >> 1) + 8 * (kk & 1), sdesc_add(dO_mn, kk * 2048), kIdV,
                    kk > 0 ? 1u : acc0);
           tc_commit(bar(kBarDOEmpty + ds_));
         }
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)  // dS^T packed like P^T, in the dP^T columns
-              mma_ts(tDK, tDP + 64 * (kk >> 2) + 8 * (kk & 3), sdesc_add(dQ_mn, kk * 2048), kIdV,
+              mma_ts(tDK, tDP + 32 * (kk >> 1) + 8 * (kk & 1), sdesc_add(dQ_mn, kk * 2048), kIdV,
                      kk > 0 ? 1u : acc0);
             tc_commit(bar(kBarQEmpty + s));
           }
@@ -480,12 +480,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_wait_warp(bar(kBarDrain), 0, own, 0x72F);
   } else if (warp >= 4) {
     // ------------------------------------------------------------ softmax / dS
-    const int half = (warp - 4) >> 2;  // query columns 64 half .. 64 half + 63
-    const int r = threadIdx.x & 127;   // key row within the tile = TMEM lane
+    const int quarter = (warp - 4) >> 2;  // query columns 32 quarter .. 32 quarter + 31
+    const int r = threadIdx.x & 127;      // key row within the tile = TMEM lane
     const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
-    const uint32_t tS = tbase + lane_off + Ly::kColS + 64 * half;
-    const uint32_t tDP = tbase + lane_off + Ly::kColDP + 64 * half;
-    const uint32_t sDSrow = sbase + Ly::kDS + half * 16384 + r * 128;
+    const uint32_t tS = tbase + lane_off + Ly::kColS + 32 * quarter;
+    const uint32_t tDP = tbase + lane_off + Ly::kColDP + 32 * quarter;
+    const uint32_t sDSrow = sbase + Ly::kDS + (quarter >> 1) * 16384 + r * 128;
     const ScoreMap& mp = p.map;
     bool ok = true;
     int g = 0;
@@ -506,74 +506,67 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int all_lo = __reduce_max_sync(0xffffffffu, q_lo);
       const int all_lim = __reduce_min_sync(0xffffffffu, q_lim);
       for (int h = 0, it = 0; h < p.group; ++g) {
-        const int s = g & 1, q0 = (t.it0 + it) * 128 + 64 * half;  // this half's first query
-        const float slope =
-            SLOPES ? __ldg(mp.slopes + t.hk * p.group + h) * 1.4426950408889634f : 0.f;
+        const int s = g & 1, q0 = (t.it0 + it) * 128 + 32 * quarter;  // the first column's query
         const bool first = it == 0 && h == 0;
         if (!(ok = mbar_wait_warp(bar(kBarQFull + s), (g >> 1) & 1, ctx, 0x730))) break;
         if (!(ok = mbar_wait_warp(bar(kBarSFull), g & 1, ctx, 0x731))) break;
         tc_fence_after();
         const float4* L2v4 =
-            reinterpret_cast<const float4*>(smem + Ly::kVec + s * 1024) + 16 * half;
+            reinterpret_cast<const float4*>(smem + Ly::kVec + s * 1024) + 8 * quarter;
         const float4* Dv4 =
-            reinterpret_cast<const float4*>(smem + Ly::kVec + s * 1024 + 512) + 16 * half;
+            reinterpret_cast<const float4*>(smem + Ly::kVec + s * 1024 + 512) + 8 * quarter;
         // P x' stays in registers (fp16) for the dS phase: the tensor core
         // overwrites these S columns with the next S once dV has read P.
-        uint32_t px[32];
+        uint32_t px[16];
         {
-          uint32_t u[64];
-          tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&u[0]));
-          tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&u[32]));
+          uint32_t u[32], pk[16];
+          tmem_ld32(tS, u);
           tmem_wait_ld();
-          auto f = [&](int e) { return __uint_as_float(u[e]); };
-          bool poly = false;
-          if constexpr (CAP) {
-            float a4[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) a4[e] = fabsf(f(e));
-#pragma unroll
-            for (int e = 4; e < 64; e += 2)
-              a4[(e >> 1) & 3] = max3f(a4[(e >> 1) & 3], fabsf(f(e)), fabsf(f(e + 1)));
-            poly = __all_sync(0xffffffffu,
-                              max3f(a4[0], a4[1], fmaxf(a4[2], a4[3])) <= mp.poly_limit);
+          auto pair = [&](int e) { return f32x2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])); };
+          float slope = 0.f, d0 = 0.f;
+          bool past = true, linear = true;
+          if constexpr (SLOPES) {
+            slope = __ldg(mp.slopes + t.hk * p.group + h) * 1.4426950408889634f;
+            d0 = float(q0 - key);
+            const int w0 = t.jt * 128 + 32 * (warp & 3);  // the warp's first key
+            past = q0 >= w0 + 31;
+            linear = past || q0 + 31 <= w0;  // one sign for every distance of the warp
+            if (past) slope = -slope;
           }
-          const bool edge = q0 < all_lo || q0 + 64 > all_lim;
-          const int w0 = t.jt * 128 + 32 * (warp & 3);  // the warp's first key
-          const float d0 = float(q0 - key);
-          const bool past = q0 >= w0 + 31, linear = past || q0 + 63 <= w0;
-          uint32_t pk[32];
           // Two columns: x - L, P and P x'.
-          auto columns = [&](int e, float l0, float l1, auto by_poly) {
-            [[maybe_unused]] constexpr bool kPoly = decltype(by_poly)::value;
+          auto columns = [&](int e, float l0, float l1, auto by_poly, auto edge) {
             [[maybe_unused]] uint64_t der;
             uint64_t y;
             if constexpr (!CAP) {
-              y = fma_f32x2(f32x2(f(e), f(e + 1)), f32x2(mp.scale_log2), f32x2(-l0, -l1));
-            } else if constexpr (kPoly) {
-              const uint64_t x = cap_poly(mp, f32x2(f(e), f(e + 1)));
+              y = fma_f32x2(pair(e), f32x2(mp.scale_log2), f32x2(-l0, -l1));
+            } else if constexpr (decltype(by_poly)::value) {
+              const uint64_t x = cap_poly(mp, pair(e));
               der = fma_f32x2(mul_f32x2(x, x), f32x2(-mp.inv_cap_log2_sq), f32x2(1.f));
               y = add_f32x2(x, f32x2(-l0, -l1));
             } else {
-              const uint64_t rr = f32x2(cap_r(mp, f(e)), cap_r(mp, f(e + 1)));
+              const uint64_t rr = f32x2(cap_r(mp, __uint_as_float(u[e])),
+                                        cap_r(mp, __uint_as_float(u[e + 1])));
               // 1 - tanh^2 = 4 r (1 - r)
               der = mul_f32x2(mul_f32x2(rr, f32x2(4.f)),
                               fma_f32x2(rr, f32x2(-1.f), f32x2(1.f)));
               y = add_f32x2(fma_f32x2(rr, f32x2(-2.f * mp.cap_log2), f32x2(mp.cap_log2)),
                             f32x2(-l0, -l1));
             }
-            if constexpr (SLOPES) {
+            if constexpr (SLOPES) {  // distances are whole numbers, exact below 2^24
+              const uint64_t dist = add_f32x2(f32x2(d0), f32x2(float(e), float(e + 1)));
               if (linear) {
-                const uint64_t dist = f32x2(d0 + float(e), d0 + float(e + 1));
-                y = fma_f32x2(f32x2(past ? -slope : slope), dist, y);
+                y = fma_f32x2(f32x2(slope), dist, y);
               } else {
-                y = fma_f32x2(f32x2(-slope),
-                              f32x2(fabsf(d0 + float(e)), fabsf(d0 + float(e + 1))), y);
+                float a, b;
+                f32x2_split(dist, a, b);
+                y = fma_f32x2(f32x2(-slope), f32x2(fabsf(a), fabsf(b)), y);
               }
             }
-            float y0, y1;
-            f32x2_split(y, y0, y1);
-            float p0 = ex2(y0), p1 = ex2(y1);
-            if (edge) {
+            float p0, p1;
+            f32x2_split(y, p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            if constexpr (decltype(edge)::value) {
               const int q = q0 + e;
               if (q < q_lo || q >= q_lim) p0 = 0.f;
               if (q + 1 < q_lo || q + 1 >= q_lim) p1 = 0.f;
@@ -582,19 +575,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (CAP) f32x2_split(mul_f32x2(f32x2(p0, p1), der), p0, p1);
             px[e / 2] = pack_f16x2(p0, p1);
           };
-          auto all = [&](auto by_poly) {
+          auto all = [&](auto by_poly, auto edge) {
 #pragma unroll
-            for (int c4 = 0; c4 < 16; ++c4) {
+            for (int c4 = 0; c4 < 8; ++c4) {
               const float4 l = L2v4[c4];  // one broadcast load for four query columns
-              columns(4 * c4, l.x, l.y, by_poly);
-              columns(4 * c4 + 2, l.z, l.w, by_poly);
+              columns(4 * c4, l.x, l.y, by_poly, edge);
+              columns(4 * c4 + 2, l.z, l.w, by_poly, edge);
             }
           };
-          if (poly)
-            all(std::true_type());
+          auto paths = [&](auto edge) {
+            bool poly = true;
+            if constexpr (CAP) poly = near_zero<32>(u, mp.poly_limit);
+            if (poly)
+              all(std::true_type(), edge);
+            else
+              all(std::false_type(), edge);
+          };
+          if (q0 < all_lo || q0 + 32 > all_lim)
+            paths(std::true_type());
           else
-            all(std::false_type());
-          tmem_st32(tS, pk);
+            paths(std::false_type());
+          tmem_st16(tS, pk);
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(bar(kBarPReady));
@@ -607,35 +608,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             !(ok = mbar_wait_warp(bar(kBarEpiFree + Ly::kEpiTurns - 1), (k - 1) & 1, ctx, 0x734)))
           break;
         tc_fence_after();
-        // two 32-column chunks of dP^T.  dS^T goes into row r of the shared
-        // dS^T tile (128-byte swizzle: 16-byte chunk c lands at c ^ (r % 8)),
-        // and where dK reads it from tensor memory also back into the dP^T
-        // columns this warp has read, packed two queries per column as P^T is.
-#pragma unroll
-        for (int ch = 0; ch < 2; ++ch) {
-          uint32_t u[32];
-          tmem_ld32(tDP + 32 * ch, u);
+        // dS^T goes into row r of the shared dS^T tile (128-byte swizzle:
+        // 16-byte chunk c lands at c ^ (r % 8)), and where dK reads it from
+        // tensor memory also back into the dP^T columns this warp has read,
+        // packed two queries per column as P^T is.
+        {
+          uint32_t u[32], ds[16];
+          tmem_ld32(tDP, u);
           tmem_wait_ld();
-          uint32_t ds[16];
-          auto dx = [&](int c, float da, float db) {  // columns 2c, 2c + 1 of the chunk
+          auto dx = [&](int c, float da, float db) {  // columns 2c, 2c + 1
             const uint64_t e = fma_f32x2(f32x2(da, db), f32x2(-1.f),
                                          f32x2(__uint_as_float(u[2 * c]),
                                                __uint_as_float(u[2 * c + 1])));
             float a, b;
-            f32x2_split(mul_f32x2(e, unpack_f16x2(px[16 * ch + c])), a, b);
+            f32x2_split(mul_f32x2(e, unpack_f16x2(px[c])), a, b);
             ds[c] = pack_bf16x2(a, b);
           };
 #pragma unroll
           for (int c4 = 0; c4 < 8; ++c4) {
-            const float4 dd = Dv4[8 * ch + c4];  // one broadcast load for four columns
+            const float4 dd = Dv4[c4];  // one broadcast load for four columns
             dx(2 * c4, dd.x, dd.y);
             dx(2 * c4 + 1, dd.z, dd.w);
           }
-          if constexpr (Ly::kSeparateDq) tmem_st16(tDP + 16 * ch, ds);
+          if constexpr (Ly::kSeparateDq) tmem_st16(tDP, ds);
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            st_shared_v4(sDSrow + (((4 * ch + c) ^ (r & 7)) << 4), ds[4 * c], ds[4 * c + 1],
-                         ds[4 * c + 2], ds[4 * c + 3]);
+            st_shared_v4(sDSrow + (((4 * (quarter & 1) + c) ^ (r & 7)) << 4), ds[4 * c],
+                         ds[4 * c + 1], ds[4 * c + 2], ds[4 * c + 3]);
         }
         tmem_wait_st();
         fence_proxy_async_smem();
@@ -644,18 +643,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++it == t.n_it) it = 0, ++h;
       }
       if (!ok) break;
-      // Epilogue of the item: dV (half 0) and dK (half 1, times the softmax
-      // scale) from tensor memory, rounded to bf16 into the shared dS^T tile
-      // (its two 16 KB blocks are the 64-column boxes of the output tile map,
-      // with the same 128-byte swizzle) and written by TMA tile stores, which
-      // leave out the rows past N.  One elected warp per turn issues them;
-      // their shared-memory reads complete before the tile is used again.
-      if (!(ok = mbar_wait_warp(bar(kBarAccFull), k & 1, ctx, 0x738 + half))) break;
+      // Epilogue of the item: dV (quarters 0 and 1, half of its columns each)
+      // and dK (2 and 3; times the softmax scale) from tensor memory, rounded
+      // to bf16 into the shared dS^T tile (its two 16 KB blocks are the
+      // 64-column boxes of the output tile map, with the same 128-byte swizzle)
+      // and written by TMA tile stores, which leave out the rows past N.  One
+      // elected warp per turn issues them; their shared-memory reads complete
+      // before the tile is used again.
+      if (!(ok = mbar_wait_warp(bar(kBarAccFull), k & 1, ctx, 0x738))) break;
       tc_fence_after();
-      const uint32_t tAcc = tbase + lane_off + (half == 0 ? Ly::kColDV : Ly::kColDK);
-      const float mult = half == 0 ? 1.f : scale;
+      const int which = quarter >> 1, part = quarter & 1;  // dV or dK; half of its columns
+      const uint32_t tAcc =
+          tbase + lane_off + (which == 0 ? Ly::kColDV : Ly::kColDK) + (HD / 2) * part;
+      const float mult = which == 0 ? 1.f : scale;
       for (int turn = 0; ok && turn < Ly::kEpiTurns; ++turn) {
-        if (Ly::kEpiTurns == 1 || half == turn) {
+        if (Ly::kEpiTurns == 1 || which == turn) {
           // The tile's previous contents: this item's dS^T (the contractions
           // have completed: AccFull), then the previous turn's store -- of this
           // item for turn 1, of the previous item for turn 0.
@@ -664,22 +666,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (prev_item >= 0 &&
               !(ok = mbar_wait_warp(bar(kBarEpiFree + prev_turn), prev_item & 1, ctx, 0x73A)))
             break;
-          const uint32_t row = sbase + Ly::kDS + (HD == 64 ? half * 16384 : 0) + r * 128;
+          // d = 128: block `part` of the tensor's two; d = 64: half of block `which`
+          const uint32_t row =
+              sbase + Ly::kDS + (HD == 128 ? part : which) * 16384 + r * 128;
 #pragma unroll
-          for (int c4 = 0; c4 < HD / 32; ++c4) {
+          for (int c4 = 0; c4 < HD / 64; ++c4) {
             uint32_t o[32];
             tmem_ld32(tAcc + 32 * c4, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int c8 = 0; c8 < 4; ++c8) {  // 16-byte chunk j of 64-column block c4 / 2
-              const int j = 4 * (c4 & 1) + c8;
+            for (int c8 = 0; c8 < 4; ++c8) {  // 16-byte chunk j of the 64-column block
+              const int j = (HD == 128 ? 4 * c4 : 4 * part) + c8;
               uint32_t w4[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 w4[e] = pack_bf16x2(__uint_as_float(o[8 * c8 + 2 * e]) * mult,
                                     __uint_as_float(o[8 * c8 + 2 * e + 1]) * mult);
-              st_shared_v4(row + (c4 >> 1) * 16384 + ((j ^ (r & 7)) << 4), w4[0], w4[1], w4[2],
-                           w4[3]);
+              st_shared_v4(row + ((j ^ (r & 7)) << 4), w4[0], w4[1], w4[2], w4[3]);
             }
           }
           tc_fence_before();
@@ -687,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           mbar_arrive(bar(kBarEpiFull + turn));
         }
-        if (warp == 4 + 4 * (Ly::kEpiTurns == 2 ? turn : 0)) {  // the turn's issuing warp
+        if (warp == 4 + 8 * turn) {  // the turn's issuing warp, one of those that wrote
           if (!(ok = mbar_wait_warp(bar(kBarEpiFull + turn), k & 1, ctx, 0x73B))) break;
           if (elect_one()) {
             const int bh = t.b * p.Hkv + t.hk;
@@ -729,10 +732,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool got = mbar_wait_warp(bar(kBarDQFull), g & 1, ctx, 0x740);
         if (!(ok = named_barrier_and(kDrainBarrierId, 128, got))) break;
         tc_fence_after();
-        // 32-column chunks.  For d = 128, chunks 0-2 are loaded, chunk 0
-        // staged, chunk 3 loaded into chunk 0's registers, and only then are
-        // the columns released to the MMA warp (the register budget does not
-        // hold all four).
+        // 32-column chunks.  The registers hold two: for d = 128, chunks 2 and
+        // 3 follow as chunks 0 and 1 are staged, and only then are the columns
+        // released to the MMA warp.
         auto stage = [&](int c, const uint32_t (&v)[32]) {
           const uint32_t buf = sbase + Ly::kStage + (c & 1) * 16384;
           // the reduction that last read this buffer (two boxes ago) is done
@@ -754,17 +756,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(tDQ, a0);
         tmem_ld32(tDQ + 32, a1);
         if constexpr (HD == 128) {
-          uint32_t a2[32];
-          tmem_ld32(tDQ + 64, a2);
           tmem_wait_ld();
           stage(0, a0);
-          tmem_ld32(tDQ + 96, a0);
+          tmem_ld32(tDQ + 64, a0);
+          stage(1, a1);
+          tmem_ld32(tDQ + 96, a1);
           tmem_wait_ld();
           tc_fence_before();
           mbar_arrive(bar(kBarDQFree));
-          stage(1, a1);
-          stage(2, a2);
-          stage(3, a0);
+          stage(2, a0);
+          stage(3, a1);
         } else {
           tmem_wait_ld();
           tc_fence_before();
