@@ -34,7 +34,10 @@
 namespace attn {
 namespace score_bwd {
 
-constexpr int kThreads = 704;
+// d = 128 takes two idle warps more, to make the last four a warpgroup that can
+// hand its registers to the drain's (see setmaxnreg below).
+template <int HD>
+constexpr int kThreads = HD == 128 ? 768 : 704;
 constexpr int kSoftmaxThreads = 512;
 constexpr int kProducerWarp = 20;
 constexpr int kMmaWarp = 21;
@@ -173,7 +176,7 @@ __device__ __forceinline__ uint64_t unpack_f16x2(uint32_t w) {
 // (16 rows) per k-step, its MN extent spanning blocks 16 KB apart (LBO).
 
 template <int HD, bool CAP, bool SLOPES>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads<HD>, 1)
     score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV,
@@ -236,248 +239,255 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_wait();
   grid_dep_launch();
 
-  if (warp == kProducerWarp) {
-    // ------------------------------------------------------------ TMA producer
-    // The whole warp runs the loop (warp-uniform operands); one lane issues.
-    // Per item: V (free once the previous item's last dP is done), K (free
-    // once its last dK/dQ is done); per query tile g: dO(g) (its stage is free
-    // once the dV of the tile that last held it is done) and Q(g+1) with its
-    // L and D vectors (two stages, free once dK(g-1) is done), which for the
-    // last tile of an item is the first of the next.
-    auto load_q = [&](int g, int b, int h, int qt) {  // elected lane only
-      const int s = g & 1;
-      mbar_arrive_expect_tx(bar(kBarQFull + s), Ly::kTileBytes + 1024);
-#pragma unroll
-      for (int cb = 0; cb < HD / 64; ++cb)
-        tma_load_4d(sbase + Ly::kQ + s * Ly::kTileBytes + cb * 16384, &tmQ, bar(kBarQFull + s),
-                    cb * 64, qt * 128, h, b);
-      const size_t vo = (size_t(b) * p.Hq + h) * p.Npad + size_t(qt) * 128;
-      bulk_load(sbase + Ly::kVec + s * 1024, ws.L2 + vo, 512, bar(kBarQFull + s));
-      bulk_load(sbase + Ly::kVec + s * 1024 + 512, ws.D + vo, 512, bar(kBarQFull + s));
-    };
-    bool ok = true;
-    int g = 0;
-    for (int k = 0, i = snake_item(0, cta, G, n_items); ok && i >= 0; ++k) {
-      const Item t = imap.item(i);
-      const int h0 = t.hk * p.group;  // the group's first query head
-      const int next = snake_item(k + 1, cta, G, n_items);
-      const Item nt = next >= 0 ? imap.item(next) : t;
-      if (k > 0 && !(ok = mbar_wait_warp(bar(kBarVEmpty), (k - 1) & 1, ctx, 0x712))) break;
-      if (elect_one()) {
-        mbar_arrive_expect_tx(bar(kBarVFull), Ly::kTileBytes);
+  // Registers for d = 128: 80 for each of 768 threads at the launch.  The last
+  // warpgroup (copies and tensor core) gives 32 of them back and the drain's
+  // takes 32 more, so that three of dQ's four 32-column chunks leave tensor
+  // memory at once: 4 x 80 + 112 + 48 = 6 x 80.
+  if (warp >= kProducerWarp) {
+    if constexpr (HD == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp == kProducerWarp) {
+      // ------------------------------------------------------------ TMA producer
+      // The whole warp runs the loop (warp-uniform operands); one lane issues.
+      // Per item: V (free once the previous item's last dP is done), K (free
+      // once its last dK/dQ is done); per query tile g: dO(g) (its stage is free
+      // once the dV of the tile that last held it is done) and Q(g+1) with its
+      // L and D vectors (two stages, free once dK(g-1) is done), which for the
+      // last tile of an item is the first of the next.
+      auto load_q = [&](int g, int b, int h, int qt) {  // elected lane only
+        const int s = g & 1;
+        mbar_arrive_expect_tx(bar(kBarQFull + s), Ly::kTileBytes + 1024);
 #pragma unroll
         for (int cb = 0; cb < HD / 64; ++cb)
-          tma_load_4d(sbase + Ly::kV + cb * 16384, &tmV, bar(kBarVFull), cb * 64, t.jt * 128, t.hk,
-                      t.b);
-      }
-      __syncwarp();
-      if (k > 0 && !(ok = mbar_wait_warp(bar(kBarKEmpty), (k - 1) & 1, ctx, 0x713))) break;
-      if (elect_one()) {
-        mbar_arrive_expect_tx(bar(kBarKFull), Ly::kTileBytes);
-#pragma unroll
-        for (int cb = 0; cb < HD / 64; ++cb)
-          tma_load_4d(sbase + Ly::kK + cb * 16384, &tmK, bar(kBarKFull), cb * 64, t.jt * 128, t.hk,
-                      t.b);
-        if (k == 0) load_q(0, t.b, h0, t.it0);
-        // Warm L2 (and the address translation) for the next item: a new head
-        // is often a cold region, and its first tiles are needed right at the
-        // item switch.
-        if (next >= 0) {
-          const int nh = nt.hk * p.group;
-#pragma unroll
-          for (int cb = 0; cb < HD / 64; ++cb) {
-            tma_prefetch_4d(&tmK, cb * 64, nt.jt * 128, nt.hk, nt.b);
-            tma_prefetch_4d(&tmV, cb * 64, nt.jt * 128, nt.hk, nt.b);
-            tma_prefetch_4d(&tmQ, cb * 64, nt.it0 * 128, nh, nt.b);
-            tma_prefetch_3d(&tmdO, cb * 64, nt.it0 * 128, nt.b * p.Hq + nh);
-          }
-          const size_t vo = (size_t(nt.b) * p.Hq + nh) * p.Npad + size_t(nt.it0) * 128;
-          bulk_prefetch(ws.L2 + vo, 512);
-          bulk_prefetch(ws.D + vo, 512);
-        }
-      }
-      __syncwarp();
-      for (int h = 0, it = 0; h < p.group; ++g) {
-        const int ds_ = g % Ly::kDOStages, dn = g / Ly::kDOStages;
-        if (dn > 0 &&
-            !(ok = mbar_wait_warp(bar(kBarDOEmpty + ds_), (dn - 1) & 1, ctx, 0x711)))
-          break;
+          tma_load_4d(sbase + Ly::kQ + s * Ly::kTileBytes + cb * 16384, &tmQ, bar(kBarQFull + s),
+                      cb * 64, qt * 128, h, b);
+        const size_t vo = (size_t(b) * p.Hq + h) * p.Npad + size_t(qt) * 128;
+        bulk_load(sbase + Ly::kVec + s * 1024, ws.L2 + vo, 512, bar(kBarQFull + s));
+        bulk_load(sbase + Ly::kVec + s * 1024 + 512, ws.D + vo, 512, bar(kBarQFull + s));
+      };
+      bool ok = true;
+      int g = 0;
+      for (int k = 0, i = snake_item(0, cta, G, n_items); ok && i >= 0; ++k) {
+        const Item t = imap.item(i);
+        const int h0 = t.hk * p.group;  // the group's first query head
+        const int next = snake_item(k + 1, cta, G, n_items);
+        const Item nt = next >= 0 ? imap.item(next) : t;
+        if (k > 0 && !(ok = mbar_wait_warp(bar(kBarVEmpty), (k - 1) & 1, ctx, 0x712))) break;
         if (elect_one()) {
-          mbar_arrive_expect_tx(bar(kBarDOFull + ds_), Ly::kTileBytes);
+          mbar_arrive_expect_tx(bar(kBarVFull), Ly::kTileBytes);
 #pragma unroll
           for (int cb = 0; cb < HD / 64; ++cb)
-            tma_load_3d(sbase + Ly::kDO + ds_ * Ly::kTileBytes + cb * 16384, &tmdO,
-                        bar(kBarDOFull + ds_), cb * 64, (t.it0 + it) * 128,
-                        t.b * p.Hq + h0 + h);
+            tma_load_4d(sbase + Ly::kV + cb * 16384, &tmV, bar(kBarVFull), cb * 64, t.jt * 128, t.hk,
+                        t.b);
         }
         __syncwarp();
-        if (++it == t.n_it) it = 0, ++h;
-        int qb = t.b, qh = h0 + h, qt = t.it0 + it;
-        if (h == p.group) {
-          if (next < 0) continue;
-          qb = nt.b;
-          qh = nt.hk * p.group;
-          qt = nt.it0;
-        }
-        const int gn = g + 1;
-        if (gn >= 2 &&
-            !(ok = mbar_wait_warp(bar(kBarQEmpty + (gn & 1)), ((gn >> 1) - 1) & 1, ctx, 0x710)))
-          break;
-        if (elect_one()) load_q(gn, qb, qh, qt);
-        __syncwarp();
-      }
-      i = next;
-    }
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------ MMA issuer
-    // The whole warp runs the loop and waits; one elected lane issues.  Every
-    // descriptor is a per-tile base plus a compile-time k-step offset.
-    constexpr uint32_t kIdS = make_idesc_bf16(128, 128, 0, 0);  // S^T, dP^T
-    constexpr uint32_t kIdV = make_idesc_bf16(128, HD, 0, 1);   // dV, dK
-    constexpr uint32_t kIdQ = make_idesc_bf16(128, HD, 1, 1);   // dQ = dS K
-    const uint64_t dK_k = make_sdesc_sw128(sbase + Ly::kK, 16, 1024);       // K, K-major
-    const uint64_t dK_mn = make_sdesc_sw128(sbase + Ly::kK, 16384, 1024);   // K, MN-major
-    const uint64_t dV_k = make_sdesc_sw128(sbase + Ly::kV, 16, 1024);
-    const uint64_t dS_k = make_sdesc_sw128(sbase + Ly::kDS, 16, 1024);      // dS^T, K-major
-    const uint64_t dS_mn = make_sdesc_sw128(sbase + Ly::kDS, 16384, 1024);  // dS, MN-major
-    const uint32_t tS = tbase + Ly::kColS, tDP = tbase + Ly::kColDP;
-    const uint32_t tDV = tbase + Ly::kColDV, tDK = tbase + Ly::kColDK;
-    const uint32_t tDQ = tbase + Ly::kColDQ;
-    // Issue order per query tile:  dP, dV, S(next), dQ, dK (d = 128; else dK,
-    // dQ).  S(next) goes right behind dV (which has consumed P from the S
-    // columns; the softmax warps keep P in registers), so the softmax warps
-    // compute the next tile's P while the tensor core runs dK and dQ.  The
-    // first S of an item waits for its K.
-    auto issue_s = [&](int stage) {  // S^T = K Q^T; elected lane only
-      const uint64_t dq = make_sdesc_sw128(sbase + Ly::kQ + stage * Ly::kTileBytes, 16, 1024);
-#pragma unroll
-      for (int k = 0; k < HD / 16; ++k) {
-        const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-        mma_ss(tS, sdesc_add(dK_k, off), sdesc_add(dq, off), kIdS, k > 0 ? 1u : 0u);
-      }
-      tc_commit(bar(kBarSFull));
-    };
-    bool ok = true;
-    int g = 0;
-    for (int k = 0, i = snake_item(0, cta, G, n_items); ok && i >= 0; ++k) {
-      const int total = imap.item(i).n_it * p.group;
-      if (!(ok = mbar_wait_warp(bar(kBarKFull), k & 1, ctx, 0x720))) break;
-      if (!(ok = mbar_wait_warp(bar(kBarQFull + (g & 1)), (g >> 1) & 1, ctx, 0x721))) break;
-      tc_fence_after();
-      if (elect_one()) issue_s(g & 1);
-      __syncwarp();
-      if (!(ok = mbar_wait_warp(bar(kBarVFull), k & 1, ctx, 0x727))) break;
-      for (int it = 0; it < total; ++it, ++g) {
-        const int s = g & 1;
-        const bool last = it + 1 == total;
-        const uint32_t sQ = sbase + Ly::kQ + s * Ly::kTileBytes;
-        const int ds_ = g % Ly::kDOStages;
-        const uint32_t sDO = sbase + Ly::kDO + ds_ * Ly::kTileBytes;
-        const uint64_t dQ_mn = make_sdesc_sw128(sQ, 16384, 1024);
-        const uint64_t dO_k = make_sdesc_sw128(sDO, 16, 1024);
-        const uint64_t dO_mn = make_sdesc_sw128(sDO, 16384, 1024);
-        const uint32_t acc0 = it > 0 ? 1u : 0u;
-        // dP^T = V dO^T.  When dQ shares the dP columns, they held the previous
-        // dQ: wait for its drain.  (Otherwise the previous dP has been read:
-        // the softmax warps signalled DS_READY, which the last tile waited on.)
-        if (!(ok = mbar_wait_warp(bar(kBarDOFull + ds_), (g / Ly::kDOStages) & 1, ctx, 0x722)))
-          break;
-        if (!Ly::kSeparateDq && g > 0 &&
-            !(ok = mbar_wait_warp(bar(kBarDQFree), (g - 1) & 1, ctx, 0x723)))
-          break;
-        tc_fence_after();
+        if (k > 0 && !(ok = mbar_wait_warp(bar(kBarKEmpty), (k - 1) & 1, ctx, 0x713))) break;
         if (elect_one()) {
+          mbar_arrive_expect_tx(bar(kBarKFull), Ly::kTileBytes);
 #pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-            mma_ss(tDP, sdesc_add(dV_k, off), sdesc_add(dO_k, off), kIdS, kk > 0 ? 1u : 0u);
+          for (int cb = 0; cb < HD / 64; ++cb)
+            tma_load_4d(sbase + Ly::kK + cb * 16384, &tmK, bar(kBarKFull), cb * 64, t.jt * 128, t.hk,
+                        t.b);
+          if (k == 0) load_q(0, t.b, h0, t.it0);
+          // Warm L2 (and the address translation) for the next item: a new head
+          // is often a cold region, and its first tiles are needed right at the
+          // item switch.
+          if (next >= 0) {
+            const int nh = nt.hk * p.group;
+#pragma unroll
+            for (int cb = 0; cb < HD / 64; ++cb) {
+              tma_prefetch_4d(&tmK, cb * 64, nt.jt * 128, nt.hk, nt.b);
+              tma_prefetch_4d(&tmV, cb * 64, nt.jt * 128, nt.hk, nt.b);
+              tma_prefetch_4d(&tmQ, cb * 64, nt.it0 * 128, nh, nt.b);
+              tma_prefetch_3d(&tmdO, cb * 64, nt.it0 * 128, nt.b * p.Hq + nh);
+            }
+            const size_t vo = (size_t(nt.b) * p.Hq + nh) * p.Npad + size_t(nt.it0) * 128;
+            bulk_prefetch(ws.L2 + vo, 512);
+            bulk_prefetch(ws.D + vo, 512);
           }
-          tc_commit(bar(kBarDPFull));
-          if (last) tc_commit(bar(kBarVEmpty));
         }
         __syncwarp();
-        // dV += P^T dO, P^T read from tensor memory: the softmax warps of 32
-        // query columns packed them into the first 16 of their own.  The first dV of an item overwrites the accumulator: the
-        // previous item's epilogue must have read it.
-        if (!(ok = mbar_wait_warp(bar(kBarPReady), g & 1, ctx, 0x724))) break;
-        if (it == 0 && k > 0 &&
-            !(ok = mbar_wait_warp(bar(kBarAccEmpty), (k - 1) & 1, ctx, 0x728)))
-          break;
-        tc_fence_after();
-        if (elect_one()) {
+        for (int h = 0, it = 0; h < p.group; ++g) {
+          const int ds_ = g % Ly::kDOStages, dn = g / Ly::kDOStages;
+          if (dn > 0 &&
+              !(ok = mbar_wait_warp(bar(kBarDOEmpty + ds_), (dn - 1) & 1, ctx, 0x711)))
+            break;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(bar(kBarDOFull + ds_), Ly::kTileBytes);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ts(tDV, tS + 32 * (kk >> 1) + 8 * (kk & 1), sdesc_add(dO_mn, kk * 2048), kIdV,
-                   kk > 0 ? 1u : acc0);
-          tc_commit(bar(kBarDOEmpty + ds_));
+            for (int cb = 0; cb < HD / 64; ++cb)
+              tma_load_3d(sbase + Ly::kDO + ds_ * Ly::kTileBytes + cb * 16384, &tmdO,
+                          bar(kBarDOFull + ds_), cb * 64, (t.it0 + it) * 128,
+                          t.b * p.Hq + h0 + h);
+          }
+          __syncwarp();
+          if (++it == t.n_it) it = 0, ++h;
+          int qb = t.b, qh = h0 + h, qt = t.it0 + it;
+          if (h == p.group) {
+            if (next < 0) continue;
+            qb = nt.b;
+            qh = nt.hk * p.group;
+            qt = nt.it0;
+          }
+          const int gn = g + 1;
+          if (gn >= 2 &&
+              !(ok = mbar_wait_warp(bar(kBarQEmpty + (gn & 1)), ((gn >> 1) - 1) & 1, ctx, 0x710)))
+            break;
+          if (elect_one()) load_q(gn, qb, qh, qt);
+          __syncwarp();
         }
+        i = next;
+      }
+    } else if (warp == kMmaWarp) {
+      // ------------------------------------------------------------ MMA issuer
+      // The whole warp runs the loop and waits; one elected lane issues.  Every
+      // descriptor is a per-tile base plus a compile-time k-step offset.
+      constexpr uint32_t kIdS = make_idesc_bf16(128, 128, 0, 0);  // S^T, dP^T
+      constexpr uint32_t kIdV = make_idesc_bf16(128, HD, 0, 1);   // dV, dK
+      constexpr uint32_t kIdQ = make_idesc_bf16(128, HD, 1, 1);   // dQ = dS K
+      const uint64_t dK_k = make_sdesc_sw128(sbase + Ly::kK, 16, 1024);       // K, K-major
+      const uint64_t dK_mn = make_sdesc_sw128(sbase + Ly::kK, 16384, 1024);   // K, MN-major
+      const uint64_t dV_k = make_sdesc_sw128(sbase + Ly::kV, 16, 1024);
+      const uint64_t dS_k = make_sdesc_sw128(sbase + Ly::kDS, 16, 1024);      // dS^T, K-major
+      const uint64_t dS_mn = make_sdesc_sw128(sbase + Ly::kDS, 16384, 1024);  // dS, MN-major
+      const uint32_t tS = tbase + Ly::kColS, tDP = tbase + Ly::kColDP;
+      const uint32_t tDV = tbase + Ly::kColDV, tDK = tbase + Ly::kColDK;
+      const uint32_t tDQ = tbase + Ly::kColDQ;
+      // Issue order per query tile:  dP, dV, S(next), dQ, dK (d = 128; else dK,
+      // dQ).  S(next) goes right behind dV (which has consumed P from the S
+      // columns; the softmax warps keep P in registers), so the softmax warps
+      // compute the next tile's P while the tensor core runs dK and dQ.  The
+      // first S of an item waits for its K.
+      auto issue_s = [&](int stage) {  // S^T = K Q^T; elected lane only
+        const uint64_t dq = make_sdesc_sw128(sbase + Ly::kQ + stage * Ly::kTileBytes, 16, 1024);
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k) {
+          const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
+          mma_ss(tS, sdesc_add(dK_k, off), sdesc_add(dq, off), kIdS, k > 0 ? 1u : 0u);
+        }
+        tc_commit(bar(kBarSFull));
+      };
+      bool ok = true;
+      int g = 0;
+      for (int k = 0, i = snake_item(0, cta, G, n_items); ok && i >= 0; ++k) {
+        const int total = imap.item(i).n_it * p.group;
+        if (!(ok = mbar_wait_warp(bar(kBarKFull), k & 1, ctx, 0x720))) break;
+        if (!(ok = mbar_wait_warp(bar(kBarQFull + (g & 1)), (g >> 1) & 1, ctx, 0x721))) break;
+        tc_fence_after();
+        if (elect_one()) issue_s(g & 1);
         __syncwarp();
-        // S of the item's next query tile into the S columns, behind dV
-        if (!last) {
-          const int s1 = (g + 1) & 1;
-          if (!(ok = mbar_wait_warp(bar(kBarQFull + s1), ((g + 1) >> 1) & 1, ctx, 0x726)))
+        if (!(ok = mbar_wait_warp(bar(kBarVFull), k & 1, ctx, 0x727))) break;
+        for (int it = 0; it < total; ++it, ++g) {
+          const int s = g & 1;
+          const bool last = it + 1 == total;
+          const uint32_t sQ = sbase + Ly::kQ + s * Ly::kTileBytes;
+          const int ds_ = g % Ly::kDOStages;
+          const uint32_t sDO = sbase + Ly::kDO + ds_ * Ly::kTileBytes;
+          const uint64_t dQ_mn = make_sdesc_sw128(sQ, 16384, 1024);
+          const uint64_t dO_k = make_sdesc_sw128(sDO, 16, 1024);
+          const uint64_t dO_mn = make_sdesc_sw128(sDO, 16384, 1024);
+          const uint32_t acc0 = it > 0 ? 1u : 0u;
+          // dP^T = V dO^T.  When dQ shares the dP columns, they held the previous
+          // dQ: wait for its drain.  (Otherwise the previous dP has been read:
+          // the softmax warps signalled DS_READY, which the last tile waited on.)
+          if (!(ok = mbar_wait_warp(bar(kBarDOFull + ds_), (g / Ly::kDOStages) & 1, ctx, 0x722)))
+            break;
+          if (!Ly::kSeparateDq && g > 0 &&
+              !(ok = mbar_wait_warp(bar(kBarDQFree), (g - 1) & 1, ctx, 0x723)))
             break;
           tc_fence_after();
-          if (elect_one()) issue_s(s1);
-          __syncwarp();
-        }
-        if (!(ok = mbar_wait_warp(bar(kBarDSReady), g & 1, ctx, 0x725))) break;
-        tc_fence_after();
-        if constexpr (Ly::kSeparateDq) {
           if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)  // dS^T packed like P^T, in the dP^T columns
-              mma_ts(tDK, tDP + 32 * (kk >> 1) + 8 * (kk & 1), sdesc_add(dQ_mn, kk * 2048), kIdV,
-                     kk > 0 ? 1u : acc0);
-            tc_commit(bar(kBarQEmpty + s));
+            for (int kk = 0; kk < HD / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+              mma_ss(tDP, sdesc_add(dV_k, off), sdesc_add(dO_k, off), kIdS, kk > 0 ? 1u : 0u);
+            }
+            tc_commit(bar(kBarDPFull));
+            if (last) tc_commit(bar(kBarVEmpty));
           }
           __syncwarp();
-          // With its own columns, dQ waits only for the previous dQ's drain.
-          if (g > 0 && !(ok = mbar_wait_warp(bar(kBarDQFree), (g - 1) & 1, ctx, 0x723))) break;
+          // dV += P^T dO, P^T read from tensor memory: the softmax warps of 32
+          // query columns packed them into the first 16 of their own.  The first dV of an item overwrites the accumulator: the
+          // previous item's epilogue must have read it.
+          if (!(ok = mbar_wait_warp(bar(kBarPReady), g & 1, ctx, 0x724))) break;
+          if (it == 0 && k > 0 &&
+              !(ok = mbar_wait_warp(bar(kBarAccEmpty), (k - 1) & 1, ctx, 0x728)))
+            break;
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              mma_ss(tDQ, sdesc_add(dS_mn, kk * 2048), sdesc_add(dK_mn, kk * 2048), kIdQ,
-                     kk > 0 ? 1u : 0u);
-            tc_commit(bar(kBarDQFull));
-          }
-          __syncwarp();
-        } else {
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_ss(tDQ, sdesc_add(dS_mn, kk * 2048), sdesc_add(dK_mn, kk * 2048), kIdQ,
-                     kk > 0 ? 1u : 0u);
-            tc_commit(bar(kBarDQFull));
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-              mma_ss(tDK, sdesc_add(dS_k, off), sdesc_add(dQ_mn, kk * 2048), kIdV,
+              mma_ts(tDV, tS + 32 * (kk >> 1) + 8 * (kk & 1), sdesc_add(dO_mn, kk * 2048), kIdV,
                      kk > 0 ? 1u : acc0);
+            tc_commit(bar(kBarDOEmpty + ds_));
+          }
+          __syncwarp();
+          // S of the item's next query tile into the S columns, behind dV
+          if (!last) {
+            const int s1 = (g + 1) & 1;
+            if (!(ok = mbar_wait_warp(bar(kBarQFull + s1), ((g + 1) >> 1) & 1, ctx, 0x726)))
+              break;
+            tc_fence_after();
+            if (elect_one()) issue_s(s1);
+            __syncwarp();
+          }
+          if (!(ok = mbar_wait_warp(bar(kBarDSReady), g & 1, ctx, 0x725))) break;
+          tc_fence_after();
+          if constexpr (Ly::kSeparateDq) {
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)  // dS^T packed like P^T, in the dP^T columns
+                mma_ts(tDK, tDP + 32 * (kk >> 1) + 8 * (kk & 1), sdesc_add(dQ_mn, kk * 2048), kIdV,
+                       kk > 0 ? 1u : acc0);
+              tc_commit(bar(kBarQEmpty + s));
             }
-            tc_commit(bar(kBarQEmpty + s));
+            __syncwarp();
+            // With its own columns, dQ waits only for the previous dQ's drain.
+            if (g > 0 && !(ok = mbar_wait_warp(bar(kBarDQFree), (g - 1) & 1, ctx, 0x723))) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                mma_ss(tDQ, sdesc_add(dS_mn, kk * 2048), sdesc_add(dK_mn, kk * 2048), kIdQ,
+                       kk > 0 ? 1u : 0u);
+              tc_commit(bar(kBarDQFull));
+            }
+            __syncwarp();
+          } else {
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                mma_ss(tDQ, sdesc_add(dS_mn, kk * 2048), sdesc_add(dK_mn, kk * 2048), kIdQ,
+                       kk > 0 ? 1u : 0u);
+              tc_commit(bar(kBarDQFull));
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk) {
+                const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+                mma_ss(tDK, sdesc_add(dS_k, off), sdesc_add(dQ_mn, kk * 2048), kIdV,
+                       kk > 0 ? 1u : acc0);
+              }
+              tc_commit(bar(kBarQEmpty + s));
+            }
+            __syncwarp();
+          }
+          // dK and dQ have read the dS^T tile; the item's last tile also
+          // releases K and hands the accumulators to the epilogue.
+          if (elect_one()) {
+            tc_commit(bar(kBarDSFree));
+            if (last) {
+              tc_commit(bar(kBarKEmpty));
+              tc_commit(bar(kBarAccFull));
+            }
           }
           __syncwarp();
         }
-        // dK and dQ have read the dS^T tile; the item's last tile also
-        // releases K and hands the accumulators to the epilogue.
-        if (elect_one()) {
-          tc_commit(bar(kBarDSFree));
-          if (last) {
-            tc_commit(bar(kBarKEmpty));
-            tc_commit(bar(kBarAccFull));
-          }
-        }
-        __syncwarp();
+        i = snake_item(k + 1, cta, G, n_items);
       }
-      i = snake_item(k + 1, cta, G, n_items);
+      if (elect_one()) tc_commit(bar(kBarDrain));
+      __syncwarp();
+      volatile int never = 0;  // this wait ignores the CTA abort flag
+      const WaitCtx own{&never, err, kWaitLimitNs};
+      mbar_wait_warp(bar(kBarDrain), 0, own, 0x72F);
     }
-    if (elect_one()) tc_commit(bar(kBarDrain));
-    __syncwarp();
-    volatile int never = 0;  // this wait ignores the CTA abort flag
-    const WaitCtx own{&never, err, kWaitLimitNs};
-    mbar_wait_warp(bar(kBarDrain), 0, own, 0x72F);
   } else if (warp >= 4) {
     // ------------------------------------------------------------ softmax / dS
     const int quarter = (warp - 4) >> 2;  // query columns 32 quarter .. 32 quarter + 31
@@ -714,6 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     bulk_wait_group_all();  // the epilogue's stores complete before the CTA retires
   } else {
+    if constexpr (HD == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
     // ------------------------------------------------------------ dQ drain
     // Tensor memory -> registers -> swizzled fp32 staging tile -> TMA
     // reduce-add into the accumulator, 32 columns (16 KB) per box, two
@@ -732,9 +743,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool got = mbar_wait_warp(bar(kBarDQFull), g & 1, ctx, 0x740);
         if (!(ok = named_barrier_and(kDrainBarrierId, 128, got))) break;
         tc_fence_after();
-        // 32-column chunks.  The registers hold two: for d = 128, chunks 2 and
-        // 3 follow as chunks 0 and 1 are staged, and only then are the columns
-        // released to the MMA warp.
+        // 32-column chunks.  For d = 128 the registers hold three: chunk 3
+        // follows when chunk 0 is staged, and then the columns are released to
+        // the MMA warp.
         auto stage = [&](int c, const uint32_t (&v)[32]) {
           const uint32_t buf = sbase + Ly::kStage + (c & 1) * 16384;
           // the reduction that last read this buffer (two boxes ago) is done
@@ -756,16 +767,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(tDQ, a0);
         tmem_ld32(tDQ + 32, a1);
         if constexpr (HD == 128) {
+          uint32_t a2[32];
+          tmem_ld32(tDQ + 64, a2);
           tmem_wait_ld();
           stage(0, a0);
-          tmem_ld32(tDQ + 64, a0);
-          stage(1, a1);
-          tmem_ld32(tDQ + 96, a1);
+          tmem_ld32(tDQ + 96, a0);
           tmem_wait_ld();
           tc_fence_before();
           mbar_arrive(bar(kBarDQFree));
-          stage(2, a0);
-          stage(3, a1);
+          stage(1, a1);
+          stage(2, a2);
+          stage(3, a0);
         } else {
           tmem_wait_ld();
           tc_fence_before();
@@ -856,7 +868,7 @@ static cudaError_t launch_t(const ScoreBwdMaps& m, const Workspace& ws, const Sc
   const long long n_items = (long long)p.n_tiles * p.B * p.Hkv;
   const int sms = device_sm_count();
   const dim3 grid(unsigned(n_items < sms ? n_items : sms));
-  return launch_kernel(score_bwd_kernel<HD, CAP, SLOPES>, grid, dim3(kThreads), Ly::kBytes, stream,
+  return launch_kernel(score_bwd_kernel<HD, CAP, SLOPES>, grid, dim3(kThreads<HD>), Ly::kBytes, stream,
                        m.q, m.k, m.v, m.dout, m.acc, m.dk, m.dv, ws, p, heads_per_group(p), scale,
                        err);
 }
