@@ -90,12 +90,17 @@ constexpr uint32_t kFp16Span = 31;
 template <int D, int TYPE>
 struct Cfg {
   static constexpr int kRow = TYPE == kCacheInt4 ? D / 2 : TYPE == kCacheE4m3 ? D : 2 * D;  // bytes
-  static constexpr int KT = kRow > 64 ? 256 / kRow : 4;  // 1, 2, 2, 4, 4, 4
+  static constexpr int KT = TYPE == kCacheInt4 ? 2 : 256 / kRow;  // 1, 2, 2, 4, 2, 2
   static constexpr int kUnit = kWarps * KT * 16;         // keys of a unit
   static constexpr int kWords = kRow / 16;               // 32-bit words of K per row and thread,
   static constexpr int kChunks = kWords < 4 ? 1 : kWords / 4;  // in this many loads
   static constexpr int kVWords = kRow / 32;              // 32-bit words of V per row and thread
 };
+
+// Blocks of an SM at a time.
+constexpr int resident_blocks(int type, int ng) {
+  return type == kCacheInt4 ? (ng == 1 ? 3 : 2) : ng == 1 ? 3 : 2;
+}
 
 __device__ __forceinline__ void ld_stream(uint32_t (&r)[4], const uint8_t* p) {
   asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -805,7 +810,7 @@ __device__ __forceinline__ void join_parts(const DecodeArgs& a, const Parts& ps,
 }
 
 template <int D, int TYPE, int NG, bool MOD>
-__global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(kThreads, resident_blocks(TYPE, NG)) decode_kernel(const DecodeArgs a) {
   using C = Cfg<D, TYPE>;
   constexpr int U = C::kUnit;
   constexpr int kHeadStride = D + 8;
@@ -1059,7 +1064,7 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
 template <int D, int TYPE, int NG, bool MOD>
 cudaError_t launch(const DecodeArgs& a, cudaStream_t stream) {
   using C = Cfg<D, TYPE>;
-  constexpr int kPerSm = NG == 1 ? 3 : 2;  // resident blocks: see __launch_bounds__
+  constexpr int kPerSm = resident_blocks(TYPE, NG);
   // at most as many blocks as there can be units
   const int seen = a.window > 0 && a.window < a.c.capacity ? a.window : a.c.capacity;
   const int64_t units = int64_t(a.c.B) * a.head_blocks * (seen / C::kUnit + 2);

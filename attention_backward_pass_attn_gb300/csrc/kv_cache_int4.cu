@@ -40,24 +40,26 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// Largest finite magnitude of a lane's eight values as bf16 bits; 0xFFFF where
-// one is a NaN.  *inf: whether there is an infinity.
-__device__ __forceinline__ uint32_t amax8(const uint4& x, bool* inf) {
-  const uint32_t w[4] = {x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu, x.z & 0x7FFF7FFFu,
-                         x.w & 0x7FFF7FFFu};
-  uint32_t m = max_u16x2(max_u16x2(w[0], w[1]), max_u16x2(w[2], w[3]));
-  m = max(m & 0xFFFFu, m >> 16);
-  *inf = false;
-  if (m < 0x7F80u) return m;
-  if (m > 0x7F80u) return 0xFFFFu;
-  *inf = true;
-  m = 0;
+// Largest magnitude of a lane's eight values as bf16 bits.
+__device__ __forceinline__ uint32_t amax8(const uint4& x) {
+  const uint32_t m = max_u16x2(max_u16x2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                               max_u16x2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+  return max(m & 0xFFFFu, m >> 16);
+}
+
+// Two bf16 values without infinities and NaN, which are rare: those become the
+// largest finite number (clamped, later, to +-7) and zero.  *nan is set if
+// there was one, and *top is the largest magnitude of the finite ones.
+__device__ __forceinline__ uint32_t tame2(uint32_t w, uint32_t* top, bool* nan) {
+  uint32_t out = 0;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t lo = w[k] & 0xFFFFu, hi = w[k] >> 16;
-    m = max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+  for (int shift = 0; shift < 32; shift += 16) {
+    const uint32_t v = w >> shift & 0x7FFFu, sign = w >> shift & 0x8000u;
+    if (v < 0x7F80u) *top = max(*top, v);
+    *nan |= v > 0x7F80u;
+    out |= (v < 0x7F80u ? sign | v : v > 0x7F80u ? 0u : sign | 0x7F7Fu) << shift;
   }
-  return m;
+  return out;
 }
 
 // The group's factor from amax's bf16 bits.
@@ -68,40 +70,44 @@ __device__ __forceinline__ float factor_of(uint32_t amax) {
   return fmaxf(__uint_as_float(q & ~0x7FFFFu), 7.5231638452626401e-37f /* 2^-120 */);
 }
 
-// Eight values as nibbles.
-__device__ __forceinline__ uint32_t codes8(const uint4& v, float f, bool inf) {
-  const float r = 1.f / f, top = 7.f * f;
+// Eight finite values as nibbles; r = 1 / f, rounded to nearest.  CLAMP: they
+// may be beyond 7.5 f (an infinity's stand-in).
+template <bool CLAMP>
+__device__ __forceinline__ uint32_t codes8(const uint4& v, float f, float r) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const uint64_t rr = f32x2(r, r), nf = f32x2(-f, -f);
+  const uint64_t bias = f32x2(12582920.f, 12582920.f);  // 1.5 2^23 + 8
   uint32_t out = 0;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     float x0 = bf16lo_to_f32(w[k]), x1 = bf16hi_to_f32(w[k]);
-    if (inf) {
-      x0 = fminf(fmaxf(x0, -top), top);
-      x1 = fminf(fmaxf(x1, -top), top);
+    if (CLAMP) {
+      x0 = fminf(fmaxf(x0, -7.f * f), 7.f * f);
+      x1 = fminf(fmaxf(x1, -7.f * f), 7.f * f);
     }
-    const uint64_t x = f32x2(x0, x1), rr = f32x2(r, r);
-    const uint64_t q = mul_f32x2(x, rr);
-    const uint64_t rest = fma_f32x2(q, f32x2(-f, -f), x);
-    const float bias = 12582920.f;  // 1.5 2^23 + 8
+    const uint64_t x = f32x2(x0, x1), q = mul_f32x2(x, rr);
     float a, b;
-    f32x2_split(add_f32x2(fma_f32x2(rest, rr, q), f32x2(bias, bias)), a, b);
+    f32x2_split(add_f32x2(fma_f32x2(fma_f32x2(q, nf, x), rr, q), bias), a, b);
     out += __float_as_uint(a) * (1u << (8 * k)) + __float_as_uint(b) * (16u << (8 * k));
   }
   return out - 0x4B400000u * 0x11111111u;  // the bits of 1.5 2^23, eight times
 }
 
 // As kv_cache.cu's e4m3 rows: D / 16 lanes take a row of K and of V, eight
-// values of either half each.  Four lanes share a group.
+// values of either half each.  Four lanes share a group in either half of
+// either row; each of them works out one of the four factors, whose divisions
+// would otherwise be a third of the kernel's instructions.  Six blocks to an SM,
+// at 40 registers a thread: with the 58 that the compiler took unasked a padded
+// batch of 4 x 8,192 tokens, 16 heads, d=128, took 45 us in place of 40.
 template <int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 6)
     kv_write_int4_kernel(const CacheArgs c, const CacheRows r, unsigned rows, int* err) {
   constexpr int kLanes = D / 16, kGroups = kThreads / kLanes;
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x % kLanes;
   const unsigned i = blockIdx.x * kGroups + threadIdx.x / kLanes;
-  uint4 x[2][2] = {};
+  uint4 x[4] = {};  // K's halves, V's halves
   int64_t dst = -1;
   if (i < rows) {
     const Row w = row_of(i, c, r);
@@ -112,37 +118,53 @@ __global__ void __launch_bounds__(kThreads)
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(r.x[s]) +
                                                           w.b * r.sb[s] + w.h * r.sh[s] +
                                                           w.t * r.st[s]);
-        x[s][0] = __ldg(src + lane);
-        x[s][1] = __ldg(src + kLanes + lane);
+        x[2 * s] = __ldg(src + lane);
+        x[2 * s + 1] = __ldg(src + kLanes + lane);
       }
     }
   }
   if (!__any_sync(0xffffffffu, dst >= 0)) return;  // a padded batch's filling
-  bool inf[2][2];
-  uint32_t amax[2];  // of either half: K's in the low 16 bits, V's in the high ones
+  uint32_t top[4];
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    amax[half] = amax8(x[0][half], &inf[0][half]) | amax8(x[1][half], &inf[1][half]) << 16;
+  for (int g = 0; g < 4; ++g) top[g] = amax8(x[g]);
+  const bool odd = __any_sync(0xffffffffu, max(max(top[0], top[1]), max(top[2], top[3])) >= 0x7F80u);
+  uint32_t nans = 0;  // a bit per group
+  if (odd) {
 #pragma unroll
-    for (int o = 2; o > 0; o >>= 1)
-      amax[half] = max_u16x2(amax[half], __shfl_xor_sync(0xffffffffu, amax[half], o));
+    for (int g = 0; g < 4; ++g) {
+      bool nan = false;
+      top[g] = 0;
+      x[g].x = tame2(x[g].x, &top[g], &nan);
+      x[g].y = tame2(x[g].y, &top[g], &nan);
+      x[g].z = tame2(x[g].z, &top[g], &nan);
+      x[g].w = tame2(x[g].w, &top[g], &nan);
+      nans |= uint32_t(nan) << g;
+    }
+    nans |= __shfl_xor_sync(0xffffffffu, nans, 1);
+    nans |= __shfl_xor_sync(0xffffffffu, nans, 2);
+  }
+  uint32_t lo = top[0] | top[1] << 16, hi = top[2] | top[3] << 16;
+#pragma unroll
+  for (int o = 2; o > 0; o >>= 1) {
+    lo = max_u16x2(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = max_u16x2(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
+  const int mine = lane % 4;  // this lane's group of the four
+  const uint32_t both = mine & 2 ? hi : lo;
+  const float f = factor_of(mine & 1 ? both >> 16 : both & 0xFFFFu), inv = 1.f / f;
+  uint32_t codes[4];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const float fg = __shfl_sync(0xffffffffu, f, g, 4), rg = __shfl_sync(0xffffffffu, inv, g, 4);
+    codes[g] = odd ? codes8<true>(x[g], fg, rg) : codes8<false>(x[g], fg, rg);
   }
   if (dst < 0) return;
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    uint32_t* codes = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(s ? c.vc : c.kc) +
-                                                  dst * (D / 2));
-    uint16_t* factors = (s ? c.vf : c.kf) + dst * (D / kInt4Group);
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const uint32_t m = s ? amax[half] >> 16 : amax[half] & 0xFFFFu;
-      const bool nan = m == 0xFFFFu;
-      const float f = factor_of(nan ? 0u : m);
-      codes[half * kLanes + lane] = codes8(x[s][half], f, inf[s][half] || nan);
-      if (lane % 4 == 0)
-        factors[(half * kLanes + lane) / 4] = nan ? 0x7FFFu : uint16_t(__float_as_uint(f) >> 16);
-    }
-  }
+  for (int g = 0; g < 4; ++g)
+    reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(g < 2 ? c.kc : c.vc) +
+                                dst * (D / 2))[(g & 1) * kLanes + lane] = codes[g];
+  (mine < 2 ? c.kf : c.vf)[dst * (D / kInt4Group) + ((mine & 1) * kLanes + lane) / 4] =
+      nans >> mine & 1 ? 0x7FFFu : uint16_t(__float_as_uint(f) >> 16);
 }
 
 template <int D>

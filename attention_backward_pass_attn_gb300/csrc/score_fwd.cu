@@ -20,9 +20,9 @@
 //    halves need not wait for one another, and sixteen warps, each with half
 //    the columns of 32 rows, take the place of eight.
 //  * The bias -slope |i - j| of a tile wholly in its rows' past or future is a
-//    number of the row plus or minus slope times the column: a table of 128
-//    numbers a head in shared memory, added in the multiply-add that scales the
-//    score.
+//    number of the row plus or minus slope times the column, whose number the
+//    multiply-add has as an immediate operand.  (From a table in shared memory
+//    the same took N=4096 b4 h16 d=128 from 380 us without a bias to 520.)
 //  * A query head reads key head h / group, through 4-D tensor maps with the
 //    caller's strides: heads of a fused projection are taken as they lie.  The
 //    heads of a group run side by side, so the L2 serves all but one of them.
@@ -61,8 +61,7 @@ struct Layout {
   static constexpr int kV = kK + kStages * kTileBytes;
   static constexpr int kBar = kV + kStages * kTileBytes;
   static constexpr int kSum = kBar + (kNumBars * 8 + 15) / 16 * 16;  // [tile][half][128] fp32
-  static constexpr int kBias = kSum + 2 * 2 * 128 * 4;               // [tile][sign][128] fp32
-  static constexpr int kTmemSlot = kBias + 2 * 2 * 128 * 4;
+  static constexpr int kTmemSlot = kSum + 2 * 2 * 128 * 4;
   static constexpr int kAbort = kTmemSlot + 4;
   // Padded past half of the SM's shared memory: one CTA, which allocates all
   // 512 tensor-memory columns, per SM.
@@ -418,14 +417,12 @@ __global__ void __launch_bounds__(Warps<BOUNDED>::kThreads, 1)
         if (!(ok = named_barrier_and(kTileBarrier + t, kTileThreads, ok))) break;
         l += sums[128 * (1 - half)];
       } else {
-        constexpr bool kChanged = CAP || SLOPES;  // u becomes the score itself
+        // Under a cap u becomes the score in base 2, else it stays a raw product,
+        // to which the bias, divided by the scale, is added.
         float slope = 0.f;
-        float* bias = reinterpret_cast<float*>(smem + Ly::kBias) + 256 * t;
         if constexpr (SLOPES) {
           slope = __ldg(mp.slopes + tk.h) * 1.4426950408889634f;
-          bias[r] = slope * float(r);
-          bias[128 + r] = -slope * float(r);
-          named_barrier_sync(kTileBarrier + t, kTileThreads);
+          if (!CAP) slope /= mp.scale_log2;
         }
         for (int j = 0; j < tk.n_kv; ++j) {
           if (!(ok = mbar_wait_warp(bar(kBarSFull + t), (c + j) & 1, ctx, 0x630 + t))) break;
@@ -463,25 +460,16 @@ __global__ void __launch_bounds__(Warps<BOUNDED>::kThreads, 1)
             const int w0 = q_tile0 + 32 * (warp & 3);  // the warp's first row
             const bool past = kv0 + 127 <= w0;
             if (past || kv0 >= w0 + 31) {  // one sign for every distance of the warp
-              row = past ? -slope * d0 : slope * d0;
-              const float4* b4 = reinterpret_cast<const float4*>(bias + (past ? 0 : 128));
+              const float sl = past ? slope : -slope;
+              row = -sl * d0;
 #pragma unroll
-              for (int e = 0; e < 128; e += 4) {
-                const float4 b = b4[e / 4];
-                if constexpr (CAP) {
-                  put(e, add_f32x2(pair(e), f32x2(b.x, b.y)));
-                  put(e + 2, add_f32x2(pair(e + 2), f32x2(b.z, b.w)));
-                } else {
-                  put(e, fma_f32x2(pair(e), sc, f32x2(b.x, b.y)));
-                  put(e + 2, fma_f32x2(pair(e + 2), sc, f32x2(b.z, b.w)));
-                }
-              }
+              for (int e = 0; e < 128; ++e) u[e] = __float_as_uint(fmaf(sl, float(e), f(e)));
             } else {  // distances are whole numbers, exact below 2^24
 #pragma unroll
               for (int e = 0; e < 128; ++e)
-                u[e] = __float_as_uint(
-                    fmaf(-slope, fabsf(d0 - float(e)), CAP ? f(e) : f(e) * mp.scale_log2));
+                u[e] = __float_as_uint(fmaf(-slope, fabsf(d0 - float(e)), f(e)));
             }
+            if (!CAP) row *= mp.scale_log2;
           }
           if (edge) {
             const int e_lo = lo_q - kv0, e_hi = hi_q - kv0;
@@ -499,7 +487,7 @@ __global__ void __launch_bounds__(Warps<BOUNDED>::kThreads, 1)
           const float mx = max3f(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], m8[5]),
                                  fmaxf(m8[6], m8[7]));
           // scale > 0, so the maximum commutes with it
-          const float m_new = fmaxf(m, kChanged ? mx + row : mx * mp.scale_log2);
+          const float m_new = fmaxf(m, CAP ? mx + row : fmaf(mx, mp.scale_log2, row));
           // Lazy rescale: move the reference maximum (and rescale l and O by
           // 2^(m - m_new)) only when the maximum grew by more than 8 in base 2.
           const bool rescale = m_new > m + 8.f;
@@ -516,8 +504,8 @@ __global__ void __launch_bounds__(Warps<BOUNDED>::kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 64; e += 2) {
               float p0, p1;
-              f32x2_split(kChanged ? add_f32x2(pair(64 * h + e), mb)
-                                   : fma_f32x2(pair(64 * h + e), sc, mb), p0, p1);
+              f32x2_split(CAP ? add_f32x2(pair(64 * h + e), mb)
+                              : fma_f32x2(pair(64 * h + e), sc, mb), p0, p1);
               p0 = ex2(p0);
               p1 = ex2(p1);
               sum[(e >> 1) & 1] = add_f32x2(sum[(e >> 1) & 1], f32x2(p0, p1));
@@ -546,13 +534,7 @@ __global__ void __launch_bounds__(Warps<BOUNDED>::kThreads, 1)
           tc_fence_before();
           mbar_arrive(bar(kBarPReady + t));
         }
-        if constexpr (SLOPES) {
-          // All of the tile's warps stop or none, and the table has been read.
-          ok = ok && mbar_wait_warp(bar(kBarOFull + t), no & 1, ctx, 0x638 + t);
-          if (!(ok = named_barrier_and(kTileBarrier + t, kTileThreads, ok))) break;
-        } else {
-          if (!ok || !(ok = mbar_wait_warp(bar(kBarOFull + t), no & 1, ctx, 0x638 + t))) break;
-        }
+        if (!ok || !(ok = mbar_wait_warp(bar(kBarOFull + t), no & 1, ctx, 0x638 + t))) break;
       }
       c += tk.n_kv;
       ++no;
