@@ -38,13 +38,16 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ uint64_t f32x2(float x) { return f32x2(x, x); }
 
-// Two capped scores in base 2 by the polynomial.
-__device__ __forceinline__ uint64_t cap_poly(const ScoreMap& m, uint64_t u) {
+// The polynomial's factor: two capped scores in base 2 are u times it.
+__device__ __forceinline__ uint64_t cap_factor(const ScoreMap& m, uint64_t u) {
   const uint64_t z = mul_f32x2(u, u);
   uint64_t h = f32x2(m.poly[kTanhTerms - 1]);
 #pragma unroll
   for (int k = kTanhTerms - 2; k >= 0; --k) h = fma_f32x2(h, z, f32x2(m.poly[k]));
-  return mul_f32x2(u, h);
+  return h;
+}
+__device__ __forceinline__ uint64_t cap_poly(const ScoreMap& m, uint64_t u) {
+  return mul_f32x2(u, cap_factor(m, u));
 }
 
 // Whether the polynomial holds for all of the warp's raw products (n each).

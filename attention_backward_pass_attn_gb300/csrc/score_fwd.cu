@@ -14,11 +14,13 @@
 // differs:
 //
 //  * Scores are changed where they lie, in registers, before the row maximum.
-//  * A cap bounds the scores, |x| <= cap log2(e) in base 2.  Up to kBoundedLog2
-//    (a cap of 55) every 2^x and their sums are fp32 (and bf16) numbers
-//    without a maximum to subtract: no maximum and no rescaling, so a row's
-//    halves need not wait for one another, and sixteen warps, each with half
-//    the columns of 32 rows, take the place of eight.
+//  * A cap bounds the scores, |x| <= cap log2(e) in base 2, and the bias of a
+//    row is largest at its own key or, with a negative slope, at the farthest
+//    one it sees.  Less that bias, up to kBoundedLog2 (a cap of 55) every 2^x
+//    and their sums are fp32 (and bf16) numbers without a maximum to subtract:
+//    no maximum and no rescaling, so a row's halves need not wait for one
+//    another, and sixteen warps, each with half the columns of 32 rows, take
+//    the place of eight.
 //  * The bias -slope |i - j| of a tile wholly in its rows' past or future is a
 //    number of the row plus or minus slope times the column, whose number the
 //    multiply-add has as an immediate operand.  (From a table in shared memory
@@ -121,7 +123,7 @@ __device__ __forceinline__ int snake_task(int k, int b, int G, int n_tasks) {
 // (16 rows) per k-step, its MN extent spanning blocks 16 KB apart (LBO).
 
 // CAP, SLOPES: how scores are changed; BOUNDED: by a cap of at most
-// kBoundedLog2, and no slopes.
+// kBoundedLog2.
 template <bool BOUNDED>
 struct Warps {
   static constexpr int kSoftmax = BOUNDED ? 16 : 8;
@@ -355,6 +357,12 @@ __global__ void __launch_bounds__(Warps<BOUNDED>::kThreads, 1)
       float m = BOUNDED ? 0.f : -INFINITY;  // running max of the base-2 scores
       float l = 0.f;                        // running sum of 2^(x - m)
       if constexpr (BOUNDED) {
+        float slope = 0.f;
+        if constexpr (SLOPES) {
+          slope = __ldg(mp.slopes + tk.h) * 1.4426950408889634f;
+          // the largest bias of the row, whose own key it sees
+          m = slope < 0.f ? -slope * float(max(q - lo_q, hi_q - 1 - q)) : 0.f;
+        }
         for (int j = 0; j < tk.n_kv; ++j) {
           if (!(ok = mbar_wait_warp(bar(kBarSFull + t), (c + j) & 1, ctx, 0x630 + t))) break;
           tc_fence_after();
@@ -366,10 +374,35 @@ __global__ void __launch_bounds__(Warps<BOUNDED>::kThreads, 1)
             uint32_t u[32], pk[16];
             tmem_ld32(tS + 32 * ch, u);
             tmem_wait_ld();
-            auto pair = [&](int e) {
-              return f32x2(__uint_as_float(u[e]), __uint_as_float(u[e + 1]));
+            // Two columns' biases less m.
+            float sl = 0.f, row = 0.f, d0 = 0.f;
+            bool linear = true;
+            if constexpr (SLOPES) {
+              d0 = float(q - kv0 - 32 * ch);
+              const int w0 = q_tile0 + 32 * (warp & 3);  // the warp's first row
+              const bool past = kv0 + 32 * ch + 31 <= w0;
+              linear = past || kv0 + 32 * ch >= w0 + 31;  // one sign for the warp's distances
+              sl = past ? slope : -slope;
+              row = fmaf(-sl, d0, -m);
+            }
+            auto bias = [&](int e, auto edge) {  // distances are whole numbers, exact below 2^24
+              if (!decltype(edge)::value || linear)
+                return f32x2(fmaf(sl, float(e), row), fmaf(sl, float(e + 1), row));
+              return f32x2(fmaf(-slope, fabsf(d0 - float(e)), -m),
+                           fmaf(-slope, fabsf(d0 - float(e + 1)), -m));
             };
-            auto weigh = [&](int e, uint64_t x, auto edge) {
+            auto weigh = [&](int e, auto near, auto edge) {
+              const uint64_t v = f32x2(__uint_as_float(u[e]), __uint_as_float(u[e + 1]));
+              uint64_t x;
+              if constexpr (decltype(near)::value) {
+                x = SLOPES ? fma_f32x2(v, cap_factor(mp, v), bias(e, edge))
+                           : mul_f32x2(v, cap_factor(mp, v));
+              } else {
+                x = fma_f32x2(f32x2(cap_r(mp, __uint_as_float(u[e])),
+                                    cap_r(mp, __uint_as_float(u[e + 1]))),
+                              f32x2(-2.f * mp.cap_log2), f32x2(mp.cap_log2));
+                if constexpr (SLOPES) x = add_f32x2(x, bias(e, edge));
+              }
               float p0, p1;
               f32x2_split(x, p0, p1);
               p0 = ex2(p0);
@@ -385,17 +418,15 @@ __global__ void __launch_bounds__(Warps<BOUNDED>::kThreads, 1)
             auto all = [&](auto edge) {
               if (near_zero<32>(u, mp.poly_limit)) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) weigh(e, cap_poly(mp, pair(e)), edge);
+                for (int e = 0; e < 32; e += 2) weigh(e, std::true_type(), edge);
               } else {
 #pragma unroll
-                for (int e = 0; e < 32; e += 2)
-                  weigh(e, fma_f32x2(f32x2(cap_r(mp, __uint_as_float(u[e])),
-                                           cap_r(mp, __uint_as_float(u[e + 1]))),
-                                     f32x2(-2.f * mp.cap_log2), f32x2(mp.cap_log2)),
-                        edge);
+                for (int e = 0; e < 32; e += 2) weigh(e, std::false_type(), edge);
               }
             };
-            if (kv0 + 32 * ch < all_lo || kv0 + 32 * ch + 32 > all_hi)
+            // (a piece with distances of both signs takes the masked path too,
+            // which is the rare one)
+            if (kv0 + 32 * ch < all_lo || kv0 + 32 * ch + 32 > all_hi || !linear)
               all(std::true_type());
             else
               all(std::false_type());
@@ -602,8 +633,9 @@ static cudaError_t launch_d(const CUtensorMap& tmQ, const CUtensorMap& tmK,
                             const CUtensorMap& tmV, void* O, float* L, const ScoreProblem& p,
                             int* err, cudaStream_t stream) {
   const bool slopes = p.map.slopes;
-  if (p.cap && !slopes && p.map.cap_log2 <= kBoundedLog2)
-    return launch_t<HD, true, false, true>(tmQ, tmK, tmV, O, L, p, err, stream);
+  if (p.cap && p.map.cap_log2 <= kBoundedLog2)
+    return slopes ? launch_t<HD, true, true, true>(tmQ, tmK, tmV, O, L, p, err, stream)
+                  : launch_t<HD, true, false, true>(tmQ, tmK, tmV, O, L, p, err, stream);
   if (p.cap)
     return slopes ? launch_t<HD, true, true, false>(tmQ, tmK, tmV, O, L, p, err, stream)
                   : launch_t<HD, true, false, false>(tmQ, tmK, tmV, O, L, p, err, stream);
