@@ -533,44 +533,44 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
           tmem_ld32(tS, u);
           tmem_wait_ld();
           auto pair = [&](int e) { return f32x2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])); };
-          float slope = 0.f, d0 = 0.f;
-          bool past = true, linear = true;
+          float slope = 0.f, d0 = 0.f, sl = 0.f, row = 0.f;
+          bool linear = true;
           if constexpr (SLOPES) {
             slope = __ldg(mp.slopes + t.hk * p.group + h) * 1.4426950408889634f;
             d0 = float(q0 - key);
             const int w0 = t.jt * 128 + 32 * (warp & 3);  // the warp's first key
-            past = q0 >= w0 + 31;
+            const bool past = q0 >= w0 + 31;
             linear = past || q0 + 31 <= w0;  // one sign for every distance of the warp
-            if (past) slope = -slope;
+            sl = past ? -slope : slope;
+            row = sl * d0;
           }
           // Two columns: x - L, P and P x'.
           auto columns = [&](int e, float l0, float l1, auto by_poly, auto edge) {
             [[maybe_unused]] uint64_t der;
-            uint64_t y;
+            uint64_t y, off = f32x2(-l0, -l1);  // what is added to the score
+            if constexpr (SLOPES) {  // distances are whole numbers, exact below 2^24
+              float a, b;
+              if (!decltype(edge)::value || linear) {
+                f32x2_split(add_f32x2(off, f32x2(row)), a, b);
+                off = f32x2(fmaf(sl, float(e), a), fmaf(sl, float(e + 1), b));
+              } else {
+                off = f32x2(fmaf(-slope, fabsf(d0 + float(e)), -l0),
+                            fmaf(-slope, fabsf(d0 + float(e + 1)), -l1));
+              }
+            }
             if constexpr (!CAP) {
-              y = fma_f32x2(pair(e), f32x2(mp.scale_log2), f32x2(-l0, -l1));
+              y = fma_f32x2(pair(e), f32x2(mp.scale_log2), off);
             } else if constexpr (decltype(by_poly)::value) {
               const uint64_t x = cap_poly(mp, pair(e));
               der = fma_f32x2(mul_f32x2(x, x), f32x2(-mp.inv_cap_log2_sq), f32x2(1.f));
-              y = add_f32x2(x, f32x2(-l0, -l1));
+              y = add_f32x2(x, off);
             } else {
               const uint64_t rr = f32x2(cap_r(mp, __uint_as_float(u[e])),
                                         cap_r(mp, __uint_as_float(u[e + 1])));
               // 1 - tanh^2 = 4 r (1 - r)
               der = mul_f32x2(mul_f32x2(rr, f32x2(4.f)),
                               fma_f32x2(rr, f32x2(-1.f), f32x2(1.f)));
-              y = add_f32x2(fma_f32x2(rr, f32x2(-2.f * mp.cap_log2), f32x2(mp.cap_log2)),
-                            f32x2(-l0, -l1));
-            }
-            if constexpr (SLOPES) {  // distances are whole numbers, exact below 2^24
-              const uint64_t dist = add_f32x2(f32x2(d0), f32x2(float(e), float(e + 1)));
-              if (linear) {
-                y = fma_f32x2(f32x2(slope), dist, y);
-              } else {
-                float a, b;
-                f32x2_split(dist, a, b);
-                y = fma_f32x2(f32x2(-slope), f32x2(fabsf(a), fabsf(b)), y);
-              }
+              y = add_f32x2(fma_f32x2(rr, f32x2(-2.f * mp.cap_log2), f32x2(mp.cap_log2)), off);
             }
             float p0, p1;
             f32x2_split(y, p0, p1);
@@ -601,7 +601,9 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
             else
               all(std::false_type(), edge);
           };
-          if (q0 < all_lo || q0 + 32 > all_lim)
+          // (a piece with distances of both signs takes the masked path too,
+          // which is the rare one)
+          if (q0 < all_lo || q0 + 32 > all_lim || !linear)
             paths(std::true_type());
           else
             paths(std::false_type());
