@@ -2,15 +2,15 @@
 // a row, and the TMA copies of strided rows.
 //
 // The cap.  x = cap tanh(s / cap) for the scaled product s, in base 2.  Near
-// zero, |s / cap| <= 0.65, tanh is an odd polynomial of five terms: two scores
-// to an instruction of the FMA pipe.  Beyond it, tanh(y) = 1 - 2 / (1 + e^2y):
-// an exponential and a reciprocal for each score, absolute error some 2^-23 of
-// the cap.  A warp takes the polynomial for a piece of a tile whose scores all
-// allow it: models that cap their scores at 30 or 50 have most of them well
-// below, and the special function unit is the busier pipe of a softmax
-// (figures in score_fwd.cu).  With a cap far above every score the polynomial
-// is also the exact one, where 1 - 2 / (1 + e^2y) would lose the score in the
-// cap's last bits.
+// zero, |s / cap| <= 0.65 (1.1), tanh is an odd polynomial of five (seven)
+// terms: two scores to an instruction of the FMA pipe.  Beyond it, tanh(y) = 1 -
+// 2 / (1 + e^2y): an exponential and a reciprocal for each score, absolute error
+// some 2^-23 of the cap.  A warp takes the polynomial for a piece of a tile
+// whose scores all allow it: models that cap their scores at 30 or 50 have most
+// of them well below, and the special function unit is the busier pipe of a
+// softmax (figures in score_fwd.cu).  With a cap far above every score the
+// polynomial is also the exact one, where 1 - 2 / (1 + e^2y) would lose the
+// score in the cap's last bits.
 #pragma once
 
 #include "f32x2.cuh"
@@ -39,20 +39,22 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ uint64_t f32x2(float x) { return f32x2(x, x); }
 
 // The polynomial's factor: two capped scores in base 2 are u times it.
-__device__ __forceinline__ uint64_t cap_factor(const ScoreMap& m, uint64_t u) {
+template <int terms>
+__device__ __forceinline__ uint64_t cap_factor(const float (&c)[terms], uint64_t u) {
   const uint64_t z = mul_f32x2(u, u);
-  uint64_t h = f32x2(m.poly[kTanhTerms - 1]);
+  uint64_t h = f32x2(c[terms - 1]);
 #pragma unroll
-  for (int k = kTanhTerms - 2; k >= 0; --k) h = fma_f32x2(h, z, f32x2(m.poly[k]));
+  for (int k = terms - 2; k >= 0; --k) h = fma_f32x2(h, z, f32x2(c[k]));
   return h;
 }
 __device__ __forceinline__ uint64_t cap_poly(const ScoreMap& m, uint64_t u) {
-  return mul_f32x2(u, cap_factor(m, u));
+  return mul_f32x2(u, cap_factor(m.poly, u));
 }
 
-// Whether the polynomial holds for all of the warp's raw products (n each).
+// The largest magnitude among the warp's raw products (n each; the same for
+// all lanes).
 template <int n>
-__device__ __forceinline__ bool near_zero(const uint32_t (&u)[n], float limit) {
+__device__ __forceinline__ float warp_top(const uint32_t (&u)[n]) {
   float a[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) a[e] = fabsf(__uint_as_float(u[e]));
@@ -60,7 +62,13 @@ __device__ __forceinline__ bool near_zero(const uint32_t (&u)[n], float limit) {
   for (int e = 4; e < n; e += 2)
     a[(e >> 1) & 3] = max3f(a[(e >> 1) & 3], fabsf(__uint_as_float(u[e])),
                             fabsf(__uint_as_float(u[e + 1])));
-  return __all_sync(0xffffffffu, max3f(a[0], a[1], fmaxf(a[2], a[3])) <= limit);
+  // magnitudes compare as their bits do
+  return __uint_as_float(__reduce_max_sync(
+      0xffffffffu, __float_as_uint(max3f(a[0], a[1], fmaxf(a[2], a[3])))));
+}
+template <int n>
+__device__ __forceinline__ bool near_zero(const uint32_t (&u)[n], float limit) {
+  return warp_top(u) <= limit;
 }
 
 // 1 / (1 + e^2y) of y = u scale / cap; the capped score is cap_log2 (1 - 2 r).

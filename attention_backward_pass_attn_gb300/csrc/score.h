@@ -22,6 +22,8 @@ struct ScoreMap {
   float scale_log2;   // scale log2(e)
   float poly[kTanhTerms];  // x = u (poly[0] + poly[1] u^2 + ...), for |u| <= poly_limit
   float poly_limit;   // negative: never
+  float far_poly[kTanhFarTerms];  // the same for |u| <= far_limit
+  float far_limit;
   float exp_scale;    // 2 log2(e) scale / cap
   float cap_log2;     // cap log2(e)
   float inv_cap_log2_sq;   // 1 / cap_log2^2: (x / cap_log2)^2 = tanh^2

@@ -16,21 +16,30 @@ bool make_score_map(float scale, float softcap, const float* slopes, ScoreMap* m
   *m = {};
   m->scale_log2 = float(scale * kLog2e);
   m->slopes = slopes;
-  m->poly_limit = -1.f;
+  m->poly_limit = m->far_limit = -1.f;
   if (!std::isfinite(m->scale_log2) || softcap == 0.f) return std::isfinite(m->scale_log2);
   const double c = double(scale) / softcap;
   m->exp_scale = float(2 * kLog2e * c);
   m->cap_log2 = float(softcap * kLog2e);
   m->inv_cap_log2_sq = float(1 / (softcap * kLog2e * softcap * kLog2e));
   if (!std::isfinite(m->exp_scale) || !std::isfinite(2 * m->cap_log2)) return false;
+  const double s = scale * kLog2e;  // x = u s sum_k c_k (c u)^2k
   bool good = std::isfinite(m->inv_cap_log2_sq);
-  double power = scale * kLog2e;  // x = u (scale log2e) sum_k c_k (c u)^2k
-  for (int k = 0; k < kTanhTerms; ++k, power *= c * c) {
-    m->poly[k] = float(tanh_poly(k) * power);
+  for (int k = 0; k < kTanhTerms; ++k) {
+    m->poly[k] = float(tanh_poly(k) * s * std::pow(c, 2 * k));
     good = good && std::isfinite(m->poly[k]);
   }
-  const float limit = float(kTanhReach / c);
-  if (good) m->poly_limit = std::isfinite(limit) ? limit : 3.4e38f;
+  bool far = good;
+  for (int k = 0; k < kTanhFarTerms; ++k) {
+    m->far_poly[k] = float(tanh_far_poly(k) * s * std::pow(c, 2 * k));
+    far = far && std::isfinite(m->far_poly[k]);
+  }
+  const auto limit = [&](double reach) {
+    const float u = float(reach / c);
+    return std::isfinite(u) ? u : 3.4e38f;
+  };
+  if (good) m->poly_limit = limit(kTanhReach);
+  m->far_limit = far ? limit(kTanhFarReach) : m->poly_limit;
   return true;
 }
 

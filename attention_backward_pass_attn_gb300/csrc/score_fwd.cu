@@ -394,9 +394,10 @@ __global__ void __launch_bounds__(Warps<BOUNDED>::kThreads, 1)
             auto weigh = [&](int e, auto near, auto edge) {
               const uint64_t v = f32x2(__uint_as_float(u[e]), __uint_as_float(u[e + 1]));
               uint64_t x;
-              if constexpr (decltype(near)::value) {
-                x = SLOPES ? fma_f32x2(v, cap_factor(mp, v), bias(e, edge))
-                           : mul_f32x2(v, cap_factor(mp, v));
+              if constexpr (decltype(near)::value > 0) {
+                const uint64_t h = decltype(near)::value == 1 ? cap_factor(mp.poly, v)
+                                                              : cap_factor(mp.far_poly, v);
+                x = SLOPES ? fma_f32x2(v, h, bias(e, edge)) : mul_f32x2(v, h);
               } else {
                 x = fma_f32x2(f32x2(cap_r(mp, __uint_as_float(u[e])),
                                     cap_r(mp, __uint_as_float(u[e + 1]))),
@@ -416,12 +417,16 @@ __global__ void __launch_bounds__(Warps<BOUNDED>::kThreads, 1)
               pk[e / 2] = pack_bf16x2(p0, p1);
             };
             auto all = [&](auto edge) {
-              if (near_zero<32>(u, mp.poly_limit)) {
+              const float top = warp_top(u);
+              if (top <= mp.poly_limit) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) weigh(e, std::true_type(), edge);
+                for (int e = 0; e < 32; e += 2) weigh(e, std::integral_constant<int, 1>(), edge);
+              } else if (top <= mp.far_limit) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) weigh(e, std::integral_constant<int, 2>(), edge);
               } else {
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) weigh(e, std::false_type(), edge);
+                for (int e = 0; e < 32; e += 2) weigh(e, std::integral_constant<int, 0>(), edge);
               }
             };
             // (a piece with distances of both signs takes the masked path too,
