@@ -651,9 +651,11 @@ def _score_problem(q, k, v, causal, scale, softcap, slopes, window, doc, prefix)
     keys = (B, Hkv, N, d)
     strides = _check_rows(q, "q", shape, dev) + _check_rows(k, "k", keys, dev) \
         + _check_rows(v, "v", keys, dev)
-    for i, (name, n) in enumerate((x, n) for x in "qkv" for n in (B, Hq if x == "q" else Hkv, N)):
-        if n > 1 and strides[i] < 1:
-            raise ValueError("%s must not be expanded: its strides must be positive" % name)
+    if min(strides) < 1:  # of a dimension of one index they say nothing
+        for i, n in enumerate((B, Hq, N, B, Hkv, N, B, Hkv, N)):
+            if n > 1 and strides[i] < 1:
+                raise ValueError("%s must not be expanded: its strides must be positive"
+                                 % "qkv"[i // 3])
     if slopes is not None:
         _check_like(slopes, "slopes", (Hq,), torch.float32, dev)
     if doc is not None:
