@@ -16,6 +16,7 @@ _BINDING_NAMES = (
     "status_string", "AttnError", "load_library", "ssd_fwd", "ssd_bwd", "ssd_workspace", "ATTN_DQ_AUTO", "ATTN_DQ_REDUCE",
     "ATTN_DQ_SEPARATE", "rope_fwd", "rope_bwd", "alloc_kv_cache", "kv_cache_write", "kv_cache_read",
     "alloc_decode_workspace", "attn_decode", "attn_fwd_score", "attn_bwd_score",
+    "alloc_score_workspace",
 )
 
 

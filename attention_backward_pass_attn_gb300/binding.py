@@ -91,6 +91,7 @@ def load_library(path: str | None = None):
             "int4_cache_read": (i, [vp] * 9 + [i] * 7 + [vp]),
             "attn_score_decode": (i, [vp] * 5 + [i] + [vp] * 4 + [i] * 8 + [f, vp, f, vp, sz, vp]),
             "attn_fwd_score": (i, [vp] * 6 + [i] * 7 + [vp, vp, f, vp, f, vp]),
+            "attn_bwd_score_workspace_size": (sz, [i] * 7),
             "attn_bwd_score": (i, [vp] * 10 + [i] * 7 + [vp, vp, f, vp, f, vp, sz, vp]),
             "attn_last_device_error": (i, [vp]),
             "attn_device_error_word": (i, [vp, ctypes.POINTER(ctypes.c_int)]),
@@ -701,6 +702,15 @@ def attn_fwd_score(q, k, v, causal: bool, scale=None, softcap=0.0, slopes=None, 
     return out, lse
 
 
+def alloc_score_workspace(B: int, Hq: int, Hkv: int, N: int, d: int, device, causal=True,
+                          window=0) -> torch.Tensor:
+    """The uint8 device buffer attn_bwd_score needs; calls that may overlap on
+    the GPU need one each."""
+    n = load_library().attn_bwd_score_workspace_size(B, Hq, Hkv, N, d, int(bool(causal)),
+                                                     max(-1, min(int(window), _INT_MAX)))
+    return torch.empty(max(int(n), 256), dtype=torch.uint8, device=device)
+
+
 def attn_bwd_score(q, k, v, o, do, lse, causal: bool, scale=None, softcap=0.0, slopes=None,
                    window=0, doc=None, prefix=None, dq=None, dk=None, dv=None, workspace=None,
                    stream=None):
@@ -709,8 +719,8 @@ def attn_bwd_score(q, k, v, o, do, lse, causal: bool, scale=None, softcap=0.0, s
     query heads that share a key head.
 
     o, lse: the forward's results; do: the gradient of o; contiguous.
-    workspace: from alloc_workspace(B, Hq, N, d, device); allocated by the call
-    without one.
+    workspace: from alloc_score_workspace for the same sizes, mask flag and
+    window; allocated by the call without one.
     """
     dev, dims, strides, rest = _score_problem(q, k, v, causal, scale, softcap, slopes, window, doc,
                                               prefix)
@@ -727,8 +737,8 @@ def attn_bwd_score(q, k, v, o, do, lse, causal: bool, scale=None, softcap=0.0, s
             _check_like(t, name, shape, torch.bfloat16, dev)
         got.append(t)
     if workspace is None:
-        workspace = _empty((max(attn_bwd_workspace_size(B, Hq, N, d), 256),), torch.uint8, dev,
-                           stream)
+        n = load_library().attn_bwd_score_workspace_size(B, Hq, Hkv, N, d, rest[0], rest[1])
+        workspace = _empty((max(n, 256),), torch.uint8, dev, stream)
     else:
         if not isinstance(workspace, torch.Tensor):
             raise TypeError("workspace must be a torch.Tensor")

@@ -32,6 +32,7 @@ struct ScoreMap {
 
 struct ScoreProblem {
   int B, Hq, Hkv, group;  // group = Hq / Hkv
+  int split;              // backward: items that share a group's heads, a divisor of group
   int N, d;
   int n_tiles, Npad;
   int causal, window;     // window 0: none
@@ -67,8 +68,12 @@ struct ScoreBwdMaps {
   CUtensorMap dout, dk, dv;  // make_tile_map
   CUtensorMap acc;           // make_acc_map
 };
-cudaError_t launch_score_bwd_main(const ScoreBwdMaps& m, const Workspace& ws,
+// sums: with split > 1, fp32 [2][B][Hkv][split][Npad][d], dV's and dK's parts.
+int score_bwd_split(const ScoreProblem& p, int sms);
+cudaError_t launch_score_bwd_main(const ScoreBwdMaps& m, const Workspace& ws, float* sums,
                                   const ScoreProblem& p, float scale, int* err,
                                   cudaStream_t stream);
+cudaError_t launch_score_bwd_join(void* dK, void* dV, const float* sums, const ScoreProblem& p,
+                                  float scale, cudaStream_t stream);
 
 }  // namespace attn

@@ -45,6 +45,8 @@ bool make_score_map(float scale, float softcap, const float* slopes, ScoreMap* m
 
 namespace {
 
+constexpr int kSms = 152;  // what the backward's items are dealt to
+
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool good(const void* p, uintptr_t n) { return p && aligned(p, n); }
 int status_of(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
@@ -82,6 +84,7 @@ int make_problem(int B, int Hq, int Hkv, int N, int d, int causal, int window, c
   p->doc = doc;
   p->prefix = prefix;
   p->cap = softcap > 0.f;
+  p->split = 1;
   return ATTN_OK;
 }
 
@@ -96,6 +99,15 @@ Shape shape_of(const ScoreProblem& p, int H) {
   s.Npad = p.Npad;
   s.H = H;
   return s;
+}
+
+// Where the backward's split sums begin in its workspace, and where they end.
+size_t sums_offset(const ScoreProblem& p) {
+  return (workspace_bytes(shape_of(p, p.Hq)) + 255) & ~size_t(255);
+}
+size_t score_workspace_bytes(const ScoreProblem& p) {
+  const size_t sums = size_t(p.B) * p.Hkv * p.split * p.Npad * p.d * 2 * sizeof(float);
+  return sums_offset(p) + (p.split > 1 ? sums : 0);
 }
 
 // Strides of Q, K and V (batch, head, token): the caller's, or contiguous rows'.
@@ -152,6 +164,17 @@ int attn_fwd_score(const void* Q, const void* K, const void* V, const int64_t* s
   return status_of(launch_score_fwd(mq, mk, mv, O, L, p, err, (cudaStream_t)stream));
 }
 
+size_t attn_bwd_score_workspace_size(int B, int Hq, int Hkv, int N, int d, int causal,
+                                     int window) {
+  ScoreProblem p;
+  bool empty = false;
+  if (make_problem(B, Hq, Hkv, N, d, causal, window, nullptr, nullptr, 0.f, nullptr, 1.f, &p,
+                   &empty) != ATTN_OK || empty)
+    return 0;
+  p.split = score_bwd_split(p, kSms);
+  return score_workspace_bytes(p);
+}
+
 int attn_bwd_score(const void* Q, const void* K, const void* V, const int64_t* strides,
                    const void* O, const void* dO, const float* L, void* dQ, void* dK, void* dV,
                    int B, int Hq, int Hkv, int N, int d, int causal, int window,
@@ -170,7 +193,9 @@ int attn_bwd_score(const void* Q, const void* K, const void* V, const int64_t* s
   RowStrides operands;
   if ((st = set_strides(strides, p, &operands)) != ATTN_OK) return st;
   const Shape rows = shape_of(p, p.Hq), keys = shape_of(p, p.Hkv);
-  if (!good(workspace, 256) || bytes < workspace_bytes(rows)) return ATTN_ERR_WORKSPACE;
+  p.split = score_bwd_split(p, kSms);
+  if (!good(workspace, 256) || bytes < score_workspace_bytes(p)) return ATTN_ERR_WORKSPACE;
+  float* sums = reinterpret_cast<float*>(static_cast<char*>(workspace) + sums_offset(p));
   const Workspace ws = carve_workspace(workspace, rows);
   int* err = error_word_ptr();
   ScoreBwdMaps m;
@@ -182,7 +207,8 @@ int attn_bwd_score(const void* Q, const void* K, const void* V, const int64_t* s
   cudaError_t e = launch_bwd_preprocess(O, dO, L, ws, rows, true, s);
   if (e == cudaSuccess && p.doc) e = launch_score_bwd_tables(ws, p, s);
   if (e == cudaSuccess && p.doc) e = launch_bwd_order(ws, shape_of(p, 1), s);
-  if (e == cudaSuccess) e = launch_score_bwd_main(m, ws, p, scale, err, s);
+  if (e == cudaSuccess) e = launch_score_bwd_main(m, ws, sums, p, scale, err, s);
+  if (e == cudaSuccess && p.split > 1) e = launch_score_bwd_join(dK, dV, sums, p, scale, s);
   if (e == cudaSuccess) e = launch_bwd_dq_convert(dQ, ws, rows, scale, s);
   return status_of(e);
 }

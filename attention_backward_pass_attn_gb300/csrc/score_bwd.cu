@@ -19,7 +19,10 @@
 //
 //  * An item is a tile of a key head and walks the query tiles of every query
 //    head that reads it, one head after another: dK and dV are summed over the
-//    group where they lie, with no further pass and no atomics.
+//    group where they lie, with no further pass and no atomics.  Where that
+//    leaves too few items for the GPU, or one too heavy (score_bwd_split), a
+//    group's heads are dealt to several items, whose fp32 sums a last kernel
+//    adds in the order of the heads.
 //  * Which queries see a key is an interval [q_lo, q_lim) under every mask,
 //    held by the thread that owns the key's row; tiles that cut no row of a
 //    warp skip the test.
@@ -106,38 +109,43 @@ struct Layout {
   static constexpr int kEpiTurns = HD == 128 ? 2 : 1;
 };
 
-// A work item: tile jt of key head hk of batch element b, and the query tiles
-// it0 .. it0 + n_it - 1 of each of the group's heads that see it.
+// A work item: tile jt of key head hk of batch element b, the first of the
+// heads whose query tiles it0 .. it0 + n_it - 1 it walks (group / split of
+// them), and which part of the group they are, counted over all key heads.
 struct Item {
-  int b, hk, jt, it0, n_it;
+  int b, hk, h0, part, jt, it0, n_it;
 };
 
 // Items, heaviest first under the causal mask: tiles by their start (an
 // earlier one is seen by more queries), with documents in the order that
 // attn_bwd_order_kernel sorted them into.  Without the mask all cost the same,
-// and key heads are taken in groups of HG whose query, dO and dQ-accumulator
-// tiles fit in L2 together.
+// and (parts of) key heads are taken in groups of HG whose query, dO and
+// dQ-accumulator tiles fit in L2 together.
 struct ItemMap {
   const ScoreProblem& p;
   const Workspace& ws;
   int HG;
   __device__ __forceinline__ Item item(int i) const {
     Item t;
-    const int heads = p.B * p.Hkv;
+    const int parts = p.Hkv * p.split;  // of a batch element
+    int part;
     if (p.doc) {
-      const int rank = i / p.Hkv, id = __ldg(ws.order + rank);
-      t.hk = i - rank * p.Hkv;
+      const int rank = i / parts, id = __ldg(ws.order + rank);
+      part = i - rank * parts;
       t.b = id / p.n_tiles;
       t.jt = id - t.b * p.n_tiles;
     } else {
       const int per_group = HG * p.n_tiles;
       const int gr = i / per_group, r = i - gr * per_group;
-      const int hg = min(HG, heads - gr * HG);  // heads in this group
+      const int hg = min(HG, p.B * parts - gr * HG);  // parts in this group
       t.jt = r / hg;
-      const int bh = gr * HG + (r - t.jt * hg);
-      t.b = bh / p.Hkv;
-      t.hk = bh - t.b * p.Hkv;
+      part = gr * HG + (r - t.jt * hg);
+      t.b = part / parts;
+      part -= t.b * parts;
     }
+    t.hk = part / p.split;
+    t.h0 = part * (p.group / p.split);
+    t.part = t.b * parts + part;
     int last = p.n_tiles - 1;
     t.it0 = 0;
     if (p.causal) {
@@ -185,8 +193,8 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
                      const __grid_constant__ CUtensorMap tmDK,
                      const __grid_constant__ CUtensorMap tmDV,
                      const __grid_constant__ Workspace ws,
-                     const __grid_constant__ ScoreProblem p, int head_group, float scale,
-                     int* err) {
+                     const __grid_constant__ ScoreProblem p, float* __restrict__ sums,
+                     int head_group, float scale, int* err) {
   using Ly = Layout<HD>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
@@ -197,7 +205,8 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
     return;
   }
 
-  const int n_items = p.B * p.Hkv * p.n_tiles;
+  const int n_items = p.B * p.Hkv * p.split * p.n_tiles;
+  const int group = p.group / p.split;  // query heads of an item
   const ItemMap imap{p, ws, head_group};
   const int G = gridDim.x, cta = blockIdx.x;
 
@@ -268,7 +277,7 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
       int g = 0;
       for (int k = 0, i = snake_item(0, cta, G, n_items); ok && i >= 0; ++k) {
         const Item t = imap.item(i);
-        const int h0 = t.hk * p.group;  // the group's first query head
+        const int h0 = t.h0;
         const int next = snake_item(k + 1, cta, G, n_items);
         const Item nt = next >= 0 ? imap.item(next) : t;
         if (k > 0 && !(ok = mbar_wait_warp(bar(kBarVEmpty), (k - 1) & 1, ctx, 0x712))) break;
@@ -292,7 +301,7 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
           // is often a cold region, and its first tiles are needed right at the
           // item switch.
           if (next >= 0) {
-            const int nh = nt.hk * p.group;
+            const int nh = nt.h0;
 #pragma unroll
             for (int cb = 0; cb < HD / 64; ++cb) {
               tma_prefetch_4d(&tmK, cb * 64, nt.jt * 128, nt.hk, nt.b);
@@ -306,7 +315,7 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
           }
         }
         __syncwarp();
-        for (int h = 0, it = 0; h < p.group; ++g) {
+        for (int h = 0, it = 0; h < group; ++g) {
           const int ds_ = g % Ly::kDOStages, dn = g / Ly::kDOStages;
           if (dn > 0 &&
               !(ok = mbar_wait_warp(bar(kBarDOEmpty + ds_), (dn - 1) & 1, ctx, 0x711)))
@@ -322,10 +331,10 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
           __syncwarp();
           if (++it == t.n_it) it = 0, ++h;
           int qb = t.b, qh = h0 + h, qt = t.it0 + it;
-          if (h == p.group) {
+          if (h == group) {
             if (next < 0) continue;
             qb = nt.b;
-            qh = nt.hk * p.group;
+            qh = nt.h0;
             qt = nt.it0;
           }
           const int gn = g + 1;
@@ -369,7 +378,7 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
       bool ok = true;
       int g = 0;
       for (int k = 0, i = snake_item(0, cta, G, n_items); ok && i >= 0; ++k) {
-        const int total = imap.item(i).n_it * p.group;
+        const int total = imap.item(i).n_it * group;
         if (!(ok = mbar_wait_warp(bar(kBarKFull), k & 1, ctx, 0x720))) break;
         if (!(ok = mbar_wait_warp(bar(kBarQFull + (g & 1)), (g >> 1) & 1, ctx, 0x721))) break;
         tc_fence_after();
@@ -515,7 +524,7 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
       // every key row of the warp is seen by queries [all_lo, all_lim)
       const int all_lo = __reduce_max_sync(0xffffffffu, q_lo);
       const int all_lim = __reduce_min_sync(0xffffffffu, q_lim);
-      for (int h = 0, it = 0; h < p.group; ++g) {
+      for (int h = 0, it = 0; h < group; ++g) {
         const int s = g & 1, q0 = (t.it0 + it) * 128 + 32 * quarter;  // the first column's query
         const bool first = it == 0 && h == 0;
         if (!(ok = mbar_wait_warp(bar(kBarQFull + s), (g >> 1) & 1, ctx, 0x730))) break;
@@ -536,7 +545,7 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
           float slope = 0.f, d0 = 0.f, sl = 0.f, row = 0.f;
           bool linear = true;
           if constexpr (SLOPES) {
-            slope = __ldg(mp.slopes + t.hk * p.group + h) * 1.4426950408889634f;
+            slope = __ldg(mp.slopes + t.h0 + h) * 1.4426950408889634f;
             d0 = float(q0 - key);
             const int w0 = t.jt * 128 + 32 * (warp & 3);  // the warp's first key
             const bool past = q0 >= w0 + 31;
@@ -616,7 +625,7 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
         // dQ reads dS from the shared-memory tile: the previous one must be done,
         // and at an item's first tile so must the previous item's epilogue
         if (g > 0 && !(ok = mbar_wait_warp(bar(kBarDSFree), (g - 1) & 1, ctx, 0x733))) break;
-        if (first && k > 0 &&
+        if (first && k > 0 && p.split == 1 &&
             !(ok = mbar_wait_warp(bar(kBarEpiFree + Ly::kEpiTurns - 1), (k - 1) & 1, ctx, 0x734)))
           break;
         tc_fence_after();
@@ -667,6 +676,26 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
       const int which = quarter >> 1, part = quarter & 1;  // dV or dK; half of its columns
       const uint32_t tAcc =
           tbase + lane_off + (which == 0 ? Ly::kColDV : Ly::kColDK) + (HD / 2) * part;
+      if (p.split > 1) {  // one of several sums: as they are, a thread's columns of its row
+        float4* dst = reinterpret_cast<float4*>(
+            sums + ((size_t(which) * p.B * p.Hkv * p.split + t.part) * p.Npad + t.jt * 128 + r) * HD +
+            (HD / 2) * part);
+#pragma unroll
+        for (int c4 = 0; c4 < HD / 64; ++c4) {
+          uint32_t o[32];
+          tmem_ld32(tAcc + 32 * c4, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            dst[8 * c4 + c] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
+                                          __uint_as_float(o[4 * c + 2]),
+                                          __uint_as_float(o[4 * c + 3]));
+        }
+        tc_fence_before();
+        mbar_arrive(bar(kBarAccEmpty));
+        i = snake_item(k + 1, cta, G, n_items);
+        continue;
+      }
       const float mult = which == 0 ? 1.f : scale;
       for (int turn = 0; ok && turn < Ly::kEpiTurns; ++turn) {
         if (Ly::kEpiTurns == 1 || which == turn) {
@@ -738,8 +767,8 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
     int g = 0;
     for (int k = 0, i = snake_item(0, cta, G, n_items); ok && i >= 0; ++k) {
       const Item t = imap.item(i);
-      for (int h = 0, it = 0; h < p.group; ++g) {
-        const int row0 = (t.b * p.Hq + t.hk * p.group + h) * p.Npad + (t.it0 + it) * 128;
+      for (int h = 0, it = 0; h < group; ++g) {
+        const int row0 = (t.b * p.Hq + t.h0 + h) * p.Npad + (t.it0 + it) * 128;
         // The four drain warps agree before any named barrier below, so that a
         // wait that gave up in one warp stops all of them.
         const bool got = mbar_wait_warp(bar(kBarDQFull), g & 1, ctx, 0x740);
@@ -849,40 +878,72 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Key heads per work-item group without the mask: as many as keep their Q, dO
-// (bf16) and dQ accumulators (fp32), 8 bytes per element of a query head,
-// within 64 MB, half the L2.
+// dK and dV of split groups: the parts' sums, added in their order, rounded to
+// bf16.  Eight values a thread.
+template <int HD>
+__global__ void __launch_bounds__(256)
+    score_bwd_join_kernel(const float* __restrict__ sums, __nv_bfloat16* __restrict__ dK,
+                          __nv_bfloat16* __restrict__ dV, const __grid_constant__ ScoreProblem p,
+                          float scale) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const size_t heads = size_t(p.B) * p.Hkv, units = heads * p.N * (HD / 8);
+  const size_t nthreads = size_t(gridDim.x) * blockDim.x;
+  for (size_t i = size_t(blockIdx.x) * blockDim.x + threadIdx.x; i < 2 * units; i += nthreads) {
+    const int which = i >= units;  // dV, dK
+    const size_t u = which ? i - units : i;
+    const size_t row = u / (HD / 8), head = row / p.N;
+    const int n = int(row - head * p.N), c = int(u % (HD / 8)) * 8;
+    const float* src =
+        sums + ((which * heads * p.split + head * p.split) * p.Npad + n) * HD + c;
+    float a[8] = {};
+    for (int s = 0; s < p.split; ++s, src += size_t(p.Npad) * HD) {
+      const float4 x = __ldcs(reinterpret_cast<const float4*>(src));
+      const float4 y = __ldcs(reinterpret_cast<const float4*>(src + 4));
+      a[0] += x.x, a[1] += x.y, a[2] += x.z, a[3] += x.w;
+      a[4] += y.x, a[5] += y.y, a[6] += y.z, a[7] += y.w;
+    }
+    const float m = which ? scale : 1.f;
+    st_global_v4((which ? dK : dV) + row * HD + c, pack_bf16x2(a[0] * m, a[1] * m),
+                 pack_bf16x2(a[2] * m, a[3] * m), pack_bf16x2(a[4] * m, a[5] * m),
+                 pack_bf16x2(a[6] * m, a[7] * m));
+  }
+}
+
+// Parts of key heads per work-item group without the mask: as many as keep
+// their Q, dO (bf16) and dQ accumulators (fp32), 8 bytes per element of a query
+// head, within 64 MB, half the L2.
 static int heads_per_group(const ScoreProblem& p) {
-  const int heads = p.B * p.Hkv;
+  const int heads = p.B * p.Hkv * p.split;
   if (p.causal) return heads;
-  const size_t per_head = size_t(p.Npad) * p.d * 8 * p.group;
+  const size_t per_head = size_t(p.Npad) * p.d * 8 * (p.group / p.split);
   const size_t hg = (size_t(64) << 20) / per_head;
   return int(hg < 1 ? 1 : hg > size_t(heads) ? heads : hg);
 }
 
 template <int HD, bool CAP, bool SLOPES>
-static cudaError_t launch_t(const ScoreBwdMaps& m, const Workspace& ws, const ScoreProblem& p,
-                            float scale, int* err, cudaStream_t stream) {
+static cudaError_t launch_t(const ScoreBwdMaps& m, const Workspace& ws, float* sums,
+                            const ScoreProblem& p, float scale, int* err, cudaStream_t stream) {
   using Ly = Layout<HD>;
   cudaError_t e = set_smem_limit_once<score_bwd_kernel<HD, CAP, SLOPES>>(Ly::kBytes);
   if (e != cudaSuccess) return e;
   // Persistent grid: at most one CTA per SM, each walking its work items.
-  const long long n_items = (long long)p.n_tiles * p.B * p.Hkv;
+  const long long n_items = (long long)p.n_tiles * p.B * p.Hkv * p.split;
   const int sms = device_sm_count();
   const dim3 grid(unsigned(n_items < sms ? n_items : sms));
   return launch_kernel(score_bwd_kernel<HD, CAP, SLOPES>, grid, dim3(kThreads<HD>), Ly::kBytes, stream,
-                       m.q, m.k, m.v, m.dout, m.acc, m.dk, m.dv, ws, p, heads_per_group(p), scale,
-                       err);
+                       m.q, m.k, m.v, m.dout, m.acc, m.dk, m.dv, ws, p, sums, heads_per_group(p),
+                       scale, err);
 }
 
 template <int HD>
-static cudaError_t launch_d(const ScoreBwdMaps& m, const Workspace& ws, const ScoreProblem& p,
-                            float scale, int* err, cudaStream_t stream) {
+static cudaError_t launch_d(const ScoreBwdMaps& m, const Workspace& ws, float* sums,
+                            const ScoreProblem& p, float scale, int* err, cudaStream_t stream) {
   if (p.cap)
-    return p.map.slopes ? launch_t<HD, true, true>(m, ws, p, scale, err, stream)
-                        : launch_t<HD, true, false>(m, ws, p, scale, err, stream);
-  return p.map.slopes ? launch_t<HD, false, true>(m, ws, p, scale, err, stream)
-                      : launch_t<HD, false, false>(m, ws, p, scale, err, stream);
+    return p.map.slopes ? launch_t<HD, true, true>(m, ws, sums, p, scale, err, stream)
+                        : launch_t<HD, true, false>(m, ws, sums, p, scale, err, stream);
+  return p.map.slopes ? launch_t<HD, false, true>(m, ws, sums, p, scale, err, stream)
+                      : launch_t<HD, false, false>(m, ws, sums, p, scale, err, stream);
 }
 
 }  // namespace score_bwd
@@ -894,11 +955,54 @@ cudaError_t launch_score_bwd_tables(const Workspace& ws, const ScoreProblem& p,
                        dim3(unsigned(blocks < 2432 ? blocks : 2432)), dim3(256), 0, stream, ws, p);
 }
 
-cudaError_t launch_score_bwd_main(const ScoreBwdMaps& m, const Workspace& ws,
+// How many items share a group's heads: the divisor of the group with the
+// shortest estimate, in query tiles that one CTA walks (2.7 us each; 2 us with
+// d = 64).  With the items heaviest first the total spreads evenly over the
+// SMs, but none ends before its heaviest item; without the mask all items are
+// equal and go in whole rounds.  Split sums cost a launch, some 3 tiles, and 5
+// (3) tiles an item for their way to memory.  Measured, one batch element, d =
+// 128, causal, one item a tile and split: 8 query heads on 1 key head, N=4096,
+// 560 and 105 us (8 items); 32 on 4, N=4096, 611 and 359 us (4); 32 on 8, 342
+// and 363 us (2), which this leaves alone.
+int score_bwd_split(const ScoreProblem& p, int sms) {
+  // tiles of the heaviest item for one head, and of all items for all heads
+  const long long n = p.n_tiles, seen = p.window > 0 ? (p.window + 254LL) / 128 + 1 : n;
+  const long long heaviest = seen < n ? seen : n;
+  const long long total = (p.causal ? heaviest * n - heaviest * (heaviest - 1) / 2 : n * n) *
+                          p.B * p.Hq;
+  int best = 1;
+  double least = 0;
+  for (int s = 1; s <= p.group; ++s) {
+    if (p.group % s) continue;
+    const double item = double(heaviest) * (p.group / s);
+    double t = double(total) / sms;
+    if (!p.causal) {  // equal items: whole rounds
+      const long long items = n * p.B * p.Hkv * s;
+      t = double((items + sms - 1) / sms) * item;
+    }
+    if (t < item) t = item;
+    if (s > 1) t += 3 + (p.d == 128 ? 5.0 : 3.0) * n * p.B * p.Hkv * s / sms;
+    if (s == 1 || t < 0.95 * least) best = s, least = t;
+  }
+  return best;
+}
+
+cudaError_t launch_score_bwd_join(void* dK, void* dV, const float* sums, const ScoreProblem& p,
+                                  float scale, cudaStream_t stream) {
+  const size_t blocks = (size_t(p.B) * p.Hkv * p.N * (p.d / 8) * 2 + 255) / 256;
+  const auto k = static_cast<__nv_bfloat16*>(dK);
+  const auto v = static_cast<__nv_bfloat16*>(dV);
+  return launch_kernel(p.d == 64 ? score_bwd::score_bwd_join_kernel<64>
+                                 : score_bwd::score_bwd_join_kernel<128>,
+                       dim3(unsigned(blocks < 2432 ? blocks : 2432)), dim3(256), 0, stream, sums, k,
+                       v, p, scale);
+}
+
+cudaError_t launch_score_bwd_main(const ScoreBwdMaps& m, const Workspace& ws, float* sums,
                                   const ScoreProblem& p, float scale, int* err,
                                   cudaStream_t stream) {
-  return p.d == 64 ? score_bwd::launch_d<64>(m, ws, p, scale, err, stream)
-                   : score_bwd::launch_d<128>(m, ws, p, scale, err, stream);
+  return p.d == 64 ? score_bwd::launch_d<64>(m, ws, sums, p, scale, err, stream)
+                   : score_bwd::launch_d<128>(m, ws, sums, p, scale, err, stream);
 }
 
 }  // namespace attn

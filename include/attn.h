@@ -529,14 +529,20 @@ int attn_score_decode(const void* Q, const void* K_cache, const void* V_cache,
  * The backward takes the forward's inputs, O and L and the gradient dO
  * (contiguous, like O) and writes dQ [B][Hq][N][d] and dK, dV [B][Hkv][N][d],
  * contiguous, the latter two summed over the query heads that share a key
- * head.  The slopes have no gradient.  Workspace:
- * attn_bwd_workspace_size(B, Hq, N, d) bytes, 256-byte aligned.  dK and dV
- * repeat bit for bit; dQ is summed in an order that varies, in fp32, as
- * attn_bwd's is.
+ * head.  The slopes have no gradient.  dK and dV repeat bit for bit; dQ is
+ * summed in an order that varies, in fp32, as attn_bwd's is.  The workspace,
+ * attn_bwd_score_workspace_size bytes for the same sizes, mask flag and window,
+ * 256-byte aligned, contents on entry of no matter, holds what attn_bwd's does
+ * and, where a key head's few tiles would leave part of the GPU idle, the fp32
+ * sums that several blocks form of its dK and dV.
  *
- * Precision: scores, maxima and sums are fp32 (a cap's tanh to 6e-8 of itself
- * where every score of a tile is below 0.8 softcap, else to some 2^-22 of the
- * cap); P and dx meet the tensor core in bf16, each rounded once.  As in
+ * Precision: scores, maxima and sums are fp32 (a cap's tanh to 1.5e-7 of itself
+ * where every score of a tile is below 1.1 softcap, else to some 2^-22 of the
+ * cap); P and dx meet the tensor core in bf16, each rounded once.  Under a cap
+ * of up to 55 the forward weighs without a maximum, from e^-softcap to
+ * e^softcap: values of V above 2^127 e^-softcap / N may overflow (2^41 for a
+ * cap of 50 and N = 16,384), and products of them below 2^-126 count as 0
+ * (values below 2^-54, where all of a row's scores lie at -50).  As in
  * attn_fwd_ex, a value of V (dO, Q, K in the backward) that the mask hides
  * from a row must be finite: its weight is 0, and 0 times infinity is NaN.
  */
@@ -544,6 +550,7 @@ int attn_fwd_score(const void* Q, const void* K, const void* V, const int64_t* s
                    float* L, int B, int Hq, int Hkv, int N, int d, int causal, int window,
                    const int* doc_start, const int* prefix, float softcap, const float* slopes,
                    float scale, void* stream);
+size_t attn_bwd_score_workspace_size(int B, int Hq, int Hkv, int N, int d, int causal, int window);
 int attn_bwd_score(const void* Q, const void* K, const void* V, const int64_t* strides,
                    const void* O, const void* dO, const float* L, void* dQ, void* dK, void* dV,
                    int B, int Hq, int Hkv, int N, int d, int causal, int window,

@@ -29,6 +29,7 @@ def test_declared_and_exported(lib):
               "int4_cache_read"):
         assert ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
     assert callable(pkg.attn_fwd_score) and callable(pkg.attn_bwd_score)
+    assert callable(pkg.alloc_score_workspace)
 
 
 def score_call(lib, kind):
@@ -39,7 +40,8 @@ def score_call(lib, kind):
         if kind == "fwd":
             return lib.attn_fwd_score(q, k, v, st, o, L, B, Hq, Hkv, N, d, causal, window, doc,
                                       prefix, cap, slopes, scale, None)
-        wsb = lib.attn_bwd_workspace_size(B, Hq, N, d) if wsb is None else wsb
+        if wsb is None:
+            wsb = lib.attn_bwd_score_workspace_size(B, Hq, Hkv, N, d, causal, window)
         return lib.attn_bwd_score(q, k, v, st, o, do, L, dq, dk, dv, B, Hq, Hkv, N, d, causal,
                                   window, doc, prefix, cap, slopes, scale, ws, wsb, None)
     return call
@@ -72,7 +74,21 @@ def test_score_validation(lib, kind):
     if kind == "bwd":
         assert call(Hq=0) == INVALID                       # dK and dV of nothing
         assert call(ws=None) == WORKSPACE and call(ws=FAKE + 16) == WORKSPACE
-        assert call(wsb=lib.attn_bwd_workspace_size(1, 4, 130, 64) - 1) == WORKSPACE
+        need = lib.attn_bwd_score_workspace_size(1, 4, 2, 130, 64, 1, 0)
+        assert need >= lib.attn_bwd_workspace_size(1, 4, 130, 64) and call(wsb=need - 1) == WORKSPACE
+
+
+def test_workspace_size(lib):
+    """The plain backward's, and the sums of a key head whose query heads are
+    dealt to several blocks: where there are few key heads, not where many."""
+    size = lib.attn_bwd_score_workspace_size
+    one = 2 * 4096 * 128 * 4  # dK and dV of one part
+    plain = lib.attn_bwd_workspace_size(1, 8, 4096, 128)
+    assert size(1, 8, 8, 4096, 128, 1, 0) == plain
+    assert size(1, 8, 1, 4096, 128, 1, 0) - plain in [s * one for s in (2, 4, 8)]
+    assert size(16, 8, 4, 4096, 128, 0, 0) == lib.attn_bwd_workspace_size(16, 8, 4096, 128)
+    assert size(0, 8, 1, 4096, 128, 1, 0) == 0 and size(1, 8, 3, 4096, 128, 1, 0) == 0
+    assert size(1, 8, 1, 4096, 128, 1, 0) % 256 == 0
 
 
 def cache_call(lib, kind):

@@ -228,3 +228,20 @@ def test_error_word_stays_clear_after_odd_document_maps():
     o, lse = ab.attn_fwd_score(q, k, v, **kw)
     ab.attn_bwd_score(q, k, v, o, do, lse, **kw)
     assert ab.attn_last_device_error() == ab.ATTN_OK
+
+
+@pytest.mark.parametrize("H,Hk,B,mask", [(8, 1, 1, "causal"), (8, 1, 1, "full"), (6, 1, 2, "doc_window"),
+                                         (12, 2, 1, "prefix"), (12, 1, 1, "window")])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_key_heads_sums_in_several_blocks(H, Hk, B, mask, d):
+    """Few key heads: their query heads are dealt to several blocks, whose sums
+    are joined in order, the same bits every time."""
+    N = 401
+    assert ab.load_library().attn_bwd_score_workspace_size(B, H, Hk, N, d, 1, 0) \
+        > ab.attn_bwd_workspace_size(B, H, N, d)
+    p = problem(N, d, H=H, Hk=Hk, B=B, cap=9.0, gain=3.0, slopes=True, seed=4, **MASKS[mask])
+    check(*p)
+    q, k, v, do, kw, cap = p
+    o, lse = ab.attn_fwd_score(q, k, v, softcap=cap, **kw)
+    a, b = (ab.attn_bwd_score(q, k, v, o, do, lse, softcap=cap, **kw) for _ in range(2))
+    assert torch.equal(a[1], b[1]) and torch.equal(a[2], b[2])

@@ -101,7 +101,7 @@ def test_given_outputs_and_workspace():
     got = ab.attn_fwd_score(q, k, v, out=out, lse=l2, **kw)
     assert got[0] is out and got[1] is l2 and torch.equal(out, o) and torch.equal(l2, lse)
     want = ab.attn_bwd_score(q, k, v, o, do, lse, **kw)
-    ws = ab.alloc_workspace(*q.shape, q.device)
+    ws = ab.alloc_score_workspace(1, 4, 2, 200, 64, q.device)
     mine = [torch.full_like(t, float("nan")) for t in (q, k, v)]
     for _ in range(2):  # whatever the workspace held
         got = ab.attn_bwd_score(q, k, v, o, do, lse, dq=mine[0], dk=mine[1], dv=mine[2], workspace=ws, **kw)
