@@ -73,19 +73,23 @@ struct Layout {
   static constexpr uint32_t kColS = 2 * HD;  // + tile * 128
 };
 
-// One task: query tiles qt_a (A) and qt_a + 1 (B, when N reaches it) of query
-// head h of batch element b against key/value tiles kv_lo .. kv_lo + n_kv - 1.
+// One task: query tiles qt_a (A) and qt_a + 1 (B, when N reaches it and a task
+// has two) of query head h of batch element b against key/value tiles kv_lo ..
+// kv_lo + n_kv - 1.
 struct Task {
   int b, h, qt_a, kv_lo, n_kv;
   bool has_b;
 };
 
-// Task i of B * Hq * n_pairs.  Causal: heaviest first (a later pair sees more
-// key/value tiles), heads interleaved, a group's side by side.  Without the
-// mask every task costs the same and tasks run head by head.
+// Query tiles of a task, and tasks of a head.
+constexpr int tasks_of(int n_tiles, int tiles) { return (n_tiles + tiles - 1) / tiles; }
+
+// Task i of B * Hq * tasks_of(n_tiles, tiles).  Causal: heaviest first (a later
+// one sees more key/value tiles), heads interleaved, a group's side by side.
+// Without the mask every task costs the same and tasks run head by head.
 struct TaskMap {
   const ScoreProblem& p;
-  int n_pairs;
+  int tiles, n;  // a task's query tiles; a head's tasks
 
   __device__ __forceinline__ RowMask mask(int b) const {
     return {p.N, p.causal, p.window, p.doc ? p.doc + size_t(b) * p.N : nullptr,
@@ -93,13 +97,13 @@ struct TaskMap {
   }
   __device__ __forceinline__ Task task(int i) const {
     const int BH = p.B * p.Hq;
-    const int bh = p.causal ? i % BH : i / n_pairs;
-    const int pair = p.causal ? n_pairs - 1 - i / BH : i % n_pairs;
+    const int bh = p.causal ? i % BH : i / n;
+    const int x = p.causal ? n - 1 - i / BH : i % n;
     Task t;
     t.b = bh / p.Hq;
     t.h = bh - t.b * p.Hq;
-    t.qt_a = 2 * pair;
-    t.has_b = t.qt_a + 1 < p.n_tiles;
+    t.qt_a = tiles * x;
+    t.has_b = tiles == 2 && t.qt_a + 1 < p.n_tiles;
     // The first row of tile A bounds the first key tile (lower bounds never
     // decrease), the last row of the last tile the last one.
     const RowMask m = mask(t.b);
@@ -138,7 +142,8 @@ __global__ void __launch_bounds__(Warps<BOUNDED>::kThreads, 1)
     score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, __nv_bfloat16* __restrict__ O,
-                     float* __restrict__ Lout, const __grid_constant__ ScoreProblem p, int* err) {
+                     float* __restrict__ Lout, const __grid_constant__ ScoreProblem p, int tiles,
+                     int* err) {
   using Ly = Layout<HD>;
   constexpr int kProducerWarp = Warps<BOUNDED>::kProducer, kMmaWarp = Warps<BOUNDED>::kMma;
   constexpr int kTileThreads = Warps<BOUNDED>::kTileThreads;
@@ -152,10 +157,9 @@ __global__ void __launch_bounds__(Warps<BOUNDED>::kThreads, 1)
   }
 
   const int N = p.N;
-  const int n_pairs = (p.n_tiles + 1) >> 1;
-  const int n_tasks = p.B * p.Hq * n_pairs;
+  const int n_tasks = p.B * p.Hq * tasks_of(p.n_tiles, tiles);
   const int G = int(gridDim.x), cta = int(blockIdx.x);
-  const TaskMap tm{p, n_pairs};
+  const TaskMap tm{p, tiles, tasks_of(p.n_tiles, tiles)};
 
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly::kAbort);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::kTmemSlot);
@@ -627,10 +631,18 @@ static cudaError_t launch_t(const CUtensorMap& tmQ, const CUtensorMap& tmK,
   constexpr int kThreads = Warps<BOUNDED>::kThreads;
   cudaError_t e = set_smem_limit_once<kern>(Ly::kBytes);
   if (e != cudaSuccess) return e;
-  const long long n_tasks = (long long)((p.n_tiles + 1) / 2) * p.B * p.Hq;
+  const long long heads = (long long)p.B * p.Hq;
+  const long long pairs = tasks_of(p.n_tiles, 2) * heads;
+  // One query tile a task where tasks of two would leave SMs idle: a step of one
+  // takes two thirds of the time of two.  Under the mask, where half of a
+  // task's tiles is what the mean has, up to one pair an SM (128 pairs of
+  // N=2048 d=128 with a cap: 38 and 30 us), without it while all single tiles
+  // run at once (64 pairs: 36 and 30 us; 96 pairs: 37 and 56).
+  const int tiles = (p.causal ? pairs : 2 * pairs) <= device_sm_count() ? 1 : 2;
+  const long long n_tasks = tasks_of(p.n_tiles, tiles) * heads;
   const dim3 grid(unsigned(fwd_grid(n_tasks, p.causal)));
   return launch_kernel(kern, grid, dim3(kThreads), Ly::kBytes, stream, tmQ, tmK, tmV,
-                       static_cast<__nv_bfloat16*>(O), L, p, err);
+                       static_cast<__nv_bfloat16*>(O), L, p, tiles, err);
 }
 
 template <int HD>

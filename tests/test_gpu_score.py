@@ -214,10 +214,14 @@ def test_gradients_against_differences():
         assert abs(mine - slope) <= room
 
 
-def test_many_heads_and_a_long_row():
-    """More tasks and items than blocks, several rounds of each block."""
-    q, k, v, do, kw, cap = problem(1100, 64, H=24, Hk=8, B=3, cap=12.0, gain=4.0, window=300)
-    check(q, k, v, do, kw, cap)
+@pytest.mark.parametrize("N,d,more", [
+    (1100, 64, dict(cap=12.0, gain=4.0, window=300)), (390, 128, dict(cap=12.0, gain=4.0, causal=False)),
+    (300, 64, dict(causal=False, slopes=True)), (390, 128, dict(slopes=True, mask="prefix")),
+    (520, 128, dict(cap=100.0, gain=4.0, slopes=True))])
+def test_many_heads(N, d, more):
+    """More tasks and items than blocks, tasks of two query tiles, several
+    rounds of each block."""
+    check(*problem(N, d, H=24, Hk=8, B=3, **more))
 
 
 def test_error_word_stays_clear_after_odd_document_maps():
