@@ -51,10 +51,9 @@ __device__ __forceinline__ uint64_t cap_poly(const ScoreMap& m, uint64_t u) {
   return mul_f32x2(u, cap_factor(m.poly, u));
 }
 
-// The largest magnitude among the warp's raw products (n each; the same for
-// all lanes).
+// The largest magnitude among a thread's n raw products.
 template <int n>
-__device__ __forceinline__ float warp_top(const uint32_t (&u)[n]) {
+__device__ __forceinline__ float top_of(const uint32_t (&u)[n]) {
   float a[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) a[e] = fabsf(__uint_as_float(u[e]));
@@ -62,13 +61,11 @@ __device__ __forceinline__ float warp_top(const uint32_t (&u)[n]) {
   for (int e = 4; e < n; e += 2)
     a[(e >> 1) & 3] = max3f(a[(e >> 1) & 3], fabsf(__uint_as_float(u[e])),
                             fabsf(__uint_as_float(u[e + 1])));
-  // magnitudes compare as their bits do
-  return __uint_as_float(__reduce_max_sync(
-      0xffffffffu, __float_as_uint(max3f(a[0], a[1], fmaxf(a[2], a[3])))));
+  return max3f(a[0], a[1], fmaxf(a[2], a[3]));
 }
-template <int n>
-__device__ __forceinline__ bool near_zero(const uint32_t (&u)[n], float limit) {
-  return warp_top(u) <= limit;
+// Whether a polynomial holds for all of the warp's products.
+__device__ __forceinline__ bool all_within(float top, float limit) {
+  return __all_sync(0xffffffffu, top <= limit);
 }
 
 // 1 / (1 + e^2y) of y = u scale / cap; the capped score is cap_log2 (1 - 2 r).

@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
           };
           auto paths = [&](auto edge) {
             bool poly = true;
-            if constexpr (CAP) poly = near_zero<32>(u, mp.poly_limit);
+            if constexpr (CAP) poly = all_within(top_of(u), mp.poly_limit);
             if (poly)
               all(std::true_type(), edge);
             else

@@ -395,12 +395,13 @@ __global__ void __launch_bounds__(Warps<BOUNDED>::kThreads, 1)
               return f32x2(fmaf(-slope, fabsf(d0 - float(e)), -m),
                            fmaf(-slope, fabsf(d0 - float(e + 1)), -m));
             };
+            float far[kTanhFarTerms];
             auto weigh = [&](int e, auto near, auto edge) {
               const uint64_t v = f32x2(__uint_as_float(u[e]), __uint_as_float(u[e + 1]));
               uint64_t x;
               if constexpr (decltype(near)::value > 0) {
                 const uint64_t h = decltype(near)::value == 1 ? cap_factor(mp.poly, v)
-                                                              : cap_factor(mp.far_poly, v);
+                                                              : cap_factor(far, v);
                 x = SLOPES ? fma_f32x2(v, h, bias(e, edge)) : mul_f32x2(v, h);
               } else {
                 x = fma_f32x2(f32x2(cap_r(mp, __uint_as_float(u[e])),
@@ -421,11 +422,20 @@ __global__ void __launch_bounds__(Warps<BOUNDED>::kThreads, 1)
               pk[e / 2] = pack_bf16x2(p0, p1);
             };
             auto all = [&](auto edge) {
-              const float top = warp_top(u);
-              if (top <= mp.poly_limit) {
+              const float top = top_of(u);
+              if (all_within(top, mp.poly_limit)) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) weigh(e, std::integral_constant<int, 1>(), edge);
-              } else if (top <= mp.far_limit) {
+              } else if (all_within(top, mp.far_limit)) {
+                // Read here and nowhere earlier: held through the loop, these
+                // constants' registers cost the nearer path 5 % (N=16384 h16
+                // d=128: 885 in place of 841 us; 820 without this path, which
+                // takes sharp heads, scores up to the cap, from 1,218 to 1,040).
+#pragma unroll
+                for (int k = 0; k < kTanhFarTerms; ++k) {
+                  far[k] = mp.far_poly[k];
+                  asm volatile("" : "+f"(far[k]));
+                }
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) weigh(e, std::integral_constant<int, 2>(), edge);
               } else {
@@ -485,7 +495,7 @@ __global__ void __launch_bounds__(Warps<BOUNDED>::kThreads, 1)
           };
           const uint64_t sc = f32x2(mp.scale_log2);
           if constexpr (CAP) {
-            if (near_zero<128>(u, mp.poly_limit)) {
+            if (all_within(top_of(u), mp.poly_limit)) {
 #pragma unroll
               for (int e = 0; e < 128; e += 2) put(e, cap_poly(mp, pair(e)));
             } else {
