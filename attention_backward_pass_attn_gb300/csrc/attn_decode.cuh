@@ -44,6 +44,15 @@
 // DRAM 16 to 31 %): eight warps an SM hide less than twelve, and 16 heads of
 // partial output are written, read back and joined where there were 8.
 //
+// A 4-bit cache (int4.cuh) is bound by instructions, not by HBM: the 131,072
+// positions above take 46 us for 151 MB (e4m3: 50 for 277), 420 warp instructions
+// for 16 keys, of which 256 make bf16 numbers of nibbles for the tensor core's
+// 24 (a shift, a mask, an addition and a product a pair); issue slots 56 %, ALU
+// 46 %.  Sixteen warps to an SM were slower (58 us), as they are with bf16.
+//
+// Changed scores (a cap, a bias) cost 1 to 3 % with bf16 and e4m3, 13 % with 4-bit
+// rows.
+//
 // Rounding.  Scores, maxima, sums and outputs are fp32.  The weights p (times
 // V's factor of an e4m3 row) meet V as a sum of two bf16 numbers, 16 bits in
 // all (2^-16), so the result's only rounding that counts is the last one to
@@ -85,22 +94,19 @@ constexpr uint32_t kFp16Span = 31;
 
 // D, the cache's type (CacheType) and the number of 8-head column tiles (1 or
 // 2) fix the rest: KT runs of 16 keys per warp and step, so that a step's K
-// (and its V) is eight 16-byte loads per thread; eight 8-byte ones in a 4-bit
-// cache with D = 64, where eight runs' scores would not fit the registers.
+// (and its V) is eight 16-byte loads per thread.  A 4-bit row takes half the
+// runs that would make: its step, 840 instructions for two runs, is bound by
+// them, and with four the loop no longer fitted the instruction caches (131,072
+// positions, 8 key heads x 4, d=128: 67 us in place of 51).
 template <int D, int TYPE>
 struct Cfg {
   static constexpr int kRow = TYPE == kCacheInt4 ? D / 2 : TYPE == kCacheE4m3 ? D : 2 * D;  // bytes
   static constexpr int KT = TYPE == kCacheInt4 ? 2 : 256 / kRow;  // 1, 2, 2, 4, 2, 2
-  static constexpr int kUnit = kWarps * KT * 16;         // keys of a unit
-  static constexpr int kWords = kRow / 16;               // 32-bit words of K per row and thread,
+  static constexpr int kUnit = kWarps * KT * 16;                  // keys of a unit
+  static constexpr int kWords = kRow / 16;  // 32-bit words of K per row and thread,
   static constexpr int kChunks = kWords < 4 ? 1 : kWords / 4;  // in this many loads
-  static constexpr int kVWords = kRow / 32;              // 32-bit words of V per row and thread
+  static constexpr int kVWords = kRow / 32;  // 32-bit words of V per row and thread
 };
-
-// Blocks of an SM at a time.
-constexpr int resident_blocks(int type, int ng) {
-  return type == kCacheInt4 ? (ng == 1 ? 3 : 2) : ng == 1 ? 3 : 2;
-}
 
 __device__ __forceinline__ void ld_stream(uint32_t (&r)[4], const uint8_t* p) {
   asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -810,7 +816,7 @@ __device__ __forceinline__ void join_parts(const DecodeArgs& a, const Parts& ps,
 }
 
 template <int D, int TYPE, int NG, bool MOD>
-__global__ void __launch_bounds__(kThreads, resident_blocks(TYPE, NG)) decode_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const DecodeArgs a) {
   using C = Cfg<D, TYPE>;
   constexpr int U = C::kUnit;
   constexpr int kHeadStride = D + 8;
@@ -1064,7 +1070,7 @@ __global__ void __launch_bounds__(kThreads, resident_blocks(TYPE, NG)) decode_ke
 template <int D, int TYPE, int NG, bool MOD>
 cudaError_t launch(const DecodeArgs& a, cudaStream_t stream) {
   using C = Cfg<D, TYPE>;
-  constexpr int kPerSm = resident_blocks(TYPE, NG);
+  constexpr int kPerSm = NG == 1 ? 3 : 2;  // resident blocks: see __launch_bounds__
   // at most as many blocks as there can be units
   const int seen = a.window > 0 && a.window < a.c.capacity ? a.window : a.c.capacity;
   const int64_t units = int64_t(a.c.B) * a.head_blocks * (seen / C::kUnit + 2);

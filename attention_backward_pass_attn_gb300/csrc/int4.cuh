@@ -20,7 +20,9 @@ constexpr int kInt4Group = 32;  // values that share a factor
 // 136 off it is c, exactly, in one addition.
 __device__ __forceinline__ uint32_t int4_pair(uint32_t w, int p, uint32_t f) {
   uint32_t x = w >> (4 * p);
-  asm("lop3.b32 %0, %0, %1, %2, 0xEA;" : "+r"(x) : "r"(0x000F000Fu), "r"(0x43004300u));  // a & b | c
+  // a & b | c, said in one instruction: written out in C it took two, a sixth
+  // of the single-token attention's
+  asm("lop3.b32 %0, %0, %1, %2, 0xEA;" : "+r"(x) : "r"(0x000F000Fu), "r"(0x43004300u));
   asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(0xC308C308u));
   return mul_bf16x2(x, f);
 }

@@ -285,8 +285,8 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
           mbar_arrive_expect_tx(bar(kBarVFull), Ly::kTileBytes);
 #pragma unroll
           for (int cb = 0; cb < HD / 64; ++cb)
-            tma_load_4d(sbase + Ly::kV + cb * 16384, &tmV, bar(kBarVFull), cb * 64, t.jt * 128, t.hk,
-                        t.b);
+            tma_load_4d(sbase + Ly::kV + cb * 16384, &tmV, bar(kBarVFull), cb * 64, t.jt * 128,
+                        t.hk, t.b);
         }
         __syncwarp();
         if (k > 0 && !(ok = mbar_wait_warp(bar(kBarKEmpty), (k - 1) & 1, ctx, 0x713))) break;
@@ -294,8 +294,8 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
           mbar_arrive_expect_tx(bar(kBarKFull), Ly::kTileBytes);
 #pragma unroll
           for (int cb = 0; cb < HD / 64; ++cb)
-            tma_load_4d(sbase + Ly::kK + cb * 16384, &tmK, bar(kBarKFull), cb * 64, t.jt * 128, t.hk,
-                        t.b);
+            tma_load_4d(sbase + Ly::kK + cb * 16384, &tmK, bar(kBarKFull), cb * 64, t.jt * 128,
+                        t.hk, t.b);
           if (k == 0) load_q(0, t.b, h0, t.it0);
           // Warm L2 (and the address translation) for the next item: a new head
           // is often a cold region, and its first tiles are needed right at the
@@ -415,8 +415,9 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
           }
           __syncwarp();
           // dV += P^T dO, P^T read from tensor memory: the softmax warps of 32
-          // query columns packed them into the first 16 of their own.  The first dV of an item overwrites the accumulator: the
-          // previous item's epilogue must have read it.
+          // query columns packed them into the first 16 of their own.  The first
+          // dV of an item overwrites the accumulator: the previous item's
+          // epilogue must have read it.
           if (!(ok = mbar_wait_warp(bar(kBarPReady), g & 1, ctx, 0x724))) break;
           if (it == 0 && k > 0 &&
               !(ok = mbar_wait_warp(bar(kBarAccEmpty), (k - 1) & 1, ctx, 0x728)))
@@ -541,7 +542,9 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
           uint32_t u[32], pk[16];
           tmem_ld32(tS, u);
           tmem_wait_ld();
-          auto pair = [&](int e) { return f32x2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])); };
+          auto pair = [&](int e) {
+            return f32x2(__uint_as_float(u[e]), __uint_as_float(u[e + 1]));
+          };
           float slope = 0.f, d0 = 0.f, sl = 0.f, row = 0.f;
           bool linear = true;
           if constexpr (SLOPES) {
@@ -678,7 +681,8 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
           tbase + lane_off + (which == 0 ? Ly::kColDV : Ly::kColDK) + (HD / 2) * part;
       if (p.split > 1) {  // one of several sums: as they are, a thread's columns of its row
         float4* dst = reinterpret_cast<float4*>(
-            sums + ((size_t(which) * p.B * p.Hkv * p.split + t.part) * p.Npad + t.jt * 128 + r) * HD +
+            sums +
+            ((size_t(which) * p.B * p.Hkv * p.split + t.part) * p.Npad + t.jt * 128 + r) * HD +
             (HD / 2) * part);
 #pragma unroll
         for (int c4 = 0; c4 < HD / 64; ++c4) {
@@ -931,8 +935,8 @@ static cudaError_t launch_t(const ScoreBwdMaps& m, const Workspace& ws, float* s
   const long long n_items = (long long)p.n_tiles * p.B * p.Hkv * p.split;
   const int sms = device_sm_count();
   const dim3 grid(unsigned(n_items < sms ? n_items : sms));
-  return launch_kernel(score_bwd_kernel<HD, CAP, SLOPES>, grid, dim3(kThreads<HD>), Ly::kBytes, stream,
-                       m.q, m.k, m.v, m.dout, m.acc, m.dk, m.dv, ws, p, sums, heads_per_group(p),
+  return launch_kernel(score_bwd_kernel<HD, CAP, SLOPES>, grid, dim3(kThreads<HD>), Ly::kBytes,
+                       stream, m.q, m.k, m.v, m.dout, m.acc, m.dk, m.dv, ws, p, sums, heads_per_group(p),
                        scale, err);
 }
 
