@@ -528,7 +528,7 @@ def _check_rows(t: torch.Tensor, name: str, shape, dev: int):
 
 def _is_int4(k_descale) -> bool:
     """Whether a cache's factors say that it holds four bits a value."""
-    return k_descale is not None and k_descale.dtype is torch.bfloat16
+    return isinstance(k_descale, torch.Tensor) and k_descale.dtype is torch.bfloat16
 
 
 def _check_cache(k_cache, v_cache, k_descale, v_descale, page_table, dev):
