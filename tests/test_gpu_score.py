@@ -91,14 +91,14 @@ def check(q, k, v, do, kw, cap, backward=True):
 
 
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("N", [1, 2, 63, 64, 65, 127, 128, 129, 255, 257, 384, 513])
+@pytest.mark.parametrize("N", [1, 2, 63, 64, 65, 127, 128, 129, 255, 256, 257, 384, 513])
 def test_lengths(N, d):
     check(*problem(N, d, gain=4.0, cap=20.0, slopes=True, seed=N))
 
 
 CHANGES = {"none": {}, "cap": dict(cap=15.0, gain=4.0), "slopes": dict(slopes=True),
            "both": dict(cap=15.0, gain=4.0, slopes=True)}
-MASKS = {"full": dict(causal=False), "causal": {}, "window": dict(window=70), "narrow": dict(window=1),
+MASKS = {"full": dict(causal=False), "causal": {}, "window": dict(window=270), "narrow": dict(window=1),
          "doc": dict(mask="doc"), "doc_window": dict(mask="doc", window=33), "prefix": dict(mask="prefix")}
 
 
@@ -114,11 +114,21 @@ def test_shared_key_heads(H, Hk, mask):
     check(*problem(200, 64, H=H, Hk=Hk, B=2, seed=H, cap=10.0, gain=3.0, slopes=True, **MASKS[mask]))
 
 
+@pytest.mark.parametrize("N", [190, 290])  # with the maximum and without
 @pytest.mark.parametrize("cap", [1e-3, 0.05, 1.0, 7.0, 50.0, 1e4, 1e30])
 @pytest.mark.parametrize("gain", [0.02, 1.0, 12.0])
-def test_caps(cap, gain):
+def test_caps(cap, gain, N):
     """Every score above the cap, every score far below it, and both."""
-    check(*problem(190, 128, cap=cap, gain=gain, seed=2))
+    check(*problem(N, 128, cap=cap, gain=gain, seed=2))
+
+
+def test_a_row_that_sees_one_key_returns_its_value():
+    q, k, v, _, kw, _ = problem(300, 64, H=2, Hk=2)
+    for more in (dict(window=1), dict(doc=torch.arange(300, dtype=torch.int32).cuda()[None])):
+        o, _ = ab.attn_fwd_score(q, k, v, softcap=0.0, **dict(kw, **more))
+        assert torch.equal(o, v)
+    o, _ = ab.attn_fwd_score(q, k, v, softcap=30.0, **dict(kw, window=1))
+    assert torch.equal(o, v)
 
 
 def test_a_cap_out_of_reach_changes_little():
