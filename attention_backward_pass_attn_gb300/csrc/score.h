@@ -73,6 +73,9 @@ int score_bwd_split(const ScoreProblem& p, int sms);
 cudaError_t launch_score_bwd_main(const ScoreBwdMaps& m, const Workspace& ws, float* sums,
                                   const ScoreProblem& p, float scale, int* err,
                                   cudaStream_t stream);
+cudaError_t launch_score_bwd_split(const ScoreBwdMaps& m, const Workspace& ws, float* sums,
+                                   const ScoreProblem& p, float scale, int* err,
+                                   cudaStream_t stream);  // the former's, with split > 1
 cudaError_t launch_score_bwd_join(void* dK, void* dV, const float* sums, const ScoreProblem& p,
                                   float scale, cudaStream_t stream);
 
