@@ -862,7 +862,7 @@ inline int heads_per_group(const ScoreProblem& p) {
 
 template <int HD, bool CAP, bool SLOPES, bool SPLIT>
 cudaError_t launch_t(const ScoreBwdMaps& m, const Workspace& ws, float* sums,
-                            const ScoreProblem& p, float scale, int* err, cudaStream_t stream) {
+                     const ScoreProblem& p, float scale, int* err, cudaStream_t stream) {
   using Ly = Layout<HD>;
   cudaError_t e = set_smem_limit_once<score_bwd_kernel<HD, CAP, SLOPES, SPLIT>>(Ly::kBytes);
   if (e != cudaSuccess) return e;
@@ -877,7 +877,7 @@ cudaError_t launch_t(const ScoreBwdMaps& m, const Workspace& ws, float* sums,
 
 template <int HD, bool SPLIT>
 cudaError_t launch_d(const ScoreBwdMaps& m, const Workspace& ws, float* sums,
-                            const ScoreProblem& p, float scale, int* err, cudaStream_t stream) {
+                     const ScoreProblem& p, float scale, int* err, cudaStream_t stream) {
   if (p.cap)
     return p.map.slopes ? launch_t<HD, true, true, SPLIT>(m, ws, sums, p, scale, err, stream)
                         : launch_t<HD, true, false, SPLIT>(m, ws, sums, p, scale, err, stream);
