@@ -17,6 +17,10 @@ namespace attn {
 // The current device's error word (attn_api.cu); null if it has none.
 int* error_word_ptr();
 
+// The backward's dx, and what is summed of it, are 2^14 times themselves
+// (score_bwd.cuh).
+constexpr float kPxUp = 16384.f, kPxDown = 1.f / 16384.f, kPxUpLog2 = 14.f;
+
 // What turns a raw product u = <q, k> into a score in base 2.
 struct ScoreMap {
   float scale_log2;   // scale log2(e)
@@ -26,7 +30,7 @@ struct ScoreMap {
   float far_limit;
   float exp_scale;    // 2 log2(e) scale / cap
   float cap_log2;     // cap log2(e)
-  float inv_cap_log2_sq;   // 1 / cap_log2^2: (x / cap_log2)^2 = tanh^2
+  float der_sq;       // -kPxUp / cap_log2^2: times x^2 it is -kPxUp tanh^2
   const float* slopes;  // [Hq] or null
 };
 

@@ -21,10 +21,10 @@ bool make_score_map(float scale, float softcap, const float* slopes, ScoreMap* m
   const double c = double(scale) / softcap;
   m->exp_scale = float(2 * kLog2e * c);
   m->cap_log2 = float(softcap * kLog2e);
-  m->inv_cap_log2_sq = float(1 / (softcap * kLog2e * softcap * kLog2e));
+  m->der_sq = float(-kPxUp / (softcap * kLog2e * softcap * kLog2e));
   if (!std::isfinite(m->exp_scale) || !std::isfinite(2 * m->cap_log2)) return false;
   const double s = scale * kLog2e;  // x = u s sum_k c_k (c u)^2k
-  bool good = std::isfinite(m->inv_cap_log2_sq);
+  bool good = std::isfinite(m->der_sq);
   for (int k = 0; k < kTanhTerms; ++k) {
     m->poly[k] = float(tanh_poly(k) * s * std::pow(c, 2 * k));
     good = good && std::isfinite(m->poly[k]);
@@ -209,7 +209,7 @@ int attn_bwd_score(const void* Q, const void* K, const void* V, const int64_t* s
   if (e == cudaSuccess && p.doc) e = launch_bwd_order(ws, shape_of(p, 1), s);
   if (e == cudaSuccess) e = launch_score_bwd_main(m, ws, sums, p, scale, err, s);
   if (e == cudaSuccess && p.split > 1) e = launch_score_bwd_join(dK, dV, sums, p, scale, s);
-  if (e == cudaSuccess) e = launch_bwd_dq_convert(dQ, ws, rows, scale, s);
+  if (e == cudaSuccess) e = launch_bwd_dq_convert(dQ, ws, rows, scale * kPxDown, s);
   return status_of(e);
 }
 

@@ -52,7 +52,7 @@ template <int HD>
 __global__ void __launch_bounds__(256)
     score_bwd_join_kernel(const float* __restrict__ sums, __nv_bfloat16* __restrict__ dK,
                           __nv_bfloat16* __restrict__ dV, const __grid_constant__ ScoreProblem p,
-                          float scale) {
+                          float mult_v, float mult_k) {
   grid_dep_wait();
   grid_dep_launch();
   const size_t heads = size_t(p.B) * p.Hkv, units = heads * p.N * (HD / 8);
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(256)
       a[0] += x.x, a[1] += x.y, a[2] += x.z, a[3] += x.w;
       a[4] += y.x, a[5] += y.y, a[6] += y.z, a[7] += y.w;
     }
-    const float m = which ? scale : 1.f;
+    const float m = which ? mult_k : mult_v;
     st_global_v4((which ? dK : dV) + row * HD + c, pack_bf16x2(a[0] * m, a[1] * m),
                  pack_bf16x2(a[2] * m, a[3] * m), pack_bf16x2(a[4] * m, a[5] * m),
                  pack_bf16x2(a[6] * m, a[7] * m));
@@ -127,7 +127,7 @@ cudaError_t launch_score_bwd_join(void* dK, void* dV, const float* sums, const S
   return launch_kernel(p.d == 64 ? score_bwd::score_bwd_join_kernel<64>
                                  : score_bwd::score_bwd_join_kernel<128>,
                        dim3(unsigned(blocks < 2432 ? blocks : 2432)), dim3(256), 0, stream, sums, k,
-                       v, p, scale);
+                       v, p, p.map.slopes && !p.cap ? kPxDown : 1.f, scale * kPxDown);
 }
 
 cudaError_t launch_score_bwd_main(const ScoreBwdMaps& m, const Workspace& ws, float* sums,

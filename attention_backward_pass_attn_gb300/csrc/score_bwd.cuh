@@ -27,8 +27,13 @@
 //  * Which queries see a key is an interval [q_lo, q_lim) under every mask,
 //    held by the thread that owns the key's row; tiles that cut no row of a
 //    warp skip the test.
-//  * dx is formed in fp32 from P x' held in fp16 (11 bits; P <= 1) and rounded
-//    to bf16 once.
+//  * dx is formed in fp32 from P x' held in fp16 and rounded to bf16 once.  P x'
+//    is held times 2^14 (kPxUp), dx, the sums of dQ and dK and all: 11 bits down
+//    to P = 2^-28, and 2^-39 off below, where 2^0 would leave the keys that
+//    every row sees a little of, 2^-20 in a million, four bits.  (N=4096 b4 h16
+//    d=128: 1,162 us became 1,171, with a cap 1,280 and 1,300.)  P is at most 1
+//    and some roundings of the scores more, fp16 ends at 4: what a cap of 10^7
+//    may leave above, whose scores differ by more, stays there.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -175,13 +180,19 @@ __device__ __forceinline__ int snake_item(int k, int b, int G, int n_items) {
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
+  uint32_t w;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  return w;
 }
 __device__ __forceinline__ uint64_t unpack_f16x2(uint32_t w) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
   return f32x2(f.x, f.y);
 }
+
+// Slopes alone: the bias brings the 2^14 along, and P too is held times that (a
+// product for every pair of scores more took N=8192 h16 d=64 from 870 us to 916).
+template <bool CAP, bool SLOPES>
+constexpr bool kUpP = SLOPES && !CAP;
 
 // Descriptor conventions (128-byte swizzle, tiles of 128 rows in 64-column
 // blocks of 16 KB): a K-major operand advances 32 bytes per 16-element k-step
@@ -212,6 +223,7 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
     return;
   }
 
+  constexpr float kUpLog2 = kUpP<CAP, SLOPES> ? kPxUpLog2 : 0.f;
   const int split = SPLIT ? p.split : 1;
   const int n_items = p.B * p.Hkv * split * p.n_tiles;
   const int group = p.group / split;  // query heads of an item
@@ -562,11 +574,11 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
             const bool past = q0 >= w0 + 31;
             linear = past || q0 + 31 <= w0;  // one sign for every distance of the warp
             sl = past ? slope : -slope;
-            row = sl * d0;
+            row = fmaf(sl, d0, -kUpLog2);
           }
           // Two columns: L - x, P and P x'.
           auto columns = [&](int e, float l0, float l1, auto by_poly, auto edge) {
-            [[maybe_unused]] uint64_t der;
+            uint64_t der = f32x2(kPxUp);  // x' times 2^14, where P is not
             // y = L - x of two columns, so that no sign has to be changed: the
             // exponential takes -y for nothing.
             uint64_t y, off = f32x2(l0, l1);
@@ -574,20 +586,20 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
               if (!decltype(edge)::value || linear)
                 off = f32x2(fmaf(sl, float(e), l0 + row), fmaf(sl, float(e + 1), l1 + row));
               else
-                off = f32x2(fmaf(slope, fabsf(d0 + float(e)), l0),
-                            fmaf(slope, fabsf(d0 + float(e + 1)), l1));
+                off = f32x2(fmaf(slope, fabsf(d0 + float(e)), l0 - kUpLog2),
+                            fmaf(slope, fabsf(d0 + float(e + 1)), l1 - kUpLog2));
             }
             if constexpr (!CAP) {
               y = fma_f32x2(pair(e), f32x2(-mp.scale_log2), off);
             } else if constexpr (decltype(by_poly)::value) {
               const uint64_t x = cap_poly(mp, pair(e));
-              der = fma_f32x2(mul_f32x2(x, x), f32x2(-mp.inv_cap_log2_sq), f32x2(1.f));
+              der = fma_f32x2(mul_f32x2(x, x), f32x2(mp.der_sq), f32x2(kPxUp));
               y = fma_f32x2(x, f32x2(-1.f), off);
             } else {
               const uint64_t rr = f32x2(cap_r(mp, __uint_as_float(u[e])),
                                         cap_r(mp, __uint_as_float(u[e + 1])));
               // 1 - tanh^2 = 4 r (1 - r)
-              der = mul_f32x2(mul_f32x2(rr, f32x2(4.f)),
+              der = mul_f32x2(mul_f32x2(rr, f32x2(4.f * kPxUp)),
                               fma_f32x2(rr, f32x2(-1.f), f32x2(1.f)));
               y = fma_f32x2(fma_f32x2(rr, f32x2(-2.f * mp.cap_log2), f32x2(mp.cap_log2)),
                             f32x2(-1.f), off);
@@ -602,7 +614,7 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
               if (q + 1 < q_lo || q + 1 >= q_lim) p1 = 0.f;
             }
             pk[e / 2] = pack_bf16x2(p0, p1);
-            if constexpr (CAP) f32x2_split(mul_f32x2(f32x2(p0, p1), der), p0, p1);
+            if constexpr (!kUpP<CAP, SLOPES>) f32x2_split(mul_f32x2(f32x2(p0, p1), der), p0, p1);
             px[e / 2] = pack_f16x2(p0, p1);
           };
           auto all = [&](auto by_poly, auto edge) {
@@ -706,7 +718,7 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
         tc_fence_before();
         mbar_arrive(bar(kBarAccEmpty));
       } else {
-        const float mult = which == 0 ? 1.f : scale;
+        const float mult = which == 0 ? (kUpP<CAP, SLOPES> ? kPxDown : 1.f) : scale * kPxDown;
         for (int turn = 0; ok && turn < Ly::kEpiTurns; ++turn) {
           if (Ly::kEpiTurns == 1 || which == turn) {
             // The tile's previous contents: this item's dS^T (the contractions

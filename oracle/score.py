@@ -99,8 +99,8 @@ def forward(q, k, v, causal=True, scale=1.0, cap=0.0, slopes=None, window=0, doc
 def backward(q, k, v, o, do, lse, causal=True, scale=1.0, cap=0.0, slopes=None, window=0, doc=None,
              prefix=None):
     """dict of dQ, dK, dV from the given o and lse, and bounds eQ, eK, eV: P
-    and dx each rounded to bf16 once, P x' to fp16 (2^-25 absolute below its
-    range), 1 - tanh^2 off by 2^-20, sums of N (d) terms in fp32."""
+    and dx each rounded to bf16 once, P x' to fp16 (2^-39 absolute below its
+    range, held times 2^14), 1 - tanh^2 off by 2^-20, sums of N (d) terms in fp32."""
     q, k, v, o, do, lse = (_f64(t) for t in (q, k, v, o, do, lse))
     B, H, N, d = q.shape
     g = H // k.shape[1]
@@ -120,7 +120,7 @@ def backward(q, k, v, o, do, lse, causal=True, scale=1.0, cap=0.0, slopes=None, 
         eP = p * (2 * err) * 1.01
         edP = (np.abs(do[b, h]) @ np.abs(v[b, hk]).T
                + np.sum(np.abs(do[b, h] * o[b, h]), axis=-1, keepdims=True)) * (d + 2) * 2.0 ** -23
-        tail = (FP16 + BF16) * np.abs(dx) + np.where(seen, 2.0 ** -25, 0.0) * np.abs(dP - D)
+        tail = (FP16 + BF16) * np.abs(dx) + np.where(seen, 2.0 ** -39, 0.0) * np.abs(dP - D)
         edx = 1.01 * (tail + (eP * der + p * (2.0 ** -20 if cap else 0.0)) * np.abs(dP - D)
                       + p * der * edP)
         sums = N * 2.0 ** -23

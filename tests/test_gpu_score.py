@@ -259,3 +259,14 @@ def test_a_key_heads_sums_in_several_blocks(H, Hk, B, mask, d):
     o, lse = ab.attn_fwd_score(q, k, v, softcap=cap, **kw)
     a, b = (ab.attn_bwd_score(q, k, v, o, do, lse, softcap=cap, **kw) for _ in range(2))
     assert torch.equal(a[1], b[1]) and torch.equal(a[2], b[2])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap,slopes", [(0.0, False), (40.0, False), (0.0, True), (40.0, True)])
+def test_gradients_of_keys_that_every_row_sees_a_little_of(cap, slopes, d):
+    """Keys of weights around 2^-20 to 2^-27: their own dK holds as well as any."""
+    q, k, v, do, kw, _ = problem(300, d, causal=False, slopes=slopes)
+    q[..., 0], k[..., 0] = 8.0, 0.0
+    k[:, :, 100:, 0] = -1.25 * math.sqrt(d)  # e^-10 (capped at 40: e^-9.8) of the others
+    k[:, :, 200:, 0] = -1.75 * math.sqrt(d)  # e^-14 (e^-13.5)
+    check(q, k, v, do, kw, cap)
