@@ -192,3 +192,28 @@ def test_refusals():
         ab.alloc_kv_cache(1, 1, 16, 48, "cuda", "int4")
     with pytest.raises(ValueError, match="int4"):
         ab.alloc_kv_cache(1, 1, 16, 64, "cuda", torch.int8)
+
+
+def test_pages_beyond_32_bits_of_bytes():
+    """The last pages of a cache of 4.4 GB a tensor: the same bits as the same
+    rows in a small one, written, read and attended to."""
+    Hkv, d, page, T = 8, 128, 256, 700
+    P = 2 ** 32 // (Hkv * page * d // 2) + 1000
+    k, v = (make_tensor((1, Hkv, T, d), 61 + i).cuda() for i in range(2))
+    q = make_tensor((1, 4 * Hkv, 1, d), 63).cuda()
+    zero = torch.zeros(1, dtype=torch.int32).cuda()
+    lens = torch.tensor([T], dtype=torch.int32).cuda()
+    big, small = filled(P, Hkv, page, d), filled(3, Hkv, page, d)
+    assert big[0].numel() > 2 ** 32
+    got = []
+    for c, first in ((big, P - 3), (small, 0)):
+        table = (torch.arange(3, dtype=torch.int32)[None] + first).cuda()
+        f = dict(k_descale=c[2], v_descale=c[3])
+        ab.kv_cache_write(k, v, c[0], c[1], table, zero, **f)
+        got.append((*ab.kv_cache_read(c[0], c[1], table, zero, T, **f),
+                    *ab.attn_decode(q, c[0], c[1], table, lens, softcap=30.0, **f),
+                    *ab.attn_decode(q, c[0], c[1], table, lens, **f)))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    for a, b in zip(big, small):
+        assert torch.equal(a[-3:], b)
+        assert bool((a[:-3] == a[0, 0, 0, 0]).all())  # and nothing else was written
