@@ -491,13 +491,14 @@ struct Warp {
     for (int g = 0; g < NG; ++g) s[g][0] = s[g][1] = s[g][2] = s[g][3] = 0.f;
     if constexpr (INT4) {
       const uint32_t f0 = kf[t][0] * 0x00010001u, f1 = kf[t][1] * 0x00010001u;
+      const uint32_t o0 = int4_off(f0), o1 = int4_off(f1);
 #pragma unroll
       for (int w = 0; w < D / 32; ++w) {
         const uint32_t x = kw[2 * t][w], y = kw[2 * t + 1][w];
 #pragma unroll
         for (int p = 0; p < 4; p += 2) {
-          const uint32_t a0 = int4_pair(x, p, f0), a2 = int4_pair(x, p + 1, f0);
-          const uint32_t a1 = int4_pair(y, p, f1), a3 = int4_pair(y, p + 1, f1);
+          const uint32_t a0 = int4_pair(x, p, f0, o0), a2 = int4_pair(x, p + 1, f0, o0);
+          const uint32_t a1 = int4_pair(y, p, f1, o1), a3 = int4_pair(y, p + 1, f1, o1);
 #pragma unroll
           for (int g = 0; g < NG; ++g)
             mma_16x8x16<false>(s[g], a0, a1, a2, a3, qf[g][2 * w + p / 2][0],
@@ -670,10 +671,12 @@ struct Warp {
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
       // INT4: factors of keys 2q, 2q + 1, and of those eight further
-      uint32_t f0 = 0, f1 = 0;
+      uint32_t f0 = 0, f1 = 0, o0 = 0, o1 = 0;
       if constexpr (INT4) {
         f0 = vf[t][0] | uint32_t(vf[t][1]) << 16;
         f1 = vf[t][2] | uint32_t(vf[t][3]) << 16;
+        o0 = int4_off(f0);
+        o1 = int4_off(f1);
       }
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
@@ -682,10 +685,10 @@ struct Warp {
           const uint32_t sel = i & 2 ? 0x7632u : 0x5410u;
           const uint32_t u = __byte_perm(vw[t][0][i / 4], vw[t][1][i / 4], sel);
           const uint32_t v = __byte_perm(vw[t][2][i / 4], vw[t][3][i / 4], sel);
-          a0 = int4_pair(u, 2 * (i & 1), f0);
-          a1 = int4_pair(u, 2 * (i & 1) + 1, f0);
-          a2 = int4_pair(v, 2 * (i & 1), f1);
-          a3 = int4_pair(v, 2 * (i & 1) + 1, f1);
+          a0 = int4_pair(u, 2 * (i & 1), f0, o0);
+          a1 = int4_pair(u, 2 * (i & 1) + 1, f0, o0);
+          a2 = int4_pair(v, 2 * (i & 1), f1, o1);
+          a3 = int4_pair(v, 2 * (i & 1) + 1, f1, o1);
         } else if (FP8) {  // columns 2i, 2i + 1 are bytes of word i / 2
           const uint32_t sel = i & 1 ? 0x7362u : 0x5140u;
           const uint32_t u = __byte_perm(vw[t][0][i / 2], vw[t][1][i / 2], sel);

@@ -27,4 +27,18 @@ __device__ __forceinline__ uint32_t int4_pair(uint32_t w, int p, uint32_t f) {
   return mul_bf16x2(x, f);
 }
 
+// The same in an instruction less, for factors f below 2^123: with the nibble
+// four bits below a bf16 number's leading one, 16 + n, the 24 to take off is a
+// number of two bits, and 24 f still one of bf16's eight: (16 + n) f - 24 f is
+// c f, exactly, in one multiply-add.
+__device__ __forceinline__ uint32_t int4_off(uint32_t f) {  // -24 f
+  return mul_bf16x2(f, 0xC1C0C1C0u);
+}
+__device__ __forceinline__ uint32_t int4_pair(uint32_t w, int p, uint32_t f, uint32_t off) {
+  uint32_t x = p == 0 ? w << 3 : w >> (4 * p - 3);
+  asm("lop3.b32 %0, %0, %1, %2, 0xEA;" : "+r"(x) : "r"(0x00780078u), "r"(0x41804180u));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(x) : "r"(x), "r"(f), "r"(off));
+  return x;
+}
+
 }  // namespace attn
