@@ -45,10 +45,11 @@
 // partial output are written, read back and joined where there were 8.
 //
 // A 4-bit cache (int4.cuh) is bound by instructions, not by HBM: the 131,072
-// positions above take 46 us for 151 MB (e4m3: 50 for 277), 420 warp instructions
-// for 16 keys, of which 256 make bf16 numbers of nibbles for the tensor core's
-// 24 (a shift, a mask, an addition and a product a pair); issue slots 56 %, ALU
-// 46 %.  Sixteen warps to an SM were slower (58 us), as they are with bf16.
+// positions above take 43 us for 151 MB (e4m3: 50 for 277), 345 warp instructions
+// for 16 keys, of which 144 make bf16 numbers of nibbles (a mask and a
+// multiply-add a pair, a shift for four) for the tensor core's 24; issue slots
+// 49 %, ALU 41 %.  (With the pairs of int4_pair, four instructions each, 46 us.)
+// Sixteen warps to an SM were slower (58 us), as they are with bf16.
 //
 // Changed scores (a cap, a bias) cost 1 to 3 % with bf16 and e4m3, 13 % with 4-bit
 // rows.
@@ -95,9 +96,10 @@ constexpr uint32_t kFp16Span = 31;
 // D, the cache's type (CacheType) and the number of 8-head column tiles (1 or
 // 2) fix the rest: KT runs of 16 keys per warp and step, so that a step's K
 // (and its V) is eight 16-byte loads per thread.  A 4-bit row takes half the
-// runs that would make: its step, 840 instructions for two runs, is bound by
-// them, and with four the loop no longer fitted the instruction caches (131,072
-// positions, 8 key heads x 4, d=128: 67 us in place of 51).
+// runs that would make: its step, 690 instructions for two runs, is bound by
+// them, and with four (of 840 for two, then) the loop no longer fitted the
+// instruction caches (131,072 positions, 8 key heads x 4, d=128: 67 us in place
+// of 51).
 template <int D, int TYPE>
 struct Cfg {
   static constexpr int kRow = TYPE == kCacheInt4 ? D / 2 : TYPE == kCacheE4m3 ? D : 2 * D;  // bytes
@@ -245,7 +247,8 @@ struct Warp {
   float kd[FP8 ? KT : 1][2], vd[FP8 ? KT : 1][2];
   // INT4: factors, as bf16, of the thread's group of two K rows and four V rows
   uint16_t kf[INT4 ? KT : 1][2], vf[INT4 ? KT : 1][4];
-  bool wide;  // FP8: q is held in bf16, see kFp16Span
+  bool wide;  // FP8: q is held in bf16, see kFp16Span; INT4: factors of any size
+  uint32_t seen;  // INT4: two largest factors less kInt4LowFactor, wrapped, as bf16 bits
   uint32_t qf[NG][D / 16][2];
   float factor[NG][2];
   float slope[MOD ? NG : 1][2];  // of distance, base 2
@@ -298,9 +301,10 @@ struct Warp {
 
   // The running state's start; q in the products' type, and what turns a
   // product into a score.
-  __device__ __forceinline__ void begin() {
+  __device__ __forceinline__ void begin(bool any_factor) {
     uint32_t top[NG];
-    wide = false;
+    wide = INT4 && any_factor;
+    seen = 0;
     if (FP8) {
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
@@ -335,6 +339,7 @@ struct Warp {
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       float f = a.scale_log2;
+      if (INT4 && !wide) f *= kInt4Up;  // K's values come times 2^-16
       if (FP8) {
         // 2^e puts the largest element into [2^14, 2^15) for fp16, into
         // [2^96, 2^97) where bf16 has to hold the row.
@@ -452,7 +457,8 @@ struct Warp {
   }
 
   // Of a step that is not full: scores of what is not visible become -inf,
-  // V's rows or factors there zero (they may hold anything, NaN included).
+  // V's rows there zero, or their factors 1 (they may hold anything, NaN
+  // included).
   __device__ __forceinline__ void mask(float (&s)[KT][NG][4], int64_t rows, int tile, int lo,
                                        int len) {
 #pragma unroll
@@ -475,7 +481,7 @@ struct Warp {
       for (int j = 0; j < 4; ++j) {
         if (sees(row, tile + 16 * t + 2 * q + (j & 1) + 8 * (j >> 1), lo, len)) continue;
         if constexpr (INT4) {
-          vf[t][j] = 0;
+          vf[t][j] = 0x3F80;  // 1: values of weight 0, finite
           continue;
         }
 #pragma unroll
@@ -490,15 +496,15 @@ struct Warp {
 #pragma unroll
     for (int g = 0; g < NG; ++g) s[g][0] = s[g][1] = s[g][2] = s[g][3] = 0.f;
     if constexpr (INT4) {
-      const uint32_t f0 = kf[t][0] * 0x00010001u, f1 = kf[t][1] * 0x00010001u;
-      const uint32_t o0 = int4_off(f0), o1 = int4_off(f1);
+      const Int4Factor f0 = int4_factor(kf[t][0] * 0x00010001u),
+                       f1 = int4_factor(kf[t][1] * 0x00010001u);
 #pragma unroll
       for (int w = 0; w < D / 32; ++w) {
         const uint32_t x = kw[2 * t][w], y = kw[2 * t + 1][w];
 #pragma unroll
         for (int p = 0; p < 4; p += 2) {
-          const uint32_t a0 = int4_pair(x, p, f0, o0), a2 = int4_pair(x, p + 1, f0, o0);
-          const uint32_t a1 = int4_pair(y, p, f1, o1), a3 = int4_pair(y, p + 1, f1, o1);
+          const uint32_t a0 = int4_value<WIDE>(x, p, f0), a2 = int4_value<WIDE>(x, p + 1, f0);
+          const uint32_t a1 = int4_value<WIDE>(y, p, f1), a3 = int4_value<WIDE>(y, p + 1, f1);
 #pragma unroll
           for (int g = 0; g < NG; ++g)
             mma_16x8x16<false>(s[g], a0, a1, a2, a3, qf[g][2 * w + p / 2][0],
@@ -589,6 +595,7 @@ struct Warp {
 
   // Weight the scores of the step's keys: running maximum and sum, rescaled
   // accumulators, and P^T as two bf16 parts in the tensor core's layout.
+  template <bool WIDE>
   __device__ __forceinline__ void weigh(float (&s)[KT][NG][4], bool full, int64_t rows, int tile,
                                         int lo, int len, uint32_t (&p)[KT][NG][2][2]) {
 #pragma unroll
@@ -635,6 +642,10 @@ struct Warp {
           float w0 = ex2(s[t][g][2 * x] - ref[g][0]), w1 = ex2(s[t][g][2 * x + 1] - ref[g][1]);
           l[g][0] += w0;
           l[g][1] += w1;
+          if (INT4 && !WIDE) {
+            w0 *= kInt4Up;
+            w1 *= kInt4Up;
+          }
           if (FP8) {
             w0 *= vd[t][x];
             w1 *= vd[t][x];
@@ -647,18 +658,42 @@ struct Warp {
       }
   }
 
+  // INT4: the walk with int4_pair_down takes note of every factor, and the run
+  // is walked once more with int4_pair if one of them was outside its range.  (A
+  // choice for every step took 131,072 positions from 41 us to 46: its branches
+  // part the loads from their use.)
+  template <int runs, int n>
+  __device__ __forceinline__ void note(const uint16_t (&f)[runs][n]) {
+#pragma unroll
+    for (int t = 0; t < runs; ++t)
+#pragma unroll
+      for (int j = 0; j < n; j += 2)
+        seen = max_u16x2(seen, add_u16x2(f[t][j] | uint32_t(f[t][j + 1]) << 16,
+                                         (0x10000u - kInt4LowFactor) * 0x00010001u));
+  }
+  __device__ __forceinline__ bool out_of_range() const {
+    return __any_sync(0xffffffffu, max(seen & 0xFFFFu, seen >> 16) >= kInt4Factors);
+  }
+  // One of int4.cuh's two forms of a pair.
+  template <bool WIDE>
+  __device__ __forceinline__ static uint32_t int4_value(uint32_t w, int p, const Int4Factor& f) {
+    return WIDE ? int4_pair(w, p, f.f) : int4_pair_down(w, p, f);
+  }
+
   // One step's keys; MORE: with the loads of the next step's among it.
   template <bool MORE, bool WIDE>
   __device__ __forceinline__ void step(int64_t rows, bool full, int tile, int lo, int len,
                                        int64_t next_rows) {
     float s[KT][NG][4];
+    if constexpr (INT4 && !WIDE) note(kf);
 #pragma unroll
     for (int t = 0; t < KT; ++t) scores<WIDE>(t, s[t]);
     uint32_t p[KT][NG][2][2];
-    weigh(s, full, rows, tile, lo, len, p);
+    weigh<WIDE>(s, full, rows, tile, lo, len, p);
     if (MORE) load_k(next_rows);
     if (!full) mask_v(rows, tile, lo, len);
-    add(p);
+    if constexpr (INT4 && !WIDE) note(vf);
+    add<WIDE>(p);
     if (MORE) load_v(next_rows);
   }
 
@@ -667,16 +702,15 @@ struct Warp {
   __device__ __forceinline__ int column(int i) const {
     return FP8 || INT4 ? (D / 8) * r + 2 * i : (i / 4) * 64 + 8 * r + 2 * (i % 4);
   }
+  template <bool WIDE>
   __device__ __forceinline__ void add(const uint32_t (&p)[KT][NG][2][2]) {
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
       // INT4: factors of keys 2q, 2q + 1, and of those eight further
-      uint32_t f0 = 0, f1 = 0, o0 = 0, o1 = 0;
+      Int4Factor f0, f1;
       if constexpr (INT4) {
-        f0 = vf[t][0] | uint32_t(vf[t][1]) << 16;
-        f1 = vf[t][2] | uint32_t(vf[t][3]) << 16;
-        o0 = int4_off(f0);
-        o1 = int4_off(f1);
+        f0 = int4_factor(vf[t][0] | uint32_t(vf[t][1]) << 16);
+        f1 = int4_factor(vf[t][2] | uint32_t(vf[t][3]) << 16);
       }
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
@@ -685,10 +719,10 @@ struct Warp {
           const uint32_t sel = i & 2 ? 0x7632u : 0x5410u;
           const uint32_t u = __byte_perm(vw[t][0][i / 4], vw[t][1][i / 4], sel);
           const uint32_t v = __byte_perm(vw[t][2][i / 4], vw[t][3][i / 4], sel);
-          a0 = int4_pair(u, 2 * (i & 1), f0, o0);
-          a1 = int4_pair(u, 2 * (i & 1) + 1, f0, o0);
-          a2 = int4_pair(v, 2 * (i & 1), f1, o1);
-          a3 = int4_pair(v, 2 * (i & 1) + 1, f1, o1);
+          a0 = int4_value<WIDE>(u, 2 * (i & 1), f0);
+          a1 = int4_value<WIDE>(u, 2 * (i & 1) + 1, f0);
+          a2 = int4_value<WIDE>(v, 2 * (i & 1), f1);
+          a3 = int4_value<WIDE>(v, 2 * (i & 1) + 1, f1);
         } else if (FP8) {  // columns 2i, 2i + 1 are bytes of word i / 2
           const uint32_t sel = i & 1 ? 0x7362u : 0x5140u;
           const uint32_t u = __byte_perm(vw[t][0][i / 2], vw[t][1][i / 2], sel);
@@ -933,7 +967,8 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
         open_count(a.arrivals + pc.group(blockIdx.x).slot0, a.tag);
         if (!pc.direct()) open_count(a.arrivals2 + pc.slot0, a.tag);
       }
-      wp.begin();
+      // (2^16 times the scale must be finite)
+      wp.begin(a.scale_log2 > 1e33f);
       const int* table = a.c.table + int64_t(w.b) * a.c.max_pages;
       const int kvh = key_head(w.h);
       auto walk = [&](auto wide) {
@@ -953,10 +988,17 @@ __global__ void __launch_bounds__(kThreads, NG == 1 ? 3 : 2) decode_kernel(const
       };
       // The bf16 walk is the branch not expected: laid out the other way, its
       // instructions cost an e4m3 call of 18 us (caches cold) 6 us more, not 2.
-      if (TYPE != kCacheE4m3 || __builtin_expect(!wp.wide, 1))
-        walk(std::false_type());
-      else
-        walk(std::true_type());
+      for (;;) {
+        if (TYPE == kCacheBf16 || __builtin_expect(!wp.wide, 1)) {
+          walk(std::false_type());
+          if (TYPE != kCacheInt4 || __builtin_expect(!wp.out_of_range(), 1)) break;
+          enter(w);
+          wp.begin(true);
+        } else {
+          walk(std::true_type());
+          break;
+        }
+      }
     }
 
     // The run's results leave the registers; the next run's first loads are

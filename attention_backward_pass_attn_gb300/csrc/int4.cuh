@@ -27,18 +27,25 @@ __device__ __forceinline__ uint32_t int4_pair(uint32_t w, int p, uint32_t f) {
   return mul_bf16x2(x, f);
 }
 
-// The same in an instruction less, for factors f below 2^123: with the nibble
-// four bits below a bf16 number's leading one, 16 + n, the 24 to take off is a
-// number of two bits, and 24 f still one of bf16's eight: (16 + n) f - 24 f is
-// c f, exactly, in one multiply-add.
-__device__ __forceinline__ uint32_t int4_off(uint32_t f) {  // -24 f
-  return mul_bf16x2(f, 0xC1C0C1C0u);
+// The same times 2^-16, for factors of [2^-110, 2^11), in a mask and a
+// multiply-add and half a shift.  A nibble in the lowest or next lowest four bits
+// of a bf16 number is, its exponent being 0 or 1, n or 16 n times 2^-133, and with
+// a factor 2^117 or 2^113 times the group's one multiply-add makes (n - 8) f 2^-16
+// of it, exactly: what it adds has at most nine bits.
+constexpr float kInt4Up = 65536.f;
+constexpr uint32_t kInt4Down = 0x37803780u;  // 2^-16, two of it
+struct Int4Factor {
+  uint32_t f;             // two factors
+  uint32_t low, high, off;  // f 2^117, f 2^113, -8 f 2^-16
+};
+__device__ __forceinline__ Int4Factor int4_factor(uint32_t f) {
+  return {f, mul_bf16x2(f, 0x7A007A00u), mul_bf16x2(f, 0x78007800u), mul_bf16x2(f, 0xB900B900u)};
 }
-__device__ __forceinline__ uint32_t int4_pair(uint32_t w, int p, uint32_t f, uint32_t off) {
-  uint32_t x = p == 0 ? w << 3 : w >> (4 * p - 3);
-  asm("lop3.b32 %0, %0, %1, %2, 0xEA;" : "+r"(x) : "r"(0x00780078u), "r"(0x41804180u));
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(x) : "r"(x), "r"(f), "r"(off));
+__device__ __forceinline__ uint32_t int4_pair_down(uint32_t w, int p, const Int4Factor& f) {
+  uint32_t x = (p & 2 ? w >> 8 : w) & (p & 1 ? 0x00F000F0u : 0x000F000Fu);
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(x) : "r"(x), "r"(p & 1 ? f.high : f.low), "r"(f.off));
   return x;
 }
+constexpr uint32_t kInt4LowFactor = 0x0880, kInt4Factors = 0x4500 - 0x0880;  // bf16 bits, count
 
 }  // namespace attn

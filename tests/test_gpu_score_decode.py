@@ -145,6 +145,47 @@ def test_int4_is_the_bf16_cache_of_its_values(d):
     assert float((o.float() - o2.float()).abs().max()) <= 2 ** -8 * float(o2.abs().max()) + 1e-6
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens", [[900, 77], [9000, 1]])
+@pytest.mark.parametrize("e", [-112, -30, 13, 100])
+def test_int4_factors_of_any_size(e, lens, d):
+    """Powers of two at K's factors and off the scale leave every bit; at V's
+    they come out again.  (Around factors of 0.4: those of 2^-110 to 2^11 and
+    the others take different paths.)"""
+    Hkv, group, page = 2, 4, 64
+    c = int4_cache(lens, page, Hkv, d, 11)
+    q = make_tensor((2, Hkv * group, 1, d), 12, std=2.0).cuda()
+    args = (q, c["kc"].cuda(), c["vc"].cuda(), c["table"].cuda(),
+            torch.tensor(lens, dtype=torch.int32).cuda())
+    kd, vd = c["kd"].cuda(), c["vd"].cuda()
+    o, lse = ab.attn_decode(*args, scale=0.125, k_descale=kd, v_descale=vd)
+    o1, lse1 = ab.attn_decode(*args, scale=0.125 * 2.0 ** -e, k_descale=kd * 2.0 ** e, v_descale=vd)
+    assert torch.equal(o, o1) and torch.equal(lse, lse1)
+    o2, lse2 = ab.attn_decode(*args, scale=0.125, k_descale=kd, v_descale=vd * 2.0 ** e)
+    assert torch.equal(lse, lse2)
+    # At V's 2^-112 results below 2^-126 are bf16 numbers of steps of 2^-133, off
+    # by 2^-134, 2^-22 of what they are times 2^112; and terms of weights of 2^-20
+    # and less end at fp32's 2^-149, 2 x 9000 of them 2^-37 each at most, 2^-22
+    # too, which may change a result by a step.
+    step = (o2.double() * 2.0 ** -e - o.double()).abs()
+    assert bool((step <= (2 ** -7 * o.double().abs() + 2 ** -21 if e < -100 else 0)).all())
+    # one row alone outside, and the same in a bf16 cache of the values
+    at = (int(c["table"][0, 40 // page]), 1, 40 % page)
+    kd, vd = kd.clone(), vd.clone()
+    kd[at] *= 2.0 ** min(e, 12)
+    vd[at] *= 2.0 ** min(e, 20)
+    o, lse = ab.attn_decode(*args, scale=2.0 ** -14, k_descale=kd, v_descale=vd)
+    held = torch.from_numpy(rows_held(c["table"], lens, page, c["P"]))[:, None, :, None].cuda()
+    both = []
+    for codes, f in ((args[1], kd), (args[2], vd)):
+        n = torch.stack((codes & 15, codes >> 4), -1).flatten(-2).double() - 8
+        x = n * f.double().repeat_interleave(32, -1)
+        both.append(torch.where(held, x, 0.0).to(torch.bfloat16))
+    o2, lse2 = ab.attn_decode(q, *both, *args[3:], scale=2.0 ** -14)
+    assert float((lse - lse2).abs().max()) <= 2e-5
+    assert float((o.float() - o2.float()).abs().max()) <= 2 ** -8 * float(o2.abs().max()) + 1e-6
+
+
 def test_special_values_in_an_int4_cache():
     """A NaN factor at a visible position shows where it counts, and only there."""
     lens, Hkv, d, page = [100], 2, 64, 16
