@@ -33,9 +33,9 @@ __device__ __forceinline__ uint32_t int4_pair(uint32_t w, int p, uint32_t f) {
 // a factor 2^117 or 2^113 times the group's one multiply-add makes (n - 8) f 2^-16
 // of it, exactly: what it adds has at most nine bits.
 constexpr float kInt4Up = 65536.f;
-constexpr uint32_t kInt4Down = 0x37803780u;  // 2^-16, two of it
+constexpr uint32_t kInt4LowFactor = 0x0880, kInt4Factors = 0x4500 - 0x0880;  // bf16 bits, count
 struct Int4Factor {
-  uint32_t f;             // two factors
+  uint32_t f;               // two factors, bf16
   uint32_t low, high, off;  // f 2^117, f 2^113, -8 f 2^-16
 };
 __device__ __forceinline__ Int4Factor int4_factor(uint32_t f) {
@@ -46,6 +46,5 @@ __device__ __forceinline__ uint32_t int4_pair_down(uint32_t w, int p, const Int4
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(x) : "r"(x), "r"(p & 1 ? f.high : f.low), "r"(f.off));
   return x;
 }
-constexpr uint32_t kInt4LowFactor = 0x0880, kInt4Factors = 0x4500 - 0x0880;  // bf16 bits, count
 
 }  // namespace attn
