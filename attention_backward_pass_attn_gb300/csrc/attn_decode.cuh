@@ -282,20 +282,20 @@ struct Warp {
           qf[g][2 * w + 1][0] = __byte_perm(x.y, x.w, 0x5410);
           qf[g][2 * w + 1][1] = __byte_perm(x.y, x.w, 0x7632);
         }
-        continue;
+      } else {
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c)
+#pragma unroll
+          for (int x = 0; x < (FP8 ? 2 : 1); ++x) {
+            const uint4 w =
+                live ? __ldg(src + (4 * c + q) * (FP8 ? 2 : 1) + x) : make_uint4(0, 0, 0, 0);
+            const int step = FP8 ? 4 * c + 2 * x : 2 * c;
+            qf[g][step][0] = w.x;
+            qf[g][step][1] = w.y;
+            qf[g][step + 1][0] = w.z;
+            qf[g][step + 1][1] = w.w;
+          }
       }
-#pragma unroll
-      for (int c = 0; c < C::kChunks; ++c)
-#pragma unroll
-        for (int x = 0; x < (FP8 ? 2 : 1); ++x) {
-          const uint4 w =
-              live ? __ldg(src + (4 * c + q) * (FP8 ? 2 : 1) + x) : make_uint4(0, 0, 0, 0);
-          const int step = FP8 ? 4 * c + 2 * x : 2 * c;
-          qf[g][step][0] = w.x;
-          qf[g][step][1] = w.y;
-          qf[g][step + 1][0] = w.z;
-          qf[g][step + 1][1] = w.w;
-        }
     }
   }
 
@@ -482,37 +482,39 @@ struct Warp {
         if (sees(row, tile + 16 * t + 2 * q + (j & 1) + 8 * (j >> 1), lo, len)) continue;
         if constexpr (INT4) {
           vf[t][j] = 0x3F80;  // 1: values of weight 0, finite
-          continue;
-        }
+        } else {
 #pragma unroll
-        for (int i = 0; i < C::kVWords; ++i) vw[t][j][i] = 0;
+          for (int i = 0; i < C::kVWords; ++i) vw[t][j][i] = 0;
+        }
       }
     }
   }
 
   // S^T of one run of 16 keys.
   template <bool WIDE>
+  __device__ __forceinline__ void scores_int4(int t, float (&s)[NG][4]) {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) s[g][0] = s[g][1] = s[g][2] = s[g][3] = 0.f;
+    const Int4Factor f0 = int4_factor(kf[t][0] * 0x00010001u),
+                     f1 = int4_factor(kf[t][1] * 0x00010001u);
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) {
+      const uint32_t x = kw[2 * t][w], y = kw[2 * t + 1][w];
+#pragma unroll
+      for (int p = 0; p < 4; p += 2) {
+        const uint32_t a0 = int4_value<WIDE>(x, p, f0), a2 = int4_value<WIDE>(x, p + 1, f0);
+        const uint32_t a1 = int4_value<WIDE>(y, p, f1), a3 = int4_value<WIDE>(y, p + 1, f1);
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+          mma_16x8x16<false>(s[g], a0, a1, a2, a3, qf[g][2 * w + p / 2][0],
+                             qf[g][2 * w + p / 2][1]);
+      }
+    }
+  }
+  template <bool WIDE>
   __device__ __forceinline__ void scores(int t, float (&s)[NG][4]) {
 #pragma unroll
     for (int g = 0; g < NG; ++g) s[g][0] = s[g][1] = s[g][2] = s[g][3] = 0.f;
-    if constexpr (INT4) {
-      const Int4Factor f0 = int4_factor(kf[t][0] * 0x00010001u),
-                       f1 = int4_factor(kf[t][1] * 0x00010001u);
-#pragma unroll
-      for (int w = 0; w < D / 32; ++w) {
-        const uint32_t x = kw[2 * t][w], y = kw[2 * t + 1][w];
-#pragma unroll
-        for (int p = 0; p < 4; p += 2) {
-          const uint32_t a0 = int4_value<WIDE>(x, p, f0), a2 = int4_value<WIDE>(x, p + 1, f0);
-          const uint32_t a1 = int4_value<WIDE>(y, p, f1), a3 = int4_value<WIDE>(y, p + 1, f1);
-#pragma unroll
-          for (int g = 0; g < NG; ++g)
-            mma_16x8x16<false>(s[g], a0, a1, a2, a3, qf[g][2 * w + p / 2][0],
-                               qf[g][2 * w + p / 2][1]);
-        }
-      }
-      return;
-    }
 #pragma unroll
     for (int c = 0; c < C::kChunks; ++c) {
       const uint32_t(&x)[4] = kw[(2 * t) * C::kChunks + c];
@@ -687,7 +689,12 @@ struct Warp {
     float s[KT][NG][4];
     if constexpr (INT4 && !WIDE) note(kf);
 #pragma unroll
-    for (int t = 0; t < KT; ++t) scores<WIDE>(t, s[t]);
+    for (int t = 0; t < KT; ++t) {
+      if constexpr (INT4)
+        scores_int4<WIDE>(t, s[t]);
+      else
+        scores<WIDE>(t, s[t]);
+    }
     uint32_t p[KT][NG][2][2];
     weigh<WIDE>(s, full, rows, tile, lo, len, p);
     if (MORE) load_k(next_rows);
