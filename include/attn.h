@@ -539,8 +539,9 @@ int attn_score_decode(const void* Q, const void* K_cache, const void* V_cache,
  * Precision: scores, maxima and sums are fp32 (a cap's tanh to 1.5e-7 of itself
  * where every score of a tile is below 1.1 softcap, else to some 2^-22 of the
  * cap); P and dx meet the tensor core in bf16, each rounded once, dx from a P
- * that is off by 2^-39 where it is below 2^-28.  The sums of dQ and dK are held
- * 2^14 times themselves: they end at 2^113.  Under a cap of up to 55, from 256
+ * that is off by 2^-39 where it is below 2^-28.  The sums of dQ and dK (with
+ * slopes and no cap dV's too) are held 2^14 times themselves: they end at 2^113.
+ * Under a cap of up to 55, from 256
  * keys on, the forward weighs without a maximum, from e^-softcap to
  * e^softcap: values of V above 2^127 e^-softcap / N may overflow (2^41 for a
  * cap of 50 and N = 16,384), and products of them below 2^-126 count as 0
