@@ -459,12 +459,15 @@ __global__ void __launch_bounds__(Warps<BOUNDED>::kThreads, 1)
           tc_fence_before();
           mbar_arrive(bar(kBarPReady + t));
         }
-        // The halves' sums; a wait that gave up in one warp stops the tile's
-        // eight.  (What was read here a task ago was read before that thread
-        // signalled this task's first P.)
-        float* sums = reinterpret_cast<float*>(smem + Ly::kSum) + 256 * t + r;
-        sums[128 * half] = l;
+        // The halves' sums, written behind the wait for O: O is complete once all
+        // threads of the tile have signalled this task's P, and each of them had
+        // read the other half's sum of the task before by then.  (Ahead of that
+        // wait nothing orders the two where a task has one key tile: its S comes
+        // without a signal from the softmax warps.)  A wait that gave up in one
+        // warp stops the tile's eight.
         ok = ok && mbar_wait_warp(bar(kBarOFull + t), no & 1, ctx, 0x638 + t);
+        float* sums = reinterpret_cast<float*>(smem + Ly::kSum) + 256 * t + r;
+        if (ok) sums[128 * half] = l;
         if (!(ok = named_barrier_and(kTileBarrier + t, kTileThreads, ok))) break;
         l += sums[128 * (1 - half)];
       } else {

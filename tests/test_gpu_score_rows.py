@@ -1,0 +1,41 @@
+"""Rows of the forward with changed scores that see little, and blocks that walk
+many short tasks, on the GPU against the fp64 oracle (oracle/score.py)."""
+
+import pytest
+import torch
+
+from attention_backward_pass_attn_gb300 import binding as ab
+from oracle import score as so
+from test_gpu_score import cuda_ready, host, problem, within  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def starts_of_tiles(B, N):
+    """Documents of one 128-row tile each."""
+    return (torch.arange(N, dtype=torch.int32) // 128 * 128).expand(B, N).contiguous().cuda()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,H,N,documents", [
+    (4, 16, 512, False),  # tasks of one query tile, the last blocks' of one key tile
+    (4, 16, 512, True),   # every task of one key tile
+    (4, 64, 384, True)])  # tasks of two query tiles, and of one at the end, of one key tile
+@pytest.mark.parametrize("slopes", [False, True])
+def test_tasks_of_one_key_tile_behind_others(B, H, N, documents, slopes, d):
+    """A block's tasks follow one another through shared memory, in which the
+    halves of a row exchange their sums: a task with one key tile must not be
+    ahead of what the one before it still reads."""
+    q, k, v, _, kw, cap = problem(N, d, B=B, H=H, Hk=H // 4, cap=50.0, gain=3.0, slopes=slopes,
+                                  seed=B + d)
+    if documents:
+        kw["doc"] = starts_of_tiles(B, N)
+    o, lse = ab.attn_fwd_score(q, k, v, softcap=cap, **kw)
+    f = so.forward(q, k, v, cap=cap, **host(kw))
+    within(o, f["O"], f["dO"], "O")
+    within(lse, f["L"], f["dL"], "L")
+    off = torch.zeros((), dtype=torch.bool, device="cuda")
+    for _ in range(300):
+        o2, lse2 = ab.attn_fwd_score(q, k, v, softcap=cap, **kw)
+        off |= (o2 != o).any() | (lse2 != lse).any()
+    assert not off
