@@ -593,7 +593,13 @@ __global__ void __launch_bounds__(Warps<BOUNDED>::kThreads, 1)
       c += tk.n_kv;
       ++no;
       tc_fence_after();
-      const float inv_l = 1.f / l;
+      // Without a maximum a row that sees one key weighs it by its 2^x, which met V
+      // rounded to bf16: divided by that, O is v, and D then <do, v>, as the
+      // gradient of such a row, zero, needs it.  (For rows of more keys the sum of
+      // the rounded weights is no better a divisor: it moves O by 2^-8 of sum p |v
+      // - o| where l moves it by as much of sum p |v|.)
+      const float inv_l =
+          1.f / (BOUNDED && hi_q - lo_q == 1 ? bf16lo_to_f32(pack_bf16x2(l, 0.f)) : l);
       const size_t row = (size_t(tk.b) * p.Hq + tk.h) * N + q;
       constexpr int kCols = BOUNDED ? HD / 2 : HD;  // of this thread
       __nv_bfloat16* orow = O + row * HD + kCols * half;
@@ -664,10 +670,9 @@ static cudaError_t launch_d(const CUtensorMap& tmQ, const CUtensorMap& tmK,
                             const CUtensorMap& tmV, void* O, float* L, const ScoreProblem& p,
                             int* err, cudaStream_t stream) {
   const bool slopes = p.map.slopes;
-  // Rows that see few keys keep the maximum: its weight is 1, exactly, where
-  // 2^x rounded to bf16 is off by up to 2^-9 of itself, the whole error of a row
-  // that sees one key.  (Dividing by the sum of the rounded weights would mend
-  // that for all rows, and took N=16384 h16 d=128 from 841 to 997 us.)
+  // Calls whose rows all see few keys keep the maximum: its weight is 1,
+  // exactly, where 2^x rounded to bf16 is off by up to 2^-8 of itself, which many
+  // keys average out.
   const int seen = p.window > 0 ? p.window : p.N;
   if (p.cap && p.map.cap_log2 <= kBoundedLog2 && seen >= kBoundedKeys)
     return slopes ? launch_t<HD, true, true, true>(tmQ, tmK, tmV, O, L, p, err, stream)

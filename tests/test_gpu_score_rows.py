@@ -39,3 +39,39 @@ def test_tasks_of_one_key_tile_behind_others(B, H, N, documents, slopes, d):
         o2, lse2 = ab.attn_fwd_score(q, k, v, softcap=cap, **kw)
         off |= (o2 != o).any() | (lse2 != lse).any()
     assert not off
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap", [5.0, 30.0, 50.0])
+@pytest.mark.parametrize("slopes", [False, True])
+def test_a_row_that_sees_one_key_returns_its_value_under_a_cap(cap, slopes, d):
+    """Its weight is 1 whatever its score, also among rows that see more: the
+    first of a causal sequence, and of every document."""
+    N = 600
+    q, k, v, _, kw, _ = problem(N, d, H=3, Hk=3, gain=3.0, slopes=slopes, seed=d)
+    starts = torch.tensor([0, 1, 2, 31, 32, 40, 127, 128, 300, 301, 599], dtype=torch.int32)
+    doc = torch.zeros(N, dtype=torch.int32)
+    for s in starts.tolist():
+        doc[s:] = s
+    at = starts.cuda()
+    for more, rows in ((dict(), at[:1]), (dict(doc=doc.cuda()[None]), at),
+                       (dict(doc=doc.cuda()[None], window=260), at),
+                       (dict(doc=torch.arange(N, dtype=torch.int32).cuda()[None]), slice(None))):
+        o, _ = ab.attn_fwd_score(q, k, v, softcap=cap, **dict(kw, **more))
+        assert torch.equal(o[:, :, rows], v[:, :, rows])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap", [30.0, 50.0])
+def test_rows_of_one_key_have_no_gradient(cap, d):
+    """A row with one key weighs it by 1 whatever its score: with o = v exactly,
+    dP - D is fp32 rounding, and dQ and dK are no more than the bounds around
+    zero (oracle/score.py)."""
+    N = 300
+    q, k, v, do, kw, _ = problem(N, d, H=2, Hk=2, seed=d)
+    kw["doc"] = torch.arange(N, dtype=torch.int32).cuda()[None]
+    o, lse = ab.attn_fwd_score(q, k, v, softcap=cap, **kw)
+    dq, dk, dv = ab.attn_bwd_score(q, k, v, o, do, lse, softcap=cap, **kw)
+    b = so.backward(q, k, v, v, do, lse, cap=cap, **host(kw))
+    for t, n in ((dq, "Q"), (dk, "K"), (dv, "V")):
+        within(t, b["d" + n], b["e" + n], "d" + n)
