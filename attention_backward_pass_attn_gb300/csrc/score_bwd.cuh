@@ -596,11 +596,17 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
               der = fma_f32x2(mul_f32x2(x, x), f32x2(mp.der_sq), f32x2(kPxUp));
               y = fma_f32x2(x, f32x2(-1.f), off);
             } else {
-              const uint64_t rr = f32x2(cap_r(mp, __uint_as_float(u[e])),
-                                        cap_r(mp, __uint_as_float(u[e + 1])));
-              // 1 - tanh^2 = 4 r (1 - r)
-              der = mul_f32x2(mul_f32x2(rr, f32x2(4.f * kPxUp)),
-                              fma_f32x2(rr, f32x2(-1.f), f32x2(1.f)));
+              // e^2y and r = 1 / (1 + e^2y): 1 - tanh^2 = 4 r (r e^2y), a product of
+              // numbers with all their digits on either side (1 - r has none far
+              // below zero).  The limit keeps r e^2y from infinity times zero.
+              const auto e2y = [&](float w) {
+                float z;
+                asm("min.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(w * mp.exp_scale), "f"(126.f));
+                return ex2(z);
+              };
+              const float e0 = e2y(__uint_as_float(u[e])), e1 = e2y(__uint_as_float(u[e + 1]));
+              const uint64_t rr = f32x2(rcp_approx(1.f + e0), rcp_approx(1.f + e1));
+              der = mul_f32x2(mul_f32x2(rr, f32x2(4.f * kPxUp)), mul_f32x2(rr, f32x2(e0, e1)));
               y = fma_f32x2(fma_f32x2(rr, f32x2(-2.f * mp.cap_log2), f32x2(mp.cap_log2)),
                             f32x2(-1.f), off);
             }
