@@ -473,6 +473,17 @@ struct Warp {
       }
     }
   }
+  // INT4: what is not visible has factors of 1 in K too, before they are noted:
+  // an unwritten row's, zero or NaN, would have the run walked a second time.
+  __device__ __forceinline__ void mask_k(int64_t rows, int tile, int lo, int len) {
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      const int64_t row = __shfl_sync(0xffffffffu, rows, t);
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (!sees(row, tile + 16 * t + 8 * x + r, lo, len)) kf[t][x] = 0x3F80;
+    }
+  }
   __device__ __forceinline__ void mask_v(int64_t rows, int tile, int lo, int len) {
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
@@ -687,7 +698,10 @@ struct Warp {
   __device__ __forceinline__ void step(int64_t rows, bool full, int tile, int lo, int len,
                                        int64_t next_rows) {
     float s[KT][NG][4];
-    if constexpr (INT4 && !WIDE) note(kf);
+    if constexpr (INT4 && !WIDE) {
+      if (!full) mask_k(rows, tile, lo, len);
+      note(kf);
+    }
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
       if constexpr (INT4)
