@@ -75,3 +75,24 @@ def test_rows_of_one_key_have_no_gradient(cap, d):
     b = so.backward(q, k, v, v, do, lse, cap=cap, **host(kw))
     for t, n in ((dq, "Q"), (dk, "K"), (dv, "V")):
         within(t, b["d" + n], b["e" + n], "d" + n)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("cap", [0.0, 30.0, 100.0])
+@pytest.mark.parametrize("slopes", [False, True])
+@pytest.mark.parametrize("N", [200, 400])
+def test_keys_that_no_row_sees_may_hold_anything(N, slopes, cap, bad):
+    """Keys behind a row, before its document or outside its window leave its
+    bits as they were, in forward form with the maximum and without."""
+    q, k, v, _, kw, _ = problem(N, 64, gain=3.0, slopes=slopes, seed=N)
+    doc = torch.zeros(N, dtype=torch.int32)
+    doc[N // 2:] = N // 2
+    for more, hidden, rows in ((dict(), slice(N - 7, N), slice(0, N - 7)),
+                               (dict(doc=doc.cuda()[None]), slice(0, N // 2), slice(N // 2, N)),
+                               (dict(window=70), slice(0, 20), slice(100, N))):
+        want = ab.attn_fwd_score(q, k, v, softcap=cap, **dict(kw, **more))
+        odd = k.clone()
+        odd[:, :, hidden] = bad
+        got = ab.attn_fwd_score(q, odd, v, softcap=cap, **dict(kw, **more))
+        for a, b in zip(got, want):
+            assert torch.equal(a[:, :, rows], b[:, :, rows])
