@@ -22,10 +22,10 @@
 //
 // A written row is read once (2 d bytes) and written once (d / 2 and d / 16 of
 // factors); reading back is the reverse.  Reading is at a copy's speed (32,768
-// rows of 16 heads, 20,480 of them held, d=128: 48 us, 6.6 TB/s); writing issues
-// in 60 % of all slots and reaches 5.2 TB/s (a padded batch of 4 x 8,192 tokens
-// of 16 heads: 40 us).
-#include "f32x2.cuh"
+// rows of 16 heads, 20,480 of them held, d=128: 49 us, 6.5 TB/s); writing issues
+// in 70 % of all slots and reaches 5.2 TB/s (a padded batch of 4 x 8,192 tokens
+// of 16 heads: 42 us).
+#include "f32x2_arith.cuh"
 #include "int4.cuh"
 #include "kv_rows.cuh"
 

@@ -2,10 +2,10 @@
 // a row, and the TMA copies of strided rows.
 //
 // The cap.  x = cap tanh(s / cap) for the scaled product s, in base 2.  Near
-// zero, |s / cap| <= 0.65 (1.1), tanh is an odd polynomial of five (seven)
-// terms: two scores to an instruction of the FMA pipe.  Beyond it, tanh(y) = 1 -
-// 2 / (1 + e^2y): an exponential and a reciprocal for each score, absolute error
-// some 2^-23 of the cap.  A warp takes the polynomial for a piece of a tile
+// zero, |s / cap| <= 0.65 (1.1 in the forward without a maximum), tanh is an odd
+// polynomial of five (seven) terms: two scores to an instruction of the FMA pipe.
+// Beyond it, tanh(y) = 1 - 2 / (1 + e^2y): an exponential and a reciprocal for
+// each score, absolute error some 2^-23 of the cap.  A warp takes the polynomial for a piece of a tile
 // whose scores all allow it: models that cap their scores at 30 or 50 have most
 // of them well below, and the special function unit is the busier pipe of a
 // softmax (figures in score_fwd.cu).  With a cap far above every score the
@@ -13,7 +13,7 @@
 // score in the cap's last bits.
 #pragma once
 
-#include "f32x2.cuh"
+#include "f32x2_arith.cuh"
 #include "mask.cuh"
 #include "ptx.cuh"
 #include "score.h"
