@@ -51,8 +51,8 @@
 // 49 %, ALU 41 %.  (With the pairs of int4_pair, four instructions each, 46 us.)
 // Sixteen warps to an SM were slower (58 us), as they are with bf16.
 //
-// Changed scores (a cap, a bias) cost 1 to 3 % with bf16 and e4m3, 13 % with 4-bit
-// rows.
+// Changed scores (a cap, a bias) cost 1 to 3 % with bf16 and e4m3, 9 to 13 % with
+// 4-bit rows.
 //
 // Rounding.  Scores, maxima, sums and outputs are fp32.  The weights p (times
 // V's factor of an e4m3 row) meet V as a sum of two bf16 numbers, 16 bits in
@@ -671,8 +671,10 @@ struct Warp {
       }
   }
 
-  // INT4: the walk with int4_pair_down takes note of every factor, and the run
-  // is walked once more with int4_pair if one of them was outside its range.  (A
+  // INT4: the walk with int4_pair_down takes note of every visible factor, and the
+  // run is walked once more with int4_pair if one of them was outside its range,
+  // which takes the warp's run twice its time (131,072 positions whose last run
+  // has such a factor: 61 us in place of 43).  (A
   // choice for every step took 131,072 positions from 41 us to 46: its branches
   // part the loads from their use.)
   template <int runs, int n>

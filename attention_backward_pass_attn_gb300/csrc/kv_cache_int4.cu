@@ -24,7 +24,7 @@
 // factors); reading back is the reverse.  Reading is at a copy's speed (32,768
 // rows of 16 heads, 20,480 of them held, d=128: 49 us, 6.5 TB/s); writing issues
 // in 70 % of all slots and reaches 5.2 TB/s (a padded batch of 4 x 8,192 tokens
-// of 16 heads: 42 us).
+// of 16 heads, mean of three sets of lengths: 42 us).
 #include "f32x2_arith.cuh"
 #include "int4.cuh"
 #include "kv_rows.cuh"
@@ -90,7 +90,8 @@ __device__ __forceinline__ uint32_t codes8(const uint4& v, float f, float r) {
 // either row; each of them works out one of the four factors, whose divisions
 // would otherwise be a third of the kernel's instructions.  Six blocks to an SM,
 // at 40 registers a thread: with the 58 that the compiler took unasked a padded
-// batch of 4 x 8,192 tokens, 16 heads, d=128, took 45 us in place of 40.
+// batch of 4 x 8,192 tokens, 16 heads, d=128 (one set of lengths), took 45 us in
+// place of 40.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 6)
     kv_write_int4_kernel(const CacheArgs c, const CacheRows r, unsigned rows, int* err) {

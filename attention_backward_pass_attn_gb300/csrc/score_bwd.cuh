@@ -599,6 +599,8 @@ __global__ void __launch_bounds__(kThreads<HD>, 1)
               // e^2y and r = 1 / (1 + e^2y): 1 - tanh^2 = 4 r (r e^2y), a product of
               // numbers with all their digits on either side (1 - r has none far
               // below zero).  The limit keeps r e^2y from infinity times zero.
+              // (Scores of 12 under a cap of 5, N=8192 h16 d=128: 661 us, where 4 r
+              // (1 - r) took 644.)
               const auto e2y = [&](float w) {
                 float z;
                 asm("min.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(w * mp.exp_scale), "f"(126.f));

@@ -430,8 +430,9 @@ __global__ void __launch_bounds__(Warps<BOUNDED>::kThreads, 1)
               } else if (all_within(top, mp.far_limit)) {
                 // Read here and nowhere earlier: held through the loop, these
                 // constants' registers cost the nearer path 5 % (N=16384 h16
-                // d=128: 885 in place of 841 us; 820 without this path, which
-                // takes sharp heads, scores up to the cap, from 1,218 to 1,040).
+                // d=128, one set of inputs: 885 in place of 841 us; 820 without
+                // this path, which takes sharp heads, scores up to the cap, from
+                // 1,218 to 1,040).
 #pragma unroll
                 for (int k = 0; k < kTanhFarTerms; ++k) {
                   far[k] = mp.far_poly[k];

@@ -537,17 +537,19 @@ int attn_score_decode(const void* Q, const void* K_cache, const void* V_cache,
  * sums that several blocks form of its dK and dV.
  *
  * Precision: scores, maxima and sums are fp32 (a cap's tanh to 1.5e-7 of itself
- * where every score of a tile is below 1.1 softcap, else to some 2^-22 of the
- * cap); P and dx meet the tensor core in bf16, each rounded once, dx from a P
- * that is off by 2^-39 where it is below 2^-28.  The sums of dQ and dK (with
- * slopes and no cap dV's too) are held 2^14 times themselves: they end at 2^113.
- * Under a cap of up to 55, from 256
- * keys on, the forward weighs without a maximum, from e^-softcap to
- * e^softcap: values of V above 2^127 e^-softcap / N may overflow (2^41 for a
- * cap of 50 and N = 16,384), and products of them below 2^-126 count as 0
- * (values below 2^-54, where all of a row's scores lie at -50).  As in
- * attn_fwd_ex, a value of V (dO, Q, K in the backward) that the mask hides
- * from a row must be finite: its weight is 0, and 0 times infinity is NaN.
+ * where every score of a tile is below 0.65 softcap, in a forward without a
+ * maximum below 1.1 softcap; else to some 2^-22 of the cap, and 1 - tanh^2 to
+ * 2^-18 of itself); P and dx meet the tensor core in bf16, each rounded once, dx
+ * from a P that is off by 2^-39 where it is below 2^-28. Weights below 2^-126
+ * count as 0. A row that sees one key returns its value exactly. The sums of dQ
+ * and dK (with slopes and no cap dV's too) are held 2^14 times themselves: they
+ * end at 2^113. Under a cap of up to 55, from 256 keys on (256 in the window, if
+ * there is one), the forward weighs without a maximum, from e^-softcap to
+ * e^softcap: values of V above 2^127 e^-softcap / N may overflow (2^41 for a cap
+ * of 50 and N = 16,384), and products of them below 2^-126 count as 0 (values
+ * below 2^-54, where all of a row's scores lie at -50). As in attn_fwd_ex, a
+ * value of V (dO, Q, K in the backward) that the mask hides from a row must be
+ * finite: its weight is 0, and 0 times infinity is NaN.
  */
 int attn_fwd_score(const void* Q, const void* K, const void* V, const int64_t* strides, void* O,
                    float* L, int B, int Hq, int Hkv, int N, int d, int causal, int window,
